@@ -262,6 +262,51 @@ int64_t dispatch_tail_units(const ep::DispatchArgs& a, int n, int sm_count, cuda
     return ring >= 2 * static_cast<int64_t>(n) * ep::dispatch_warps() ? tail : 0;
 }
 
+// Host checks shared by the experts' products. The tensor copies need 16-byte
+// aligned rows (K % 16) and address columns and weight rows with int32.
+ep_status_t check_expert(const uint8_t* a, const float* a_scale, int64_t num_recv,
+                         const int32_t* offsets, int E, const uint8_t* w, const float* w_scale,
+                         int64_t N, int64_t K, const int32_t* status) {
+    if (num_recv < 0 || E < 1 || K <= 0 || K % 16 != 0) return EP_ERR_INVALID;
+    if (E > EP_MAX_EXPERTS || num_recv > kMaxPairs || K > kMaxPairs - 128 ||
+        N > (kMaxPairs - 256) / E)
+        return EP_ERR_UNSUPPORTED;
+    if (num_recv == 0) return EP_OK;
+    if (a == nullptr || a_scale == nullptr || offsets == nullptr || w == nullptr || w_scale == nullptr)
+        return EP_ERR_INVALID;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
+        !aligned(offsets, 4) || !aligned(status, 4))
+        return EP_ERR_INVALID;
+    return EP_OK;
+}
+
+ep::ExpertArgs expert_args(const uint8_t* a, const float* a_scale, int64_t num_recv,
+                           const int32_t* offsets, int E, const uint8_t* w, const float* w_scale,
+                           int64_t N, int64_t K, int32_t* status) {
+    ep::ExpertArgs x{};
+    x.a = a;
+    x.a_scale = a_scale;
+    x.num_recv = num_recv;
+    x.offsets = offsets;
+    x.E = E;
+    x.w = w;
+    x.w_scale = w_scale;
+    x.n = static_cast<int>(N);
+    x.k = K;
+    x.status = status;
+    return x;
+}
+
+// The products compute rather than move, so the SM budget (which leaves SMs
+// to work like them) does not bound them; an SM partition's stream does.
+ep_status_t run_expert(const ep::ExpertArgs& x, cudaStream_t stream) {
+    int sm_count = 0, smem_optin = 0;
+    if (!device_limits(&sm_count, &smem_optin)) return EP_ERR_CUDA;
+    const int part = ep::partition_sms(stream);
+    const ep::CallBytes call_bytes(x.num_recv * x.k);
+    return from_cuda(ep::launch_expert(x, part > 0 ? part : sm_count, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -516,6 +561,37 @@ ep_status_t ep_combine(const uint16_t* expert_out, int64_t num_recv, const int32
     if (use_combine_tma(K, n))
         return from_cuda(ep::launch_combine_tma(a, n, smem_optin, static_cast<cudaStream_t>(stream)));
     return from_cuda(ep::launch_combine(a, n, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_expert_matmul_fp8(const uint8_t* a, const float* a_scale, int64_t num_recv,
+                                 const int32_t* offsets, int E, const uint8_t* w,
+                                 const float* w_scale, int64_t N, int64_t K, uint16_t* out,
+                                 int32_t* status, void* stream) {
+    ep::ApiRange range("ep_expert_matmul_fp8");
+    if (N <= 0 || N % 8 != 0) return EP_ERR_INVALID;
+    const ep_status_t st = check_expert(a, a_scale, num_recv, offsets, E, w, w_scale, N, K, status);
+    if (st != EP_OK || num_recv == 0) return st;
+    if (out == nullptr || !aligned(out, 16)) return EP_ERR_INVALID;
+    ep::ExpertArgs x = expert_args(a, a_scale, num_recv, offsets, E, w, w_scale, N, K, status);
+    x.out = out;
+    return run_expert(x, static_cast<cudaStream_t>(stream));
+}
+
+ep_status_t ep_expert_gate_up_fp8(const uint8_t* a, const float* a_scale, int64_t num_recv,
+                                  const int32_t* offsets, int E, const uint8_t* w,
+                                  const float* w_scale, int64_t I, int64_t K, uint8_t* out_q,
+                                  float* out_scale, int32_t* status, void* stream) {
+    ep::ApiRange range("ep_expert_gate_up_fp8");
+    if (I <= 0 || I % 128 != 0) return EP_ERR_INVALID;
+    if (I > kMaxPairs / 2) return EP_ERR_UNSUPPORTED;
+    const ep_status_t st = check_expert(a, a_scale, num_recv, offsets, E, w, w_scale, 2 * I, K, status);
+    if (st != EP_OK || num_recv == 0) return st;
+    if (out_q == nullptr || out_scale == nullptr || !aligned(out_q, 16) || !aligned(out_scale, 4))
+        return EP_ERR_INVALID;
+    ep::ExpertArgs x = expert_args(a, a_scale, num_recv, offsets, E, w, w_scale, 2 * I, K, status);
+    x.out_q = out_q;
+    x.out_scale = out_scale;
+    return run_expert(x, static_cast<cudaStream_t>(stream));
 }
 
 ep_status_t ep_get_status(const int32_t* status, void* stream) {

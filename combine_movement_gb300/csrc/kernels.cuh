@@ -196,6 +196,29 @@ bool combine_tma_supported(int K);
 cudaError_t launch_combine_tma(const CombineArgs& a, int num_sms, int smem_optin,
                                cudaStream_t stream);
 
+// ---- expert products --------------------------------------------------------
+
+struct ExpertArgs {
+    const uint8_t* a;          // e4m3 [num_recv][k]
+    const float* a_scale;      // [num_recv][k_blocks]
+    int64_t num_recv;
+    const int32_t* offsets;    // [E + 1]
+    int E;
+    const uint8_t* w;          // e4m3 [E][n][k]
+    const float* w_scale;      // [E][ceil(n / 128)][k_blocks]
+    int n;
+    int64_t k;
+    uint16_t* out;             // bf16 [num_recv][n], or null for the gated form:
+    uint8_t* out_q;            // e4m3 [num_recv][n / 2]
+    float* out_scale;          // [num_recv][n / 256]
+    int32_t* status;
+    // set by launch_expert
+    int k_blocks;
+    int col_tiles;
+};
+
+cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream);
+
 // Launch a kernel of the hot path. With programmatic dependent launch the
 // launch may start while the previous kernel on the stream finishes: its CTAs
 // become resident and wait in griddep_wait(), which every such kernel calls

@@ -31,6 +31,9 @@ EP_ERR_WORKSPACE = 7
 EP_MAX_TOPK = 32
 EP_MAX_EXPERTS = 4096
 
+# Values that share one scale in the 8-bit operands.
+FP8_BLOCK = 128
+
 
 def _header_define(name: str) -> int:
     """Integer value of a #define in include/ep.h (the C ABI's own header),
@@ -106,6 +109,10 @@ def _load() -> ctypes.CDLL:
     lib.ep_combine.restype = i32
     lib.ep_get_dispatch_layout_noalloc.argtypes = [p, i64, i32, i32, p, p, p, p, p]
     lib.ep_get_dispatch_layout_noalloc.restype = i32
+    lib.ep_expert_matmul_fp8.argtypes = [p, p, i64, p, i32, p, p, i64, i64, p, p, p]
+    lib.ep_expert_matmul_fp8.restype = i32
+    lib.ep_expert_gate_up_fp8.argtypes = [p, p, i64, p, i32, p, p, i64, i64, p, p, p, p]
+    lib.ep_expert_gate_up_fp8.restype = i32
     lib.ep_sm_partition.argtypes = [i32, ctypes.POINTER(p), ctypes.POINTER(p),
                                     ctypes.POINTER(i32), ctypes.POINTER(i32)]
     lib.ep_sm_partition.restype = i32
@@ -303,6 +310,54 @@ def ep_combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tenso
     _check(code, "ep_combine")
 
 
+def _shape(t: torch.Tensor, shape: Tuple[int, ...], what: str) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _expert_operands(a, a_scale, offsets, w, w_scale):
+    """Checks the operands of an expert product against each other and
+    returns (num_recv, E, rows of w, K)."""
+    (R, K), (E, N) = a.shape, w.shape[:2]
+    kb = -(-K // FP8_BLOCK)
+    _shape(a_scale, (R, kb), "a_scale")
+    _shape(offsets, (E + 1,), "offsets")
+    _shape(w, (E, N, K), "w")
+    _shape(w_scale, (E, -(-N // FP8_BLOCK), kb), "w_scale")
+    return R, E, N, K
+
+
+def ep_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor,
+                         w: torch.Tensor, w_scale: torch.Tensor, out: torch.Tensor,
+                         status: Optional[torch.Tensor] = None, stream=None) -> None:
+    R, E, N, K = _expert_operands(a, a_scale, offsets, w, w_scale)
+    _shape(out, (R, N), "out")
+    code = lib.ep_expert_matmul_fp8(
+        _ptr(a, torch.float8_e4m3fn, "a"), _ptr(a_scale, torch.float32, "a_scale"), R,
+        _ptr(offsets, torch.int32, "offsets"), E, _ptr(w, torch.float8_e4m3fn, "w"),
+        _ptr(w_scale, torch.float32, "w_scale"), N, K, _ptr(out, torch.bfloat16, "out"),
+        _ptr(status, torch.int32, "status"), _stream(stream))
+    _check(code, "ep_expert_matmul_fp8")
+
+
+def ep_expert_gate_up_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor,
+                          w: torch.Tensor, w_scale: torch.Tensor, out_q: torch.Tensor,
+                          out_scale: torch.Tensor, status: Optional[torch.Tensor] = None,
+                          stream=None) -> None:
+    R, E, N, K = _expert_operands(a, a_scale, offsets, w, w_scale)
+    if N % 2:
+        raise ValueError(f"w: expected a gate half and an up half, got {N} rows")
+    _shape(out_q, (R, N // 2), "out_q")
+    _shape(out_scale, (R, -(-N // 2 // FP8_BLOCK)), "out_scale")
+    code = lib.ep_expert_gate_up_fp8(
+        _ptr(a, torch.float8_e4m3fn, "a"), _ptr(a_scale, torch.float32, "a_scale"), R,
+        _ptr(offsets, torch.int32, "offsets"), E, _ptr(w, torch.float8_e4m3fn, "w"),
+        _ptr(w_scale, torch.float32, "w_scale"), N // 2, K,
+        _ptr(out_q, torch.float8_e4m3fn, "out_q"), _ptr(out_scale, torch.float32, "out_scale"),
+        _ptr(status, torch.int32, "status"), _stream(stream))
+    _check(code, "ep_expert_gate_up_fp8")
+
+
 def ep_sm_partition(num_sms: int) -> Tuple[int, Optional[int], int, int]:
     """(stream, rest_stream, sms, rest_sms) of an SM partition of at least
     num_sms SMs on the current device; the streams are raw cudaStream_t
@@ -360,3 +415,26 @@ def combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tensor,
     y = torch.empty((T, expert_out.shape[1]), dtype=expert_out.dtype, device=expert_out.device)
     ep_combine(expert_out, slot, topk_w, y, status, stream)
     return y
+
+
+def expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor,
+                      w: torch.Tensor, w_scale: torch.Tensor,
+                      status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Each expert's rows times its weights: bf16 [num_recv, N]. Rows no
+    expert has (from offsets[E] on) are left as allocated."""
+    out = torch.empty((a.shape[0], w.shape[1]), dtype=torch.bfloat16, device=a.device)
+    ep_expert_matmul_fp8(a, a_scale, offsets, w, w_scale, out, status, stream)
+    return out
+
+
+def expert_gate_up_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor,
+                       w: torch.Tensor, w_scale: torch.Tensor,
+                       status: Optional[torch.Tensor] = None, stream=None
+                       ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """silu(gate) * up of each expert's rows, quantised again: (e4m3
+    [num_recv, I], fp32 scales [num_recv, I / 128]); the next product's rows."""
+    R, width = a.shape[0], w.shape[1] // 2
+    out_q = torch.empty((R, width), dtype=torch.float8_e4m3fn, device=a.device)
+    out_scale = torch.empty((R, -(-width // FP8_BLOCK)), dtype=torch.float32, device=a.device)
+    ep_expert_gate_up_fp8(a, a_scale, offsets, w, w_scale, out_q, out_scale, status, stream)
+    return out_q, out_scale

@@ -284,6 +284,47 @@ EP_API ep_status_t ep_combine(const uint16_t* expert_out, int64_t num_recv,
                        int64_t T, int64_t H, int K,
                        uint16_t* y, int32_t* status, void* stream);
 
+/* ---- the experts, in 8 bits --------------------------------------------------
+ * Rows and weights as e4m3 bytes with one fp32 scale for each block of 128
+ * values, so that value = byte * scale: rows in blocks of 1 x 128 along
+ * their width (the last block may be shorter), weights in blocks of
+ * 128 x 128. Row r belongs to expert e where offsets[e] <= r < offsets[e+1]
+ * (offsets of the layout calls); rows from offsets[E] on are neither used nor
+ * written. The pages have no counterpart: they end where the rows arrive. */
+
+/* The experts' product:
+ *   out[r, n] = bf16_rne( sum over blocks b of a_scale[r,b] *
+ *               w_scale[e, n/128, b] * (sum over k in b of a[r,k] * w[e,n,k]) )
+ * with fp32 sums throughout.
+ *   a        e4m3 [num_recv][K]            a_scale  fp32 [num_recv][ceil(K/128)]
+ *   w        e4m3 [E][N][K]                w_scale  fp32 [E][ceil(N/128)][ceil(K/128)]
+ *   offsets  int32 [E+1], on the device    out      bf16 [num_recv][N]
+ * K a multiple of 16, N of 8; a, w and out 16-byte aligned; E * N and K below
+ * 2^31 - 256. Offsets that do not ascend from 0 or more to at most num_recv
+ * report EP_ERR_BAD_SLOT, and the expert concerned is skipped. The SM budget
+ * does not apply (it leaves SMs to work like this); a call into an SM
+ * partition's stream uses the partition's SMs. */
+EP_API ep_status_t ep_expert_matmul_fp8(const uint8_t* a, const float* a_scale, int64_t num_recv,
+                                        const int32_t* offsets, int E, const uint8_t* w,
+                                        const float* w_scale, int64_t N, int64_t K, uint16_t* out,
+                                        int32_t* status, void* stream);
+
+/* The experts' first product with its activation: w holds a gate half (rows
+ * 0 .. I-1 of each expert) and an up half (rows I .. 2I-1);
+ *   h[r, i] = silu(y[r, i]) * y[r, I + i],  silu(g) = g / (1 + exp(-g))
+ * with y the product above in fp32, and h quantised in blocks of 128:
+ *   m = max(max |h| of the block, 1e-30)  out_scale = m / 448
+ *   out_q = e4m3_rne(h * (448 / m))
+ *   w        e4m3 [E][2I][K]               w_scale  fp32 [E][2I/128][ceil(K/128)]
+ *   out_q    e4m3 [num_recv][I]            out_scale fp32 [num_recv][I/128]
+ * I a multiple of 128; otherwise as ep_expert_matmul_fp8, whose `a` and
+ * `a_scale` these outputs are. A block of h that holds an infinity or NaN
+ * gets a scale that is not finite. */
+EP_API ep_status_t ep_expert_gate_up_fp8(const uint8_t* a, const float* a_scale, int64_t num_recv,
+                                         const int32_t* offsets, int E, const uint8_t* w,
+                                         const float* w_scale, int64_t I, int64_t K, uint8_t* out_q,
+                                         float* out_scale, int32_t* status, void* stream);
+
 /* Layout without a workspace argument, for callers that cannot allocate
  * device memory. The pages have no counterpart; this is a library addition.
  * Such callers include a serving engine that reserved nearly all of HBM up
