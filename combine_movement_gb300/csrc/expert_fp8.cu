@@ -18,7 +18,7 @@
 // along K, so they cannot ride in the tensor core's sum: eight warps read each
 // block's sums back and add them, scaled, into fp32 registers (a thread holds
 // 64 + 64 columns of one row), while the tensor core works on the next
-// block. One warp issues the copies, one the products.
+// block. One warp issues the copies, one the products, one the scales' copies.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -39,9 +39,18 @@ constexpr uint32_t kStageB = kTileCols * kTileK;
 constexpr uint32_t kStageBytes = kStageA + kStageB;
 constexpr int kStages = 4;
 constexpr int kAccWarps = 8;
-constexpr int kThreads = (kAccWarps + 2) * 32;
+constexpr int kCopyWarp = kAccWarps, kProductWarp = kAccWarps + 1, kScaleWarp = kAccWarps + 2;
+constexpr int kThreads = (kAccWarps + 3) * 32;
 constexpr uint32_t kTmemCols = 512;            // two halves of 256 columns
 constexpr int kRowBoxes = 4;                   // row boxes of 16, 32, 64, 128
+
+// Scales of one stage: of the tile's 128 rows, then of its two weight blocks.
+// The scales of fill i overwrite those of fill i - kScaleSlots. A stage is
+// refilled once its product is done (fill i - kStages), and that product
+// began after the sums of fill i - kStages - 2 were read, with their scales:
+// so kStages + 2 slots suffice.
+constexpr int kScaleSlots = 8;
+static_assert(kScaleSlots >= kStages + 2, "scales in use would be overwritten");
 
 struct Maps {
     CUtensorMap rows[kRowBoxes];
@@ -59,6 +68,8 @@ struct Control {
     int32_t abort;
     int32_t warp_sum[32];
     uint32_t amax[2][2][kTileRows];
+    float row_scale[kScaleSlots][kTileRows];
+    float weight_scale[kScaleSlots][2];
 };
 
 // Wait on a barrier; false once it gave up after kWaitLimitNs or another
@@ -66,6 +77,8 @@ struct Control {
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int32_t* abort,
                                               int32_t* status) {
     if (mbar_try_wait(bar, parity)) return true;
+    for (int i = 0; i < 64; ++i)  // the timer is slow to read
+        if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -137,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + 8 * i, 1);
+            mbar_init(full + 8 * i, 1 + 32);  // the copies' bytes, the scale warp's lanes
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -149,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ctl.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kAccWarps + 1) tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
-    if (warp == kAccWarps && lane == 0) {
+    if (warp == kProductWarp) tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
+    if (warp == kCopyWarp && lane == 0) {
         for (int i = 0; i < kRowBoxes; ++i) prefetch_tensor_map(&maps.rows[i]);
         prefetch_tensor_map(&maps.weights);
     }
@@ -187,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kb_count = a.k_blocks;
     int64_t fills = 0;  // stages filled so far (the copying lane's)
 
-    if (warp == kAccWarps) {
+    if (warp == kCopyWarp) {
         // ---- copies: one lane fills the stages in order ----
         if (lane == 0) {
             const uint64_t keep = policy_evict_last(), stream = policy_evict_normal();
@@ -214,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fills = it;
         }
-    } else if (warp == kAccWarps + 1) {
+    } else if (warp == kProductWarp) {
         // ---- products: one lane ----
         if (lane == 0) {
             constexpr uint32_t kDesc = mma_desc_e4m3(kTileRows, kTileCols);
@@ -239,36 +252,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+    } else if (warp == kScaleWarp) {
+        // ---- scales: small copies that arrive on the stage's barrier too ----
+        const int n_blocks = (a.n + kFp8Block - 1) / kFp8Block;
+        int64_t it = 0;
+        bool ok = true;
+        for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            const Tile tile = find_tile(t, cum, a);
+            const int b0 = kGateUp ? tile.col_tile : 2 * tile.col_tile;
+            const int b1 = kGateUp ? b0 + n_blocks / 2 : min(b0 + 1, n_blocks - 1);
+            const float* row[kTileRows / 32];
+#pragma unroll
+            for (int i = 0; i < kTileRows / 32; ++i)
+                row[i] = a.a_scale +
+                         static_cast<int64_t>(tile.row0 + min(i * 32 + lane, tile.rows - 1)) * kb_count;
+            const float* weight =
+                a.w_scale +
+                (static_cast<int64_t>(tile.expert) * n_blocks + (lane == 0 ? b0 : b1)) * kb_count;
+            for (int kb = 0; kb < kb_count; ++kb, ++it) {
+                const uint32_t s = static_cast<uint32_t>(it % kStages), slot = it % kScaleSlots;
+                ok = wait_or_abort(empty + 8 * s, static_cast<uint32_t>((it / kStages) & 1) ^ 1u, abort,
+                                   a.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kTileRows / 32; ++i)
+                    if (i * 32 < tile.rows)
+                        copy_async4(smem_u32(&ctl.row_scale[slot][i * 32 + lane]), row[i] + kb);
+                if (lane < 2) copy_async4(smem_u32(&ctl.weight_scale[slot][lane]), weight + kb);
+                copy_async_arrive(full + 8 * s);
+            }
+        }
+        copy_async_wait_all();
     } else {
         // ---- scaled sums: thread = one row, columns [64 h, 64 h + 64) of both blocks ----
         const int h = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t sums = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + h * 64;
-        const int n_blocks = (a.n + kFp8Block - 1) / kFp8Block;
         int64_t it = 0;
         uint32_t tile_no = 0;
         bool ok = true;
         for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
             const Tile tile = find_tile(t, cum, a);
             const bool live = quarter * 32 < tile.rows;  // warp-uniform
-            const int b0 = kGateUp ? tile.col_tile : 2 * tile.col_tile;
-            const int b1 = kGateUp ? b0 + n_blocks / 2 : min(b0 + 1, n_blocks - 1);
-            const int64_t grow = tile.row0 + min(row, tile.rows - 1);
-            const float* sa = a.a_scale + grow * kb_count;
-            const float* sw0 = a.w_scale + (static_cast<int64_t>(tile.expert) * n_blocks + b0) * kb_count;
-            const float* sw1 = a.w_scale + (static_cast<int64_t>(tile.expert) * n_blocks + b1) * kb_count;
+            const int64_t grow = tile.row0 + row;
             uint64_t acc[2][32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0ull;
-            float na = __ldg(sa), n0 = __ldg(sw0), n1 = __ldg(sw1);
             for (int kb = 0; kb < kb_count; ++kb, ++it) {
-                const float s0 = na * n0, s1 = na * n1;
-                if (kb + 1 < kb_count) {
-                    na = __ldg(sa + kb + 1);
-                    n0 = __ldg(sw0 + kb + 1);
-                    n1 = __ldg(sw1 + kb + 1);
-                }
-                const uint32_t half = it & 1;
+                const uint32_t half = it & 1, slot = it % kScaleSlots;
                 ok = wait_or_abort(sums_full + 8 * half, static_cast<uint32_t>((it >> 1) & 1), abort,
                                    a.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
@@ -276,6 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tcgen05_fence_after();
                 if (live) {
                     const uint32_t src = sums + half * kTileCols;
+                    const float sa = ctl.row_scale[slot][row];
+                    const float s0 = sa * ctl.weight_scale[slot][0];
+                    const float s1 = sa * ctl.weight_scale[slot][1];
                     uint64_t s2[2];
                     asm("mov.b64 %0, {%1, %1};" : "=l"(s2[0]) : "f"(s0));
                     asm("mov.b64 %0, {%1, %1};" : "=l"(s2[1]) : "f"(s1));
@@ -373,15 +408,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // no product may run once its tensor memory is released. (Otherwise every
     // copy and product has been waited for.)
     if (*abort != 0) {
-        if (warp == kAccWarps && lane == 0)
+        if (warp == kCopyWarp && lane == 0)
             mbar_drain_bounded<kStages>(full, fills > kStages ? fills - kStages : 0, fills - 1);
-        if (warp == kAccWarps + 1 && lane == 0) {
+        if (warp == kProductWarp && lane == 0) {
             mma_commit(smem_u32(&ctl.drained));
             mbar_wait_bounded(smem_u32(&ctl.drained), 0);
         }
         __syncwarp();
     }
-    if (warp == kAccWarps + 1) {
+    if (warp == kProductWarp) {
         tcgen05_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }

@@ -110,6 +110,19 @@ __device__ __forceinline__ void tensor_load_2d(uint32_t dst_smem, const CUtensor
         : "memory");
 }
 
+// ---- small asynchronous copies ------------------------------------------------------
+// Four bytes global -> shared by this lane; copy_async_arrive makes one
+// (already counted) arrival on `bar` when this lane's copies so far are done.
+__device__ __forceinline__ void copy_async4(uint32_t dst_smem, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
