@@ -8,17 +8,23 @@
 // bf16, or, for a first product whose columns are a gate half and an up half,
 // h = silu(y[r, i]) * y[r, I + i] quantised in blocks of 128 columns again.
 //
-// Mapping: a persistent grid, one CTA per SM. A tile is 128 rows of one
-// expert times two blocks of 128 weight rows (neighbours; for the gated form
-// block j of the gate half and block j of the up half, so that the tile holds
-// a whole quantisation block of h). Per 128 values along K one stage of
-// shared memory takes the operands (tensor copies, 128-byte swizzle) and four
-// tcgen05.mma of 128 x 256 x 32 leave that block's plain sums in one of two
-// halves of tensor memory. The scales differ between rows and between blocks
-// along K, so they cannot ride in the tensor core's sum: eight warps read each
-// block's sums back and add them, scaled, into fp32 registers (a thread holds
-// 64 + 64 columns of one row), while the tensor core works on the next
-// block. One warp issues the copies, one the products, one the scales' copies.
+// Mapping: a persistent grid of CTA pairs (clusters of two), one CTA per SM. A
+// tile is 256 rows of one expert times two blocks of 128 weight rows
+// (neighbours; for the gated form block j of the gate half and block j of
+// the up half, so that the tile holds a whole quantisation block of h). Each
+// Per 128 values along K one stage of shared memory takes the operands
+// (tensor copies, 128-byte swizzle), and tcgen05.mma of 256 x 128 x 32, four
+// for each half of the tile's columns, leave the block's plain sums in tensor
+// memory. The scales differ between rows and between blocks along K, so they
+// cannot ride in the tensor core's sum: for each half a warpgroup reads the
+// sums back and adds them, scaled, into fp32 registers (a thread holds 64
+// columns of both weight blocks of one row), while the tensor cores work on
+// the other half and on the next block (each half has two places in tensor
+// memory). One warp issues the copies, one for each half (of the first CTA)
+// the products, one the scales' copies.
+// A block's product takes the tensor cores 512 cycles, and a barrier that is
+// ready still takes 90 to ask, a commit 105 to issue: hence a product warp for
+// each half, and one wait (and a quarter) per block in the adding warps.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -35,22 +41,30 @@ constexpr int kTileRows = 128;
 constexpr int kTileK = 128;                    // bytes and values of one stage row
 constexpr int kTileCols = 2 * kFp8Block;       // weight rows of a tile
 constexpr uint32_t kStageA = kTileRows * kTileK;
-constexpr uint32_t kStageB = kTileCols * kTileK;
-constexpr uint32_t kStageBytes = kStageA + kStageB;
+constexpr int kPieceRows = kFp8Block / 2;      // weight rows per copy: a half's part of a block
+constexpr uint32_t kPiece = kPieceRows * kTileK;
+constexpr uint32_t kStageBytes = kStageA + 4 * kPiece;
 constexpr int kStages = 4;
+constexpr int kHalfCols = kTileCols / 2;       // columns of one product: 64 of each weight block
+constexpr int kSlots = 2;                      // of each half in tensor memory
 constexpr int kAccWarps = 8;
-constexpr int kCopyWarp = kAccWarps, kProductWarp = kAccWarps + 1, kScaleWarp = kAccWarps + 2;
-constexpr int kThreads = (kAccWarps + 3) * 32;
-constexpr uint32_t kTmemCols = 512;            // two halves of 256 columns
+constexpr int kAccCols = kHalfCols / 2;        // of each weight block, in one thread
+constexpr int kProductWarp = kAccWarps;        // and the next, one for each half
+constexpr int kCopyWarp = kAccWarps + 2, kScaleWarp = kAccWarps + 3;
+constexpr int kThreads = (kAccWarps + 4) * 32;
+// Registers per thread: the launch's 168 (384 threads) move from the last
+// warpgroup to the two that hold the sums: 256 x 224 + 128 x 56 = 384 x 168.
+constexpr int kAccRegs = 224, kOtherRegs = 56;
+static_assert(kAccWarps * 32 * kAccRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+constexpr uint32_t kTmemCols = kSlots * kTileCols;
+constexpr unsigned kPatienceNs = 100;
 constexpr int kRowBoxes = 4;                   // row boxes of 16, 32, 64, 128
 
-// Scales of one stage: of the tile's 128 rows, then of its two weight blocks.
-// The scales of fill i overwrite those of fill i - kScaleSlots. A stage is
-// refilled once its product is done (fill i - kStages), and that product
-// began after the sums of fill i - kStages - 2 were read, with their scales:
-// so kStages + 2 slots suffice.
-constexpr int kScaleSlots = 8;
-static_assert(kScaleSlots >= kStages + 2, "scales in use would be overwritten");
+// Scales: of the CTA's 128 rows and of the two weight blocks, for kScaleGroup
+// blocks along K at a time (a tile's last group may have fewer), in a ring of
+// their own between the scale warp and the adding warps.
+constexpr int kScaleGroup = 4;
+constexpr int kScaleGroups = 4;
 
 struct Maps {
     CUtensorMap rows[kRowBoxes];
@@ -58,65 +72,107 @@ struct Maps {
 };
 
 struct Control {
-    uint64_t full[kStages];
-    uint64_t empty[kStages];
-    uint64_t sums_full[2];
-    uint64_t sums_empty[2];
+    uint64_t full[kStages];       // the copies have landed
+    uint64_t done[2][kStages];    // the stage's product of a half is done: its sums are there
+    uint64_t scales[kScaleGroups];       // a group has landed: the scale warp's lanes
+    uint64_t scales_read[kScaleGroups];  // and has been read: the adding warps
+    alignas(16) uint64_t sums_read[2][kSlots];
     uint64_t joined;       // accumulating warps, once per tile
-    uint64_t drained;      // after an abort: products still in flight
+    uint64_t drained[2];   // after an abort: products still in flight
     uint32_t tmem;
     int32_t abort;
     int32_t warp_sum[32];
     uint32_t amax[2][2][kTileRows];
-    float row_scale[kScaleSlots][kTileRows];
-    float weight_scale[kScaleSlots][2];
+    float row_scale[kScaleGroups][kScaleGroup][kTileRows];
+    alignas(8) float weight_scale[kScaleGroups][kScaleGroup][2];
 };
 
-// Wait on a barrier; false once it gave up after kWaitLimitNs or another
-// warp did.
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int32_t* abort,
-                                              int32_t* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    for (int i = 0; i < 64; ++i)  // the timer is slow to read
-        if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort != 0) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            *abort = 1;
-            set_status(status, EP_ERR_TIMEOUT);
-            return false;
-        }
-    }
+__device__ __forceinline__ uint32_t load_shared(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float load_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 load_shared_f32x2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_shared(uint32_t addr, uint32_t v) {
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// One tile: 128 rows of an expert times two blocks of its weight rows.
+// Wait of a whole warp on a barrier; false, in every lane, once a lane gave up
+// after kWaitLimitNs or another warp did (the word at `abort`). The timer is
+// slow to read, so the first tries go without. A patient wait, for the warps
+// that run ahead of the products, sleeps between its tries: asking on takes
+// issue slots from the adding warps.
+template <bool kPatient>
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort,
+                                          int32_t* status) {
+    for (int i = 0; i < 256; ++i) {
+        if (kPatient) __nanosleep(kPatienceNs);
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    }
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+        const bool late = global_timer_ns() - t0 > kWaitLimitNs;
+        if (late) {
+            store_shared(abort, 1);
+            set_status(status, EP_ERR_TIMEOUT);
+        }
+        if (__any_sync(0xFFFFFFFFu, late || load_shared(abort) != 0)) return false;
+    }
+}
+template <bool kPatient = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort,
+                                          int32_t* status) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    return wait_slow<kPatient>(bar, parity, abort, status);
+}
+
+// Position in a ring of N: index, and the parity of its current round.
+template <int N>
+struct Ring {
+    uint32_t i = 0, round = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            round ^= 1u;
+        }
+    }
+};
+
+// One tile: up to 128 rows of an expert times two blocks of its weight rows.
 struct Tile {
     int expert;
     int col_tile;
     int row0;   // first row
-    int rows;   // valid rows, 1 .. 128
+    int rows;   // 1 .. 128
 };
 
-// The tiles of expert e are [cum[e], cum[e + 1]) * col_tiles, row tiles
-// innermost: tiles that read the same weights run at the same time.
-__device__ __forceinline__ Tile find_tile(int64_t t, const int32_t* cum, const ExpertArgs& a) {
-    int lo = 0, hi = a.E;  // cum[lo] * col_tiles <= t < cum[hi] * col_tiles
+// The tiles of expert e are cum[e] .. cum[e + 1], row tiles innermost: tiles
+// that read the same weights run at the same time.
+__device__ __forceinline__ Tile find_tile(int t, const int32_t* cum, const ExpertArgs& a) {
+    int lo = 0, hi = a.E;  // cum[lo] <= t < cum[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (static_cast<int64_t>(cum[mid]) * a.col_tiles <= t)
+        if (cum[mid] <= t)
             lo = mid;
         else
             hi = mid;
     }
-    const int row_tiles = cum[lo + 1] - cum[lo];
-    const uint32_t local = static_cast<uint32_t>(t - static_cast<int64_t>(cum[lo]) * a.col_tiles);
+    const int begin = __ldg(a.offsets + lo), end = __ldg(a.offsets + lo + 1);
+    const uint32_t local = t - cum[lo], row_tiles = (end - begin + kTileRows - 1) / kTileRows;
     Tile tile;
     tile.expert = lo;
     tile.col_tile = static_cast<int>(local / row_tiles);
-    const int rt = static_cast<int>(local - static_cast<uint32_t>(tile.col_tile) * row_tiles);
-    const int begin = __ldg(a.offsets + lo), end = __ldg(a.offsets + lo + 1);
+    const int rt = static_cast<int>(local - tile.col_tile * row_tiles);
     tile.row0 = begin + rt * kTileRows;
     tile.rows = min(kTileRows, end - tile.row0);
     return tile;
@@ -133,6 +189,14 @@ __device__ __forceinline__ int expert_rows(int e, const ExpertArgs& a) {
     return end - begin;
 }
 
+// acc[i0 ..] += s * v for 16 columns. (Single fmas: a packed pair, fma.rn.f32x2,
+// takes three issue slots on this GPU, two single ones two.)
+__device__ __forceinline__ void add_scaled(float (&acc)[kAccCols], int i0, const uint32_t (&v)[16],
+                                           float s) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i0 + i] = fmaf(s, __uint_as_float(v[i]), acc[i0 + i]);
+}
+
 template <bool kGateUp>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_kernel(const ExpertArgs a, const __grid_constant__ Maps maps) {
@@ -143,22 +207,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t* cum = reinterpret_cast<int32_t*>(smem_raw + (base - smem_u32(smem_raw)) +
                                               kStages * kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t full = smem_u32(ctl.full), empty = smem_u32(ctl.empty);
-    const uint32_t sums_full = smem_u32(ctl.sums_full), sums_empty = smem_u32(ctl.sums_empty);
+    const uint32_t full = smem_u32(ctl.full), done = smem_u32(ctl.done);
+    const uint32_t sums_read = smem_u32(ctl.sums_read);
+    const uint32_t scales = smem_u32(ctl.scales), scales_read = smem_u32(ctl.scales_read);
     const uint32_t joined = smem_u32(&ctl.joined);
-    volatile int32_t* abort = &ctl.abort;
+    const uint32_t abort = smem_u32(&ctl.abort);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(full + 8 * i, 1 + 32);  // the copies' bytes, the scale warp's lanes
-            mbar_init(empty + 8 * i, 1);
+            mbar_init(full + 8 * i, 1);
+            mbar_init(done + 8 * i, 1);
+            mbar_init(done + 8 * (kStages + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(sums_full + 8 * i, 1);
-            mbar_init(sums_empty + 8 * i, kAccWarps);
+        for (int i = 0; i < kScaleGroups; ++i) {
+            mbar_init(scales + 8 * i, 32);
+            mbar_init(scales_read + 8 * i, kAccWarps);
         }
+        for (int i = 0; i < 2 * kSlots; ++i) mbar_init(sums_read + 8 * i, kAccWarps / 2);
         mbar_init(joined, kAccWarps);
-        mbar_init(smem_u32(&ctl.drained), 1);
+        mbar_init(smem_u32(&ctl.drained[0]), 1);
+        mbar_init(smem_u32(&ctl.drained[1]), 1);
         ctl.abort = 0;
         fence_mbar_init();
     }
@@ -170,12 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     griddep_launch_dependents();
 
-    // cum[e] = row tiles of the experts before e
+    // cum[e] = tiles of the experts before e
     {
         const int per = (a.E + kThreads - 1) / kThreads;
         const int e0 = min(static_cast<int>(threadIdx.x) * per, a.E), e1 = min(e0 + per, a.E);
         int mine = 0;
-        for (int e = e0; e < e1; ++e) mine += (expert_rows(e, a) + kTileRows - 1) / kTileRows;
+        for (int e = e0; e < e1; ++e) mine += (expert_rows(e, a) + kTileRows - 1) / kTileRows * a.col_tiles;
         int incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -188,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 0; w < warp; ++w) run += ctl.warp_sum[w];
         for (int e = e0; e < e1; ++e) {
             cum[e] = run;
-            run += (expert_rows(e, a) + kTileRows - 1) / kTileRows;
+            run += (expert_rows(e, a) + kTileRows - 1) / kTileRows * a.col_tiles;
         }
         if (threadIdx.x == kThreads - 1) cum[a.E] = run;
     }
@@ -196,184 +264,194 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tcgen05_fence_after();
     const uint32_t tmem = ctl.tmem;
-    const int64_t tiles = static_cast<int64_t>(cum[a.E]) * a.col_tiles;
+    const int tiles = cum[a.E];
     const int kb_count = a.k_blocks;
-    int64_t fills = 0;  // stages filled so far (the copying lane's)
+    uint32_t fills = 0;  // stages filled so far (the copying warp's)
 
-    if (warp == kCopyWarp) {
-        // ---- copies: one lane fills the stages in order ----
-        if (lane == 0) {
-            const uint64_t keep = policy_evict_last(), stream = policy_evict_normal();
-            int64_t it = 0;
+    if (warp >= kAccWarps) {
+        set_max_registers_down<kOtherRegs>();
+        if (warp == kCopyWarp) {
+            // ---- copies: one lane fills the stages in order ----
+            const uint64_t keep = policy_evict_last();
+            Ring<kStages> st;
             bool ok = true;
-            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 const Tile tile = find_tile(t, cum, a);
                 const int box = tile.rows > 64 ? 3 : tile.rows > 32 ? 2 : tile.rows > 16 ? 1 : 0;
-                const uint32_t bytes = (16u << box) * kTileK + kStageB;
+                const uint32_t bytes = (16u << box) * kTileK + 4 * kPiece;
                 const int w0 = tile.expert * a.n + tile.col_tile * (kGateUp ? kFp8Block : kTileCols);
                 const int w1 = w0 + (kGateUp ? a.n / 2 : kFp8Block);
-                for (int kb = 0; kb < kb_count; ++kb, ++it) {
-                    const uint32_t s = static_cast<uint32_t>(it % kStages);
-                    ok = wait_or_abort(empty + 8 * s, static_cast<uint32_t>((it / kStages) & 1) ^ 1u,
-                                       abort, a.status);
+                for (int kb = 0; kb < kb_count; ++kb, st.next(), ++fills) {
+#pragma unroll 1
+                    for (int h = 0; ok && h < 2; ++h)  // both halves are done with the stage
+                        ok = warp_wait<true>(done + 8 * (h * kStages + st.i), st.round ^ 1u, abort,
+                                             a.status);
                     if (!ok) break;
-                    const uint32_t dst = base + s * kStageBytes, bar = full + 8 * s;
-                    mbar_arrive_expect_tx(bar, bytes);
-                    tensor_load_2d(dst, &maps.rows[box], kb * kTileK, tile.row0, bar, keep);
-                    tensor_load_2d(dst + kStageA, &maps.weights, kb * kTileK, w0, bar, stream);
-                    tensor_load_2d(dst + kStageA + kStageB / 2, &maps.weights, kb * kTileK, w1, bar,
-                                   stream);
+                    if (elect_one()) {
+                        // rows, then each half's pieces of both weight blocks
+                        const uint32_t dst = base + st.i * kStageBytes, bar = full + 8 * st.i;
+                        const int x = kb * kTileK;
+                        mbar_arrive_expect_tx(bar, bytes);
+                        tensor_load_2d(dst, &maps.rows[box], x, tile.row0, bar, keep);
+                        tensor_load_2d(dst + kStageA, &maps.weights, x, w0, bar);
+                        tensor_load_2d(dst + kStageA + kPiece, &maps.weights, x, w1, bar);
+                        tensor_load_2d(dst + kStageA + 2 * kPiece, &maps.weights, x, w0 + kPieceRows, bar);
+                        tensor_load_2d(dst + kStageA + 3 * kPiece, &maps.weights, x, w1 + kPieceRows, bar);
+                    }
+                    __syncwarp();
                 }
             }
-            fills = it;
-        }
-    } else if (warp == kProductWarp) {
-        // ---- products: one lane ----
-        if (lane == 0) {
-            constexpr uint32_t kDesc = mma_desc_e4m3(kTileRows, kTileCols);
-            int64_t it = 0;
+        } else if (warp != kScaleWarp) {
+            // ---- products of one half ----
+            constexpr uint32_t kDesc = mma_desc_e4m3(kTileRows, kHalfCols);
+            const uint32_t h = warp - kProductWarp;
+            const uint64_t desc0 = operand_desc(base);
+            const uint32_t done_h = done + 8 * kStages * h, read_h = sums_read + 8 * kSlots * h;
+            Ring<kStages> st;
+            Ring<kSlots> slot;
             bool ok = true;
-            for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                for (int kb = 0; kb < kb_count; ++kb, ++it) {
-                    const uint32_t s = static_cast<uint32_t>(it % kStages), half = it & 1;
-                    ok = wait_or_abort(sums_empty + 8 * half, static_cast<uint32_t>((it >> 1) & 1) ^ 1u,
-                                       abort, a.status) &&
-                         wait_or_abort(full + 8 * s, static_cast<uint32_t>((it / kStages) & 1), abort,
-                                       a.status);
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                for (int kb = 0; kb < kb_count; ++kb, st.next(), slot.next()) {
+                    ok = warp_wait(full + 8 * st.i, st.round, abort, a.status) &&
+                         warp_wait(read_h + 8 * slot.i, slot.round ^ 1u, abort, a.status);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint64_t da = operand_desc(base + s * kStageBytes);
-                    const uint64_t db = operand_desc(base + s * kStageBytes + kStageA);
+                    if (elect_one()) {
+                        const uint64_t da = desc0 + st.i * (kStageBytes >> 4);
+                        const uint64_t db = da + ((kStageA + h * 2 * kPiece) >> 4);
+                        const uint32_t sums = tmem + (2 * slot.i + h) * kHalfCols;
 #pragma unroll
-                    for (int k = 0; k < kTileK / 32; ++k)
-                        mma_e4m3(tmem + half * kTileCols, da + 2 * k, db + 2 * k, kDesc, k > 0);
-                    mma_commit(empty + 8 * s);
-                    mma_commit(sums_full + 8 * half);
+                        for (int k = 0; k < kTileK / 32; ++k)
+                            mma_e4m3(sums, da + 2 * k, db + 2 * k, kDesc, k > 0);
+                        mma_commit(done_h + 8 * st.i);
+                    }
+                    __syncwarp();
                 }
             }
-        }
-    } else if (warp == kScaleWarp) {
-        // ---- scales: small copies that arrive on the stage's barrier too ----
-        const int n_blocks = (a.n + kFp8Block - 1) / kFp8Block;
-        int64_t it = 0;
-        bool ok = true;
-        for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const Tile tile = find_tile(t, cum, a);
-            const int b0 = kGateUp ? tile.col_tile : 2 * tile.col_tile;
-            const int b1 = kGateUp ? b0 + n_blocks / 2 : min(b0 + 1, n_blocks - 1);
-            const float* row[kTileRows / 32];
-#pragma unroll
-            for (int i = 0; i < kTileRows / 32; ++i)
-                row[i] = a.a_scale +
-                         static_cast<int64_t>(tile.row0 + min(i * 32 + lane, tile.rows - 1)) * kb_count;
-            const float* weight =
-                a.w_scale +
-                (static_cast<int64_t>(tile.expert) * n_blocks + (lane == 0 ? b0 : b1)) * kb_count;
-            for (int kb = 0; kb < kb_count; ++kb, ++it) {
-                const uint32_t s = static_cast<uint32_t>(it % kStages), slot = it % kScaleSlots;
-                ok = wait_or_abort(empty + 8 * s, static_cast<uint32_t>((it / kStages) & 1) ^ 1u, abort,
-                                   a.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < kTileRows / 32; ++i)
-                    if (i * 32 < tile.rows)
-                        copy_async4(smem_u32(&ctl.row_scale[slot][i * 32 + lane]), row[i] + kb);
-                if (lane < 2) copy_async4(smem_u32(&ctl.weight_scale[slot][lane]), weight + kb);
-                copy_async_arrive(full + 8 * s);
+        } else if (warp == kScaleWarp) {
+            // ---- scales: small copies, ahead of the sums by the stages' depth ----
+            const int n_blocks = (a.n + kFp8Block - 1) / kFp8Block;
+            const uint32_t row_dst = smem_u32(&ctl.row_scale[0][0][lane]);
+            Ring<kScaleGroups> group;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const Tile tile = find_tile(t, cum, a);
+                const int b0 = kGateUp ? tile.col_tile : 2 * tile.col_tile;
+                const int b1 = kGateUp ? b0 + n_blocks / 2 : min(b0 + 1, n_blocks - 1);
+                const int rows = tile.rows;
+                const float* row = a.a_scale + static_cast<int64_t>(tile.row0 + lane) * kb_count;
+                const float* weight =
+                    a.w_scale +
+                    (static_cast<int64_t>(tile.expert) * n_blocks + ((lane & 1) == 0 ? b0 : b1)) * kb_count;
+                for (int kb0 = 0; kb0 < kb_count; kb0 += kScaleGroup, group.next()) {
+                    ok = warp_wait<true>(scales_read + 8 * group.i, group.round ^ 1u, abort, a.status);
+                    if (!ok) break;
+                    const int count = min(kScaleGroup, kb_count - kb0);
+                    uint32_t dst = row_dst + group.i * sizeof(ctl.row_scale[0]);
+#pragma unroll 1
+                    for (int i = lane; i < rows; i += 32, dst += 32 * 4) {
+                        const float* src = row + static_cast<int64_t>(i - lane) * kb_count + kb0;
+                        for (int j = 0; j < count; ++j) copy_async4(dst + j * (4 * kTileRows), src + j);
+                    }
+                    if (lane < 2 * count) {
+                        const uint32_t j = lane >> 1;
+                        copy_async4(smem_u32(&ctl.weight_scale[group.i][j][lane & 1]), weight + kb0 + j);
+                    }
+                    copy_async_arrive(scales + 8 * group.i);
+                }
             }
+            copy_async_wait_all();
         }
-        copy_async_wait_all();
     } else {
         // ---- scaled sums: thread = one row, columns [64 h, 64 h + 64) of both blocks ----
+        set_max_registers_up<kAccRegs>();
         const int h = warp >> 2, quarter = warp & 3;
-        const int row = quarter * 32 + lane;
-        const uint32_t sums = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + h * 64;
-        int64_t it = 0;
+        const uint32_t row_scale = smem_u32(&ctl.row_scale[0][0][quarter * 32 + lane]);
+        const uint32_t weight_scale = smem_u32(ctl.weight_scale);
+        uint32_t sums = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + h * kHalfCols;
+        uint32_t read = sums_read + 8 * kSlots * h;
+        const uint32_t done_h = done + 8 * kStages * h;
+        Ring<kScaleGroups> group;
+        Ring<kStages> st;
         uint32_t tile_no = 0;
         bool ok = true;
-        for (int64_t t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
-            const Tile tile = find_tile(t, cum, a);
-            const bool live = quarter * 32 < tile.rows;  // warp-uniform
-            const int64_t grow = tile.row0 + row;
-            uint64_t acc[2][32];
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
+            const bool live = quarter * 32 < find_tile(t, cum, a).rows;  // warp-uniform
+            float acc[2][kAccCols];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0ull;
-            for (int kb = 0; kb < kb_count; ++kb, ++it) {
-                const uint32_t half = it & 1, slot = it % kScaleSlots;
-                ok = wait_or_abort(sums_full + 8 * half, static_cast<uint32_t>((it >> 1) & 1), abort,
-                                   a.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+            for (int i = 0; i < kAccCols; ++i) acc[0][i] = acc[1][i] = 0.0f;
+            for (int kb0 = 0; kb0 < kb_count; kb0 += kScaleGroup, group.next()) {
+                ok = warp_wait(scales + 8 * group.i, group.round, abort, a.status);
                 if (!ok) break;
-                tcgen05_fence_after();
-                if (live) {
-                    const uint32_t src = sums + half * kTileCols;
-                    const float sa = ctl.row_scale[slot][row];
-                    const float s0 = sa * ctl.weight_scale[slot][0];
-                    const float s1 = sa * ctl.weight_scale[slot][1];
-                    uint64_t s2[2];
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(s2[0]) : "f"(s0));
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(s2[1]) : "f"(s1));
-                    uint32_t v[2][16];
-                    tmem_load16(src, v[0]);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        tmem_load_wait16(v[c & 1]);
-                        if (c < 7)
-                            tmem_load16(src + ((c + 1) >> 2) * kFp8Block + ((c + 1) & 3) * 16,
-                                        v[(c + 1) & 1]);
+                uint32_t row_at = row_scale + group.i * sizeof(ctl.row_scale[0]);
+                uint32_t weight_at = weight_scale + group.i * sizeof(ctl.weight_scale[0]);
+                const int kb1 = min(kb0 + kScaleGroup, kb_count);
+#pragma unroll 1
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    const float sa = load_shared_f32(row_at);
+                    const float2 sw = load_shared_f32x2(weight_at);
+                    const float s0 = sa * sw.x, s1 = sa * sw.y;
+                    ok = warp_wait(done_h + 8 * st.i, st.round, abort, a.status);
+                    if (!ok) break;
+                    st.next();
+                    if (live) {
+                        // while 16 columns are added the next 16 are on their way
+                        tcgen05_fence_after();
+                        uint32_t v[2][16];
+                        tmem_load16(sums, v[0]);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            uint64_t d;
-                            asm("mov.b64 %0, {%1, %2};"
-                                : "=l"(d)
-                                : "r"(v[c & 1][2 * i]), "r"(v[c & 1][2 * i + 1]));
-                            asm("fma.rn.f32x2 %0, %1, %2, %0;"
-                                : "+l"(acc[c >> 2][(c & 3) * 8 + i])
-                                : "l"(d), "l"(s2[c >> 2]));
+                            tmem_load_wait16(v[i & 1]);
+                            if (i < 7) tmem_load16(sums + 16 * (i + 1), v[(i + 1) & 1]);
+                            if (i == 7) {
+                                tcgen05_fence_before();
+                                if (lane == 0) mbar_arrive(read);
+                            }
+                            add_scaled(acc[i >> 2], 16 * (i & 3), v[i & 1], i < 4 ? s0 : s1);
                         }
+                    } else if (lane == 0) {
+                        mbar_arrive(read);
                     }
-                    tcgen05_fence_before();
+                    row_at += sizeof(ctl.row_scale[0][0]);
+                    weight_at += sizeof(ctl.weight_scale[0][0]);
+                    sums ^= kTileCols;  // the half's other place: tmem starts at a multiple of 512
+                    read ^= 8u;         // sums_read is 16-byte aligned
                 }
+                if (!ok) break;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sums_empty + 8 * half);
+                if (lane == 0) mbar_arrive(scales_read + 8 * group.i);
             }
             if (!ok) break;
+            // (looked up again rather than kept in registers through the sums)
+            const Tile tile = find_tile(t, cum, a);
+            const int row = quarter * 32 + lane;
             const bool store = row < tile.rows;
+            const int64_t grow = tile.row0 + row;
             if (kGateUp) {
-                float v[64];
                 uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float g[2], u[2];
-                    asm("mov.b64 {%0, %1}, %2;" : "=f"(g[0]), "=f"(g[1]) : "l"(acc[0][i]));
-                    asm("mov.b64 {%0, %1}, %2;" : "=f"(u[0]), "=f"(u[1]) : "l"(acc[1][i]));
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float y = g[j] / (1.0f + expf(-g[j])) * u[j];
-                        v[2 * i + j] = y;
-                        top = max(top, abs_bits(y));
-                    }
+                for (int i = 0; i < kAccCols; ++i) {
+                    const float g = acc[0][i];
+                    acc[0][i] = g / (1.0f + expf(-g)) * acc[1][i];
+                    top = max(top, abs_bits(acc[0][i]));
                 }
-                // the block's other 64 columns are in the other half's warps
-                uint32_t* amax = &ctl.amax[tile_no & 1][0][0];
-                amax[h * kTileRows + row] = top;
+                // the block's other columns are in the other half's warps
+                uint32_t* amax = &ctl.amax[tile_no & 1][0][row];
+                amax[h * kTileRows] = top;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(joined);
-                ok = wait_or_abort(joined, tile_no & 1, abort, a.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                ok = warp_wait(joined, tile_no & 1, abort, a.status);
                 if (!ok) break;
-                top = max(top, amax[(h ^ 1) * kTileRows + row]);
-                const BlockScale bs = block_scale(top);
+                const BlockScale bs = block_scale(max(top, amax[(h ^ 1) * kTileRows]));
                 if (store) {
                     const int width = a.n / 2;
-                    uint8_t* q = a.out_q + grow * width + tile.col_tile * kFp8Block + h * 64;
+                    uint8_t* q = a.out_q + grow * width + tile.col_tile * kFp8Block + h * kAccCols;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kAccCols / 16; ++i) {
                         uint32_t p[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float* f = v + i * 16 + j * 4;
+                            const float* f = &acc[0][i * 16 + j * 4];
                             p[j] = pack_e4m3x4(f[0] * bs.inverse, f[1] * bs.inverse,
                                                f[2] * bs.inverse, f[3] * bs.inverse);
                         }
@@ -382,21 +460,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (h == 0) a.out_scale[grow * (width / kFp8Block) + tile.col_tile] = bs.scale;
                 }
             } else if (store) {
-                const int64_t col0 = static_cast<int64_t>(tile.col_tile) * kTileCols + h * 64;
+                const int64_t col0 = static_cast<int64_t>(tile.col_tile) * kTileCols + h * kAccCols;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < kAccCols / 8; ++i) {
                         const int64_t col = col0 + b * kFp8Block + i * 8;
-                        uint32_t p[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float lo, hi;
-                            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(acc[b][i * 4 + j]));
-                            p[j] = pack_bf16x2(lo, hi);
-                        }
+                        const float* f = &acc[b][i * 8];
                         if (col < a.n)
-                            st_v4(a.out + grow * a.n + col, make_uint4(p[0], p[1], p[2], p[3]));
+                            st_v4(a.out + grow * a.n + col,
+                                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
                     }
             }
         }
@@ -407,15 +481,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // After a wait that gave up: no copy may land once the CTA has exited, and
     // no product may run once its tensor memory is released. (Otherwise every
     // copy and product has been waited for.)
-    if (*abort != 0) {
+    if (load_shared(abort) != 0) {
         if (warp == kCopyWarp && lane == 0)
-            mbar_drain_bounded<kStages>(full, fills > kStages ? fills - kStages : 0, fills - 1);
-        if (warp == kProductWarp && lane == 0) {
-            mma_commit(smem_u32(&ctl.drained));
-            mbar_wait_bounded(smem_u32(&ctl.drained), 0);
+            mbar_drain_bounded<kStages>(full, fills > kStages ? fills - kStages : 0u,
+                                        static_cast<int64_t>(fills) - 1);
+        if (warp == kProductWarp || warp == kProductWarp + 1) {
+            const uint32_t bar = smem_u32(&ctl.drained[warp - kProductWarp]);
+            if (elect_one()) mma_commit(bar);
+            __syncwarp();
+            mbar_wait_bounded(bar, 0);
         }
-        __syncwarp();
     }
+    __syncwarp();
     if (warp == kProductWarp) {
         tcgen05_fence_after();
         tmem_dealloc(tmem, kTmemCols);
@@ -464,12 +541,13 @@ cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream) {
     Maps maps;
     for (int i = 0; i < kRowBoxes; ++i)
         if (!encode_map(&maps.rows[i], a.a, a.num_recv, a.k, 16 << i)) return cudaErrorInvalidValue;
-    if (!encode_map(&maps.weights, a.w, static_cast<int64_t>(a.E) * a.n, a.k, kFp8Block))
+    if (!encode_map(&maps.weights, a.w, static_cast<int64_t>(a.E) * a.n, a.k, kPieceRows))
         return cudaErrorInvalidValue;
     // at most this many tiles, whatever the offsets say
     const int64_t row_tiles =
         a.num_recv / kTileRows + (a.num_recv < a.E ? a.num_recv : static_cast<int64_t>(a.E));
     const int64_t most = row_tiles * a.col_tiles;
+    if (most > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const int grid = static_cast<int>(most < num_sms ? most : num_sms);
     const size_t smem = 1024 + kStages * kStageBytes + sizeof(int32_t) * (a.E + 1);
     auto kern = gated ? expert_kernel<true> : expert_kernel<false>;

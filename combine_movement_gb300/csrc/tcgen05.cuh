@@ -47,8 +47,8 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&v)[16]) {
           "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
 }
-// Wait for this warp's tensor-memory loads; `v`, the last load's registers,
-// pass through so that nothing reads them before.
+// Wait for this warp's tensor-memory loads; `v`, a load's registers, pass
+// through so that nothing reads them before.
 __device__ __forceinline__ void tmem_load_wait16(uint32_t (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
@@ -75,7 +75,7 @@ constexpr uint32_t mma_desc_e4m3(uint32_t m, uint32_t n) {
     return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
-// D[tmem] = A B^T (+ D where `accumulate`), 32 values along K. One thread.
+// D[tmem] = A B^T (+ D where `accumulate`), 32 values along K; one thread.
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t desc,
                                          bool accumulate) {
     asm volatile(
@@ -93,20 +93,42 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
+// ---- registers ------------------------------------------------------------------
+// By all warps of a warpgroup; the kernel's warpgroups together stay within
+// the registers it was launched with.
+template <int N>
+__device__ __forceinline__ void set_max_registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---- tensor copies --------------------------------------------------------------
 
 __device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// Box of `map` at (x, y) -> shared memory, completing its bytes on `bar`.
-// x times the element size is a multiple of 16; out-of-range elements read 0.
+// Box of `map` at (x, y) -> shared memory, completing its bytes on `bar`. x
+// times the element size is a multiple of 16; out-of-range elements read 0.
 __device__ __forceinline__ void tensor_load_2d(uint32_t dst_smem, const CUtensorMap* map, int32_t x,
                                                int32_t y, uint32_t bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst_smem),
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst_smem),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// The same with the default L2 policy.
+__device__ __forceinline__ void tensor_load_2d(uint32_t dst_smem, const CUtensorMap* map, int32_t x,
+                                               int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst_smem),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
 
