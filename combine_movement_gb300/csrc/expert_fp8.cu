@@ -47,15 +47,16 @@ constexpr uint32_t kStageBytes = kStageA + 4 * kPiece;
 constexpr int kStages = 4;
 constexpr int kHalfCols = kTileCols / 2;       // columns of one product: 64 of each weight block
 constexpr int kSlots = 2;                      // of each half in tensor memory
-constexpr int kAccWarps = 8;
-constexpr int kAccCols = kHalfCols / 2;        // of each weight block, in one thread
+constexpr int kAccWarps = 16;
+constexpr int kAccGroups = kAccWarps / 4;      // warpgroups, two for each half
+constexpr int kAccCols = kHalfCols / 4;        // of each weight block, in one thread
 constexpr int kProductWarp = kAccWarps;        // and the next, one for each half
 constexpr int kCopyWarp = kAccWarps + 2, kScaleWarp = kAccWarps + 3;
 constexpr int kThreads = (kAccWarps + 4) * 32;
-// Registers per thread: the launch's 168 (384 threads) move from the last
-// warpgroup to the two that hold the sums: 256 x 224 + 128 x 56 = 384 x 168.
-constexpr int kAccRegs = 224, kOtherRegs = 56;
-static_assert(kAccWarps * 32 * kAccRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+// Registers per thread: the launch's 96 (640 threads) move from the last
+// warpgroup to the four that hold the sums: 512 x 104 + 128 x 64 = 640 x 96.
+constexpr int kAccRegs = 104, kOtherRegs = 64;
+static_assert(kAccWarps * 32 * kAccRegs + 128 * kOtherRegs <= kThreads * 96, "register split");
 constexpr uint32_t kTmemCols = kSlots * kTileCols;
 constexpr unsigned kPatienceNs = 100;
 constexpr int kRowBoxes = 4;                   // row boxes of 16, 32, 64, 128
@@ -82,7 +83,7 @@ struct Control {
     uint32_t tmem;
     int32_t abort;
     int32_t warp_sum[32];
-    uint32_t amax[2][2][kTileRows];
+    uint32_t amax[2][kAccGroups][kTileRows];
     float row_scale[kScaleGroups][kScaleGroup][kTileRows];
     alignas(8) float weight_scale[kScaleGroups][kScaleGroup][2];
 };
@@ -189,12 +190,20 @@ __device__ __forceinline__ int expert_rows(int e, const ExpertArgs& a) {
     return end - begin;
 }
 
-// acc[i0 ..] += s * v for 16 columns. (Single fmas: a packed pair, fma.rn.f32x2,
-// takes three issue slots on this GPU, two single ones two.)
+// acc[i0 ..] += s * v for 16 columns, two to an instruction (each rounded as by
+// fmaf; the pairs take as long as single fmas, and half the issue slots).
 __device__ __forceinline__ void add_scaled(float (&acc)[kAccCols], int i0, const uint32_t (&v)[16],
                                            float s) {
+    uint64_t s2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i0 + i] = fmaf(s, __uint_as_float(v[i]), acc[i0 + i]);
+    for (int i = 0; i < 16; i += 2) {
+        uint64_t d, sum;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(v[i]), "r"(v[i + 1]));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(sum) : "f"(acc[i0 + i]), "f"(acc[i0 + i + 1]));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(d), "l"(s2));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[i0 + i]), "=f"(acc[i0 + i + 1]) : "l"(sum));
+    }
 }
 
 template <bool kGateUp>
@@ -309,9 +318,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t done_h = done + 8 * kStages * h, read_h = sums_read + 8 * kSlots * h;
             Ring<kStages> st;
             Ring<kSlots> slot;
+            Ring<kScaleGroups> group;
             bool ok = true;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 for (int kb = 0; kb < kb_count; ++kb, st.next(), slot.next()) {
+                    // (the adding warps need the scales, and wait for this product only)
+                    if (kb % kScaleGroup == 0) {
+                        ok = warp_wait(scales + 8 * group.i, group.round, abort, a.status);
+                        if (!ok) break;
+                        group.next();
+                    }
                     ok = warp_wait(full + 8 * st.i, st.round, abort, a.status) &&
                          warp_wait(read_h + 8 * slot.i, slot.round ^ 1u, abort, a.status);
                     if (!ok) break;
@@ -363,12 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             copy_async_wait_all();
         }
     } else {
-        // ---- scaled sums: thread = one row, columns [64 h, 64 h + 64) of both blocks ----
+        // ---- scaled sums: thread = one row, columns [32 c, 32 c + 32) of both blocks ----
         set_max_registers_up<kAccRegs>();
-        const int h = warp >> 2, quarter = warp & 3;
+        const int c = warp >> 2, h = c >> 1, quarter = warp & 3;
         const uint32_t row_scale = smem_u32(&ctl.row_scale[0][0][quarter * 32 + lane]);
         const uint32_t weight_scale = smem_u32(ctl.weight_scale);
-        uint32_t sums = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + h * kHalfCols;
+        uint32_t sums = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + h * kHalfCols +
+                        (c & 1) * kAccCols;
         uint32_t read = sums_read + 8 * kSlots * h;
         const uint32_t done_h = done + 8 * kStages * h;
         Ring<kScaleGroups> group;
@@ -376,50 +393,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t tile_no = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
-            const bool live = quarter * 32 < find_tile(t, cum, a).rows;  // warp-uniform
             float acc[2][kAccCols];
 #pragma unroll
             for (int i = 0; i < kAccCols; ++i) acc[0][i] = acc[1][i] = 0.0f;
+            // The loop has no branch but the waits': warps whose rows the tile lacks
+            // add along (with a branch around that, 32768 rows on 256 experts took
+            // 1706 us instead of 1377), and after a wait that gave up the rest of
+            // the tile runs on without waiting or arriving.
             for (int kb0 = 0; kb0 < kb_count; kb0 += kScaleGroup, group.next()) {
-                ok = warp_wait(scales + 8 * group.i, group.round, abort, a.status);
-                if (!ok) break;
                 uint32_t row_at = row_scale + group.i * sizeof(ctl.row_scale[0]);
                 uint32_t weight_at = weight_scale + group.i * sizeof(ctl.weight_scale[0]);
                 const int kb1 = min(kb0 + kScaleGroup, kb_count);
 #pragma unroll 1
                 for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = ok && warp_wait(done_h + 8 * st.i, st.round, abort, a.status);
+                    st.next();
+                    tcgen05_fence_after();
+                    uint32_t v[16];
+                    tmem_load16(sums, v);
                     const float sa = load_shared_f32(row_at);
                     const float2 sw = load_shared_f32x2(weight_at);
                     const float s0 = sa * sw.x, s1 = sa * sw.y;
-                    ok = warp_wait(done_h + 8 * st.i, st.round, abort, a.status);
-                    if (!ok) break;
-                    st.next();
-                    if (live) {
-                        // while 16 columns are added the next 16 are on their way
-                        tcgen05_fence_after();
-                        uint32_t v[2][16];
-                        tmem_load16(sums, v[0]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            tmem_load_wait16(v[i & 1]);
-                            if (i < 7) tmem_load16(sums + 16 * (i + 1), v[(i + 1) & 1]);
-                            if (i == 7) {
-                                tcgen05_fence_before();
-                                if (lane == 0) mbar_arrive(read);
-                            }
-                            add_scaled(acc[i >> 2], 16 * (i & 3), v[i & 1], i < 4 ? s0 : s1);
-                        }
-                    } else if (lane == 0) {
-                        mbar_arrive(read);
-                    }
+                    tmem_load_wait16(v);
+                    add_scaled(acc[0], 0, v, s0);
+                    tmem_load16(sums + 16, v);
+                    tmem_load_wait16(v);
+                    add_scaled(acc[0], 16, v, s0);
+                    tmem_load16(sums + 64, v);
+                    tmem_load_wait16(v);
+                    add_scaled(acc[1], 0, v, s1);
+                    tmem_load16(sums + 80, v);
+                    tmem_load_wait16(v);
+                    tcgen05_fence_before();
+                    mbar_arrive_if(read, ok && lane == 0);
+                    add_scaled(acc[1], 16, v, s1);
                     row_at += sizeof(ctl.row_scale[0][0]);
                     weight_at += sizeof(ctl.weight_scale[0][0]);
                     sums ^= kTileCols;  // the half's other place: tmem starts at a multiple of 512
                     read ^= 8u;         // sums_read is 16-byte aligned
                 }
-                if (!ok) break;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(scales_read + 8 * group.i);
+                mbar_arrive_if(scales_read + 8 * group.i, ok && lane == 0);
             }
             if (!ok) break;
             // (looked up again rather than kept in registers through the sums)
@@ -435,17 +449,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     acc[0][i] = g / (1.0f + expf(-g)) * acc[1][i];
                     top = max(top, abs_bits(acc[0][i]));
                 }
-                // the block's other columns are in the other half's warps
+                // the block's other columns are in the other groups' warps
                 uint32_t* amax = &ctl.amax[tile_no & 1][0][row];
-                amax[h * kTileRows] = top;
+                amax[c * kTileRows] = top;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(joined);
                 ok = warp_wait(joined, tile_no & 1, abort, a.status);
                 if (!ok) break;
-                const BlockScale bs = block_scale(max(top, amax[(h ^ 1) * kTileRows]));
+#pragma unroll
+                for (int i = 0; i < kAccGroups; ++i) top = max(top, amax[i * kTileRows]);
+                const BlockScale bs = block_scale(top);
                 if (store) {
                     const int width = a.n / 2;
-                    uint8_t* q = a.out_q + grow * width + tile.col_tile * kFp8Block + h * kAccCols;
+                    uint8_t* q = a.out_q + grow * width + tile.col_tile * kFp8Block + c * kAccCols;
 #pragma unroll
                     for (int i = 0; i < kAccCols / 16; ++i) {
                         uint32_t p[4];
@@ -457,10 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         st_v4(q + i * 16, make_uint4(p[0], p[1], p[2], p[3]));
                     }
-                    if (h == 0) a.out_scale[grow * (width / kFp8Block) + tile.col_tile] = bs.scale;
+                    if (c == 0) a.out_scale[grow * (width / kFp8Block) + tile.col_tile] = bs.scale;
                 }
             } else if (store) {
-                const int64_t col0 = static_cast<int64_t>(tile.col_tile) * kTileCols + h * kAccCols;
+                const int64_t col0 = static_cast<int64_t>(tile.col_tile) * kTileCols + c * kAccCols;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
