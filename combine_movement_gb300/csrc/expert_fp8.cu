@@ -8,23 +8,32 @@
 // bf16, or, for a first product whose columns are a gate half and an up half,
 // h = silu(y[r, i]) * y[r, I + i] quantised in blocks of 128 columns again.
 //
-// Mapping: a persistent grid of CTA pairs (clusters of two), one CTA per SM. A
-// tile is 256 rows of one expert times two blocks of 128 weight rows
-// (neighbours; for the gated form block j of the gate half and block j of
-// the up half, so that the tile holds a whole quantisation block of h). Each
-// Per 128 values along K one stage of shared memory takes the operands
-// (tensor copies, 128-byte swizzle), and tcgen05.mma of 256 x 128 x 32, four
-// for each half of the tile's columns, leave the block's plain sums in tensor
-// memory. The scales differ between rows and between blocks along K, so they
-// cannot ride in the tensor core's sum: for each half a warpgroup reads the
-// sums back and adds them, scaled, into fp32 registers (a thread holds 64
-// columns of both weight blocks of one row), while the tensor cores work on
-// the other half and on the next block (each half has two places in tensor
-// memory). One warp issues the copies, one for each half (of the first CTA)
-// the products, one the scales' copies.
-// A block's product takes the tensor cores 512 cycles, and a barrier that is
-// ready still takes 90 to ask, a commit 105 to issue: hence a product warp for
-// each half, and one wait (and a quarter) per block in the adding warps.
+// Mapping: a persistent grid, one CTA per SM. A tile is 128 rows of one expert
+// times two blocks of 128 weight rows (neighbours; for the gated form block j
+// of the gate half and block j of the up half, so that the tile holds a whole
+// quantisation block of h). Per 128 values along K one of four stages of
+// shared memory takes the operands (tensor copies, 128-byte swizzle), and
+// tcgen05.mma of 128 x 128 x 32, four for each half of the tile's columns (64
+// of each weight block), leave the block's plain sums in tensor memory. The
+// scales differ between rows and between blocks along K, so they cannot ride
+// in the tensor core's sum: for each half two warpgroups read the sums back
+// and add them, scaled, into fp32 registers (a thread holds 32 columns of
+// both weight blocks of one row), while the tensor cores work on the other
+// half and on the next block (each half has two places in tensor memory). One
+// warp issues the tensor copies, one for each half the products, one the
+// scales' copies (four bytes each, asynchronous, four blocks ahead).
+//
+// What bounds it: few rows to an expert, the weights' bytes (256 experts x
+// 7168 x 2048 for 1024 rows: 538 us, 6.9 TB/s; one row each for eight experts
+// of 4096 x 7168: 50 us, 4.7 TB/s, 128 tiles on 152 SMs). Many rows, the adding:
+// a block's products take the tensor cores 512 cycles, a block's adding about
+// 850, mostly latencies (a barrier that is ready takes 70-150 cycles to ask, a
+// load from tensor memory 50-70), with 384 of them in the fma pipe (131072
+// rows x 7168 x 4096 on 128 experts: 3.19 ms, 2.4 PFLOP/s). Measured on the
+// way: eight adding warps with 64 columns of each block, 3.76 ms; a branch
+// around the adding for rows a tile lacks, 25 % slower at 128 rows an expert;
+// pairs of CTAs on tiles of 256 rows (cta_group::2: two thirds of the bytes
+// from L2) 3-5 % faster at 1000 rows an expert, 18-36 % slower below 130.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
