@@ -20,6 +20,9 @@
 // segment. Units whose K slots are all valid and which lie wholly inside the
 // row take an unpredicated body whose fmas go in packed fp32 pairs
 // (fma.rn.f32x2, the same rounding per element), for every K <= 8.
+//
+// Without weights (topk_w null) every weight is 1 and the sum is dispatch's
+// gradient: dx[t] = sum over k of d_recv[slot[t,k]].
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -126,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1) combine_kernel(const CombineArgs 
         if (t != tok) {
             tok = t;
             int32_t s = lane < K ? __ldg(a.slot + t * K + lane) : -1;
-            const float w = lane < K ? __ldg(a.topk_w + t * K + lane) : 0.0f;
+            float w = lane < K ? 1.0f : 0.0f;
+            if (lane < K && a.topk_w != nullptr) w = __ldg(a.topk_w + t * K + lane);
             if (s >= a.num_recv) {
                 set_status(a.status, EP_ERR_BAD_SLOT);
                 s = -1;

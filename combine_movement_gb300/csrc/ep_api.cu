@@ -262,6 +262,45 @@ int64_t dispatch_tail_units(const ep::DispatchArgs& a, int n, int sm_count, cuda
     return ring >= 2 * static_cast<int64_t>(n) * ep::dispatch_warps() ? tail : 0;
 }
 
+// Host checks shared by ep_combine, ep_dispatch_grad and ep_combine_grad:
+// `rows` in receive order, `tokens` in token order.
+ep_status_t check_combine(const uint16_t* rows, int64_t num_recv, const int32_t* slot, int64_t T,
+                          int64_t H, int K, const uint16_t* tokens, const int32_t* status) {
+    if (T < 0 || H <= 0 || H % 8 != 0 || K < 1 || K > EP_MAX_TOPK || num_recv < 0)
+        return EP_ERR_INVALID;
+    if (!pairs_fit(T, K) || num_recv > kMaxPairs || !row_fits(H)) return EP_ERR_UNSUPPORTED;
+    if (T == 0) return EP_OK;
+    if (slot == nullptr || tokens == nullptr || (num_recv > 0 && rows == nullptr))
+        return EP_ERR_INVALID;
+    if (!aligned(rows, 16) || !aligned(tokens, 16) || !aligned(slot, 4) || !aligned(status, 4))
+        return EP_ERR_INVALID;
+    return EP_OK;
+}
+
+// Combine, or with a null topk_w dispatch's gradient.
+ep_status_t run_combine(const uint16_t* rows, int64_t num_recv, const int32_t* slot,
+                        const float* topk_w, int64_t T, int64_t H, int K, uint16_t* y,
+                        int32_t* status, cudaStream_t stream) {
+    const ep::CallBytes call_bytes(T * K * 2 * H);
+    int sm_count = 0, smem_optin = 0;
+    if (!device_limits(&sm_count, &smem_optin)) return EP_ERR_CUDA;
+    ep::CombineArgs a{};
+    a.expert_out = reinterpret_cast<const uint8_t*>(rows);
+    a.num_recv = num_recv;
+    a.slot = slot;
+    a.topk_w = topk_w;
+    a.T = T;
+    a.row_bytes = static_cast<uint32_t>(H * 2);
+    a.K = K;
+    a.y = reinterpret_cast<uint8_t*>(y);
+    a.status = status;
+    const int n = sms_for_stream(sm_count, stream);
+    a.tail_percent = combine_tail_percent(T, H, K, n, sm_count, stream);
+    if (topk_w != nullptr && use_combine_tma(K, n))
+        return from_cuda(ep::launch_combine_tma(a, n, smem_optin, stream));
+    return from_cuda(ep::launch_combine(a, n, stream));
+}
+
 // Host checks shared by the experts' products. The tensor copies need 16-byte
 // aligned rows (K % 16) and address columns and weight rows with int32.
 ep_status_t check_expert(const uint8_t* a, const float* a_scale, int64_t num_recv,
@@ -533,34 +572,80 @@ ep_status_t ep_combine(const uint16_t* expert_out, int64_t num_recv, const int32
                        const float* topk_w, int64_t T, int64_t H, int K, uint16_t* y,
                        int32_t* status, void* stream) {
     ep::ApiRange range("ep_combine");
-    if (T < 0 || H <= 0 || H % 8 != 0 || K < 1 || K > EP_MAX_TOPK || num_recv < 0)
-        return EP_ERR_INVALID;
-    if (!pairs_fit(T, K) || num_recv > kMaxPairs || !row_fits(H)) return EP_ERR_UNSUPPORTED;
-    if (T == 0) return EP_OK;
-    if (slot == nullptr || topk_w == nullptr || y == nullptr ||
-        (num_recv > 0 && expert_out == nullptr))
-        return EP_ERR_INVALID;
-    if (!aligned(expert_out, 16) || !aligned(y, 16) || !aligned(slot, 4) || !aligned(topk_w, 4) ||
-        !aligned(status, 4))
+    const ep_status_t st = check_combine(expert_out, num_recv, slot, T, H, K, y, status);
+    if (st != EP_OK || T == 0) return st;
+    if (topk_w == nullptr || !aligned(topk_w, 4)) return EP_ERR_INVALID;
+    return run_combine(expert_out, num_recv, slot, topk_w, T, H, K, y, status,
+                       static_cast<cudaStream_t>(stream));
+}
+
+ep_status_t ep_dispatch_grad(const uint16_t* d_recv, int64_t num_recv, const int32_t* slot, int64_t T,
+                             int64_t H, int K, uint16_t* dx, int32_t* status, void* stream) {
+    ep::ApiRange range("ep_dispatch_grad");
+    const ep_status_t st = check_combine(d_recv, num_recv, slot, T, H, K, dx, status);
+    if (st != EP_OK || T == 0) return st;
+    return run_combine(d_recv, num_recv, slot, nullptr, T, H, K, dx, status,
+                       static_cast<cudaStream_t>(stream));
+}
+
+ep_status_t ep_combine_grad(const uint16_t* dy, const uint16_t* expert_out, int64_t num_recv,
+                            const int32_t* slot, const float* topk_w, int64_t T, int64_t H, int K,
+                            uint16_t* d_expert_out, float* d_topk_w, int32_t* status, void* stream) {
+    ep::ApiRange range("ep_combine_grad");
+    const ep_status_t st = check_combine(expert_out, num_recv, slot, T, H, K, dy, status);
+    if (st != EP_OK || T == 0) return st;
+    if (topk_w == nullptr || (d_expert_out == nullptr && d_topk_w == nullptr)) return EP_ERR_INVALID;
+    if (!aligned(topk_w, 4) || !aligned(d_expert_out, 16) || !aligned(d_topk_w, 4))
         return EP_ERR_INVALID;
     const ep::CallBytes call_bytes(T * K * 2 * H);
     int sm_count = 0, smem_optin = 0;
     if (!device_limits(&sm_count, &smem_optin)) return EP_ERR_CUDA;
-    ep::CombineArgs a{};
-    a.expert_out = reinterpret_cast<const uint8_t*>(expert_out);
+    ep::CombineGradArgs a{};
+    a.dy = dy;
+    a.expert_out = expert_out;
     a.num_recv = num_recv;
     a.slot = slot;
     a.topk_w = topk_w;
     a.T = T;
-    a.row_bytes = static_cast<uint32_t>(H * 2);
+    a.H = H;
     a.K = K;
-    a.y = reinterpret_cast<uint8_t*>(y);
+    a.d_expert_out = d_expert_out;
+    a.d_topk_w = d_topk_w;
     a.status = status;
-    const int n = sms_for_stream(sm_count, static_cast<cudaStream_t>(stream));
-    a.tail_percent = combine_tail_percent(T, H, K, n, sm_count, static_cast<cudaStream_t>(stream));
-    if (use_combine_tma(K, n))
-        return from_cuda(ep::launch_combine_tma(a, n, smem_optin, static_cast<cudaStream_t>(stream)));
-    return from_cuda(ep::launch_combine(a, n, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return from_cuda(ep::launch_combine_grad(a, sms_for_stream(sm_count, s), s));
+}
+
+ep_status_t ep_dispatch_fp8(const uint16_t* x, int64_t T, int64_t H, int K, const int32_t* slot,
+                            const float* topk_w, int64_t num_recv, uint8_t* recv_q,
+                            float* recv_scale, float* recv_w, int32_t* recv_src, int32_t* status,
+                            void* stream) {
+    ep::ApiRange range("ep_dispatch_fp8");
+    if (H % 16 != 0) return EP_ERR_INVALID;
+    const ep_status_t st =
+        check_dispatch(x, T, H, K, slot, topk_w, num_recv, reinterpret_cast<const uint16_t*>(recv_q),
+                       recv_w, recv_src, status);
+    if (st != EP_OK || T == 0) return st;
+    if ((num_recv > 0 && recv_scale == nullptr) || !aligned(recv_scale, 4)) return EP_ERR_INVALID;
+    const ep::CallBytes call_bytes(T * K * H);
+    int sm_count = 0, smem_optin = 0;
+    if (!device_limits(&sm_count, &smem_optin)) return EP_ERR_CUDA;
+    ep::DispatchFp8Args a{};
+    a.x = x;
+    a.T = T;
+    a.H = H;
+    a.K = K;
+    a.slot = slot;
+    a.topk_w = topk_w;
+    a.num_recv = num_recv;
+    a.recv_q = recv_q;
+    a.recv_scale = recv_scale;
+    a.blocks = (H + 127) / 128;
+    a.recv_w = recv_w;
+    a.recv_src = recv_src;
+    a.status = status;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return from_cuda(ep::launch_dispatch_fp8(a, sms_for_stream(sm_count, s), s));
 }
 
 ep_status_t ep_expert_matmul_fp8(const uint8_t* a, const float* a_scale, int64_t num_recv,

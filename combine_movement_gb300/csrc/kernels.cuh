@@ -164,13 +164,33 @@ int dispatch_ring_stages(bool fused, cudaStream_t stream);
 // Warps per dispatch CTA.
 int dispatch_warps();
 
+// ---- dispatch with quantised rows ------------------------------------------
+
+struct DispatchFp8Args {
+    const uint16_t* x;       // bf16 [T][H]
+    int64_t T;
+    int64_t H;
+    int K;
+    const int32_t* slot;
+    const float* topk_w;
+    int64_t num_recv;
+    uint8_t* recv_q;         // e4m3 [num_recv][H]
+    float* recv_scale;       // [num_recv][blocks]
+    int64_t blocks;          // ceil(H / 128)
+    float* recv_w;
+    int32_t* recv_src;
+    int32_t* status;
+};
+
+cudaError_t launch_dispatch_fp8(const DispatchFp8Args& a, int num_sms, cudaStream_t stream);
+
 // ---- combine --------------------------------------------------------------
 
 struct CombineArgs {
     const uint8_t* expert_out;
     int64_t num_recv;
     const int32_t* slot;
-    const float* topk_w;
+    const float* topk_w;  // null: every weight is 1 (dispatch's gradient)
     int64_t T;
     uint32_t row_bytes;
     int K;
@@ -189,6 +209,23 @@ struct CombineArgs {
 };
 
 cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t stream);
+
+// The gradient of combine (combine_grad.cu).
+struct CombineGradArgs {
+    const uint16_t* dy;          // bf16 [T][H]
+    const uint16_t* expert_out;  // bf16 [num_recv][H]
+    int64_t num_recv;
+    const int32_t* slot;
+    const float* topk_w;
+    int64_t T;
+    int64_t H;
+    int K;
+    uint16_t* d_expert_out;      // nullable
+    float* d_topk_w;             // nullable; then expert_out is not read
+    int32_t* status;
+};
+
+cudaError_t launch_combine_grad(const CombineGradArgs& a, int num_sms, cudaStream_t stream);
 
 // Combine with the expert rows staged through a per-warp bulk-copy ring
 // (combine_tma.cu); K <= 8 only.

@@ -109,6 +109,12 @@ def _load() -> ctypes.CDLL:
     lib.ep_combine.restype = i32
     lib.ep_get_dispatch_layout_noalloc.argtypes = [p, i64, i32, i32, p, p, p, p, p]
     lib.ep_get_dispatch_layout_noalloc.restype = i32
+    lib.ep_dispatch_fp8.argtypes = [p, i64, i64, i32, p, p, i64, p, p, p, p, p, p]
+    lib.ep_dispatch_fp8.restype = i32
+    lib.ep_combine_grad.argtypes = [p, p, i64, p, p, i64, i64, i32, p, p, p, p]
+    lib.ep_combine_grad.restype = i32
+    lib.ep_dispatch_grad.argtypes = [p, i64, p, i64, i64, i32, p, p, p]
+    lib.ep_dispatch_grad.restype = i32
     lib.ep_expert_matmul_fp8.argtypes = [p, p, i64, p, i32, p, p, i64, i64, p, p, p]
     lib.ep_expert_matmul_fp8.restype = i32
     lib.ep_expert_gate_up_fp8.argtypes = [p, p, i64, p, i32, p, p, i64, i64, p, p, p, p]
@@ -315,6 +321,59 @@ def _shape(t: torch.Tensor, shape: Tuple[int, ...], what: str) -> None:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
 
 
+def ep_dispatch_fp8(x: torch.Tensor, slot: torch.Tensor, recv_q: torch.Tensor,
+                    recv_scale: torch.Tensor, topk_w: Optional[torch.Tensor] = None,
+                    recv_w: Optional[torch.Tensor] = None,
+                    recv_src: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None) -> None:
+    T, H = x.shape
+    K, R = slot.shape[1], recv_q.shape[0]
+    _shape(slot, (T, K), "slot")
+    _shape(recv_q, (R, H), "recv_q")
+    _shape(recv_scale, (R, -(-H // FP8_BLOCK)), "recv_scale")
+    code = lib.ep_dispatch_fp8(
+        _ptr(x, torch.bfloat16, "x"), T, H, K, _ptr(slot, torch.int32, "slot"),
+        _ptr(topk_w, torch.float32, "topk_w"), R, _ptr(recv_q, torch.float8_e4m3fn, "recv_q"),
+        _ptr(recv_scale, torch.float32, "recv_scale"), _ptr(recv_w, torch.float32, "recv_w"),
+        _ptr(recv_src, torch.int32, "recv_src"), _ptr(status, torch.int32, "status"),
+        _stream(stream))
+    _check(code, "ep_dispatch_fp8")
+
+
+def ep_combine_grad(dy: torch.Tensor, expert_out: torch.Tensor, slot: torch.Tensor,
+                    topk_w: torch.Tensor, d_expert_out: Optional[torch.Tensor],
+                    d_topk_w: Optional[torch.Tensor], status: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    T, H = dy.shape
+    K, R = slot.shape[1], expert_out.shape[0]
+    _shape(expert_out, (R, H), "expert_out")
+    _shape(slot, (T, K), "slot")
+    _shape(topk_w, (T, K), "topk_w")
+    if d_expert_out is not None:
+        _shape(d_expert_out, (R, H), "d_expert_out")
+    if d_topk_w is not None:
+        _shape(d_topk_w, (T, K), "d_topk_w")
+    code = lib.ep_combine_grad(
+        _ptr(dy, torch.bfloat16, "dy"), _ptr(expert_out, torch.bfloat16, "expert_out"), R,
+        _ptr(slot, torch.int32, "slot"), _ptr(topk_w, torch.float32, "topk_w"), T, H, K,
+        _ptr(d_expert_out, torch.bfloat16, "d_expert_out"),
+        _ptr(d_topk_w, torch.float32, "d_topk_w"), _ptr(status, torch.int32, "status"),
+        _stream(stream))
+    _check(code, "ep_combine_grad")
+
+
+def ep_dispatch_grad(d_recv: torch.Tensor, slot: torch.Tensor, dx: torch.Tensor,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    T, H = dx.shape
+    K, R = slot.shape[1], d_recv.shape[0]
+    _shape(d_recv, (R, H), "d_recv")
+    _shape(slot, (T, K), "slot")
+    code = lib.ep_dispatch_grad(
+        _ptr(d_recv, torch.bfloat16, "d_recv"), R, _ptr(slot, torch.int32, "slot"), T, H, K,
+        _ptr(dx, torch.bfloat16, "dx"), _ptr(status, torch.int32, "status"), _stream(stream))
+    _check(code, "ep_dispatch_grad")
+
+
 def _expert_operands(a, a_scale, offsets, w, w_scale):
     """Checks the operands of an expert product against each other and
     returns (num_recv, E, rows of w, K)."""
@@ -415,6 +474,41 @@ def combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tensor,
     y = torch.empty((T, expert_out.shape[1]), dtype=expert_out.dtype, device=expert_out.device)
     ep_combine(expert_out, slot, topk_w, y, status, stream)
     return y
+
+
+def dispatch_fp8(x: torch.Tensor, slot: torch.Tensor, num_recv: int,
+                 topk_w: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                 stream=None):
+    """Returns recv_q [num_recv, H] (e4m3) and recv_scale [num_recv, ceil(H / 128)]
+    (and recv_w, recv_src when topk_w is given)."""
+    H, dev = x.shape[1], x.device
+    recv_q = torch.empty((num_recv, H), dtype=torch.float8_e4m3fn, device=dev)
+    recv_scale = torch.empty((num_recv, -(-H // FP8_BLOCK)), dtype=torch.float32, device=dev)
+    recv_w = recv_src = None
+    if topk_w is not None:
+        recv_w = torch.empty(num_recv, dtype=torch.float32, device=dev)
+        recv_src = torch.empty(num_recv, dtype=torch.int32, device=dev)
+    ep_dispatch_fp8(x, slot, recv_q, recv_scale, topk_w, recv_w, recv_src, status, stream)
+    return (recv_q, recv_scale) if topk_w is None else (recv_q, recv_scale, recv_w, recv_src)
+
+
+def combine_grad(dy: torch.Tensor, expert_out: torch.Tensor, slot: torch.Tensor,
+                 topk_w: torch.Tensor, status: Optional[torch.Tensor] = None, stream=None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Returns (d_expert_out [num_recv, H], d_topk_w [T, K]). Rows no entry
+    maps to are left as allocated."""
+    d_expert_out = torch.empty_like(expert_out)
+    d_topk_w = torch.empty_like(topk_w)
+    ep_combine_grad(dy, expert_out, slot, topk_w, d_expert_out, d_topk_w, status, stream)
+    return d_expert_out, d_topk_w
+
+
+def dispatch_grad(d_recv: torch.Tensor, slot: torch.Tensor, status: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Returns dx [T, H], each token's receive-row gradients summed."""
+    dx = torch.empty((slot.shape[0], d_recv.shape[1]), dtype=d_recv.dtype, device=d_recv.device)
+    ep_dispatch_grad(d_recv, slot, dx, status, stream)
+    return dx
 
 
 def expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor,

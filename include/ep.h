@@ -284,6 +284,33 @@ EP_API ep_status_t ep_combine(const uint16_t* expert_out, int64_t num_recv,
                        int64_t T, int64_t H, int K,
                        uint16_t* y, int32_t* status, void* stream);
 
+/* ---- gradients of the movement ------------------------------------------------
+ * For training through dispatch and combine (the pages cover the forward
+ * movement only). Both run on the SM budget like dispatch and combine. */
+
+/* The gradient of ep_combine, given the gradient dy of y:
+ *   d_expert_out[slot[t,k], :] = bf16_rne( topk_w[t,k] * dy[t, :] )
+ *   d_topk_w[t,k] = sum over h of dy[t,h] * expert_out[slot[t,k], h]  (fp32)
+ *   dy            bf16 [T][H]          expert_out    bf16 [num_recv][H]
+ *   d_expert_out  bf16 [num_recv][H]   d_topk_w      fp32 [T][K]
+ * Either output may be null (not both). Masked entries get d_topk_w = 0;
+ * rows of d_expert_out no entry maps to are left untouched. The same inputs
+ * and SM budget give the same bits every time. */
+EP_API ep_status_t ep_combine_grad(const uint16_t* dy, const uint16_t* expert_out, int64_t num_recv,
+                                   const int32_t* slot, const float* topk_w, int64_t T, int64_t H,
+                                   int K, uint16_t* d_expert_out, float* d_topk_w, int32_t* status,
+                                   void* stream);
+
+/* The gradient of ep_dispatch, given the gradient d_recv of recv_x:
+ *   dx[t, :] = bf16_rne( sum over k = 0..K-1, in that order, in fp32, of
+ *              d_recv[slot[t,k], :] )
+ *   d_recv  bf16 [num_recv][H]         dx  bf16 [T][H]
+ * Masked entries contribute nothing; a token without entries gets +0.0. (It
+ * is ep_combine with every weight 1.) */
+EP_API ep_status_t ep_dispatch_grad(const uint16_t* d_recv, int64_t num_recv, const int32_t* slot,
+                                    int64_t T, int64_t H, int K, uint16_t* dx, int32_t* status,
+                                    void* stream);
+
 /* ---- the experts, in 8 bits --------------------------------------------------
  * Rows and weights as e4m3 bytes with one fp32 scale for each block of 128
  * values, so that value = byte * scale: rows in blocks of 1 x 128 along
@@ -291,6 +318,21 @@ EP_API ep_status_t ep_combine(const uint16_t* expert_out, int64_t num_recv,
  * 128 x 128. Row r belongs to expert e where offsets[e] <= r < offsets[e+1]
  * (offsets of the layout calls); rows from offsets[E] on are neither used nor
  * written. The pages have no counterpart: they end where the rows arrive. */
+
+/* Dispatch with the rows quantised on the way: for every block of 128 columns
+ * of a token row,
+ *   m = max(max |x| of the block, 1e-30)   scale = m / 448
+ *   q = e4m3_rne(x * (448 / m))
+ * and recv_q[slot[t,k], :] = q, recv_scale[slot[t,k], :] = the row's scales.
+ *   x           bf16 [T][H]            recv_q      e4m3 [num_recv][H]
+ *   recv_scale  fp32 [num_recv][ceil(H/128)]
+ * H a multiple of 16. The other arguments, the SM budget and what is left
+ * untouched are as for ep_dispatch. A block that holds an infinity or NaN
+ * gets a scale that is not finite. */
+EP_API ep_status_t ep_dispatch_fp8(const uint16_t* x, int64_t T, int64_t H, int K,
+                                   const int32_t* slot, const float* topk_w, int64_t num_recv,
+                                   uint8_t* recv_q, float* recv_scale, float* recv_w,
+                                   int32_t* recv_src, int32_t* status, void* stream);
 
 /* The experts' product:
  *   out[r, n] = bf16_rne( sum over blocks b of a_scale[r,b] *
