@@ -6,9 +6,16 @@
 // columns of one token: a lane takes 16 columns (two 16-byte loads), eight
 // lanes a block, whose maximum goes round by three shuffles; each lane then
 // stores its 16 bytes to each of the K receive rows, 512 contiguous bytes a
-// warp. Units are split evenly over the warps of one CTA per SM of the budget.
+// warp.
 //
-// Bound by the writes: T = 4096, H = 7168, top-8 moves 301 MB.
+// On the whole GPU a unit goes to a warp of a small CTA, and the SMs that
+// finish first take the next CTAs; on a smaller SM budget (one CTA per SM of
+// it) the units are split evenly over the warps of the budget.
+//
+// Bound by the writes: T = 4096, H = 7168, top-8 moves 301 MB (a fifth of it reads) in
+// 46.6 us, 6.5 TB/s, 0.95 of a plain copy's rate; with one CTA per SM it took
+// 54 us (some SMs write a quarter slower than others), with two or four units
+// to a warp 50 and 53 us. T = 128: about the launch, 7 us.
 #include <cuda_runtime.h>
 
 #include "../../include/ep.h"
@@ -22,8 +29,10 @@ namespace {
 
 constexpr unsigned kFullMask = 0xFFFFFFFFu;
 constexpr int kThreads = 1024;
+constexpr int kSmallThreads = 256;
 constexpr int kLaneCols = 16;
 constexpr int kWarpCols = 32 * kLaneCols;
+constexpr int64_t kMaxGrid = 0x7FFFFFFF;
 constexpr int kBlockLanes = kFp8Block / kLaneCols;
 
 // The two bf16 values of a word, widened exactly.
@@ -39,8 +48,8 @@ __global__ void __launch_bounds__(kThreads, 1) dispatch_fp8_kernel(const Dispatc
     constexpr int kUnitCols = kParts * kWarpCols;
     const int64_t n_units = (a.H + kUnitCols - 1) / kUnitCols;  // of a row
     const int64_t units = a.T * n_units;
-    const int64_t gw = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp;
-    const int64_t nw = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
+    const int64_t gw = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp;
+    const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
     const int64_t u0 = split_begin(units, gw, nw), u1 = split_begin(units, gw + 1, nw);
     int64_t t = div_floor(u0, n_units);
     int64_t part = u0 - t * n_units;
@@ -112,8 +121,14 @@ __global__ void __launch_bounds__(kThreads, 1) dispatch_fp8_kernel(const Dispatc
 template <int kParts>
 cudaError_t launch_parts(const DispatchFp8Args& a, int num_sms, cudaStream_t stream) {
     const int64_t units = a.T * ((a.H + kParts * kWarpCols - 1) / (kParts * kWarpCols));
-    const int64_t ctas = (units + kThreads / 32 - 1) / (kThreads / 32);
     auto kern = dispatch_fp8_kernel<kParts>;
+    if (a.whole_gpu) {  // a unit to a warp
+        constexpr int64_t kPer = kSmallThreads / 32;
+        if (units <= kMaxGrid * kPer)
+            return launch_dependent(kern, static_cast<int>((units + kPer - 1) / kPer), kSmallThreads,
+                                    0, stream, a);
+    }
+    const int64_t ctas = (units + kThreads / 32 - 1) / (kThreads / 32);
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(kExclusiveSmem));
     if (err != cudaSuccess) return err;
@@ -124,7 +139,7 @@ cudaError_t launch_parts(const DispatchFp8Args& a, int num_sms, cudaStream_t str
 }  // namespace
 
 cudaError_t launch_dispatch_fp8(const DispatchFp8Args& a, int num_sms, cudaStream_t stream) {
-    // wide units where every warp still gets two of them
+    // wide units (more loads in flight) where every warp still gets two of them
     const int64_t wide = a.T * ((a.H + 2 * kWarpCols - 1) / (2 * kWarpCols));
     if (wide >= 2ll * num_sms * (kThreads / 32)) return launch_parts<2>(a, num_sms, stream);
     return launch_parts<1>(a, num_sms, stream);

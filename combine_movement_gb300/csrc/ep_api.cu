@@ -613,7 +613,9 @@ ep_status_t ep_combine_grad(const uint16_t* dy, const uint16_t* expert_out, int6
     a.d_topk_w = d_topk_w;
     a.status = status;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return from_cuda(ep::launch_combine_grad(a, sms_for_stream(sm_count, s), s));
+    const int n = sms_for_stream(sm_count, s);
+    a.whole_gpu = n >= sm_count;
+    return from_cuda(ep::launch_combine_grad(a, n, s));
 }
 
 ep_status_t ep_dispatch_fp8(const uint16_t* x, int64_t T, int64_t H, int K, const int32_t* slot,
@@ -645,7 +647,9 @@ ep_status_t ep_dispatch_fp8(const uint16_t* x, int64_t T, int64_t H, int K, cons
     a.recv_src = recv_src;
     a.status = status;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return from_cuda(ep::launch_dispatch_fp8(a, sms_for_stream(sm_count, s), s));
+    const int n = sms_for_stream(sm_count, s);
+    a.whole_gpu = n >= sm_count;
+    return from_cuda(ep::launch_dispatch_fp8(a, n, s));
 }
 
 ep_status_t ep_expert_matmul_fp8(const uint8_t* a, const float* a_scale, int64_t num_recv,

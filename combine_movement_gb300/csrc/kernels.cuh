@@ -180,6 +180,7 @@ struct DispatchFp8Args {
     float* recv_w;
     int32_t* recv_src;
     int32_t* status;
+    bool whole_gpu;          // the budget covers every SM of the device
 };
 
 cudaError_t launch_dispatch_fp8(const DispatchFp8Args& a, int num_sms, cudaStream_t stream);
@@ -223,6 +224,7 @@ struct CombineGradArgs {
     uint16_t* d_expert_out;      // nullable
     float* d_topk_w;             // nullable; then expert_out is not read
     int32_t* status;
+    bool whole_gpu;              // the budget covers every SM of the device
 };
 
 cudaError_t launch_combine_grad(const CombineGradArgs& a, int num_sms, cudaStream_t stream);
