@@ -7,7 +7,7 @@ library and raises if it is missing: there is no CPU fallback.
 """
 import importlib
 
-__all__ = ["ep", "workloads"]
+__all__ = ["ep", "moe", "workloads"]
 
 
 def __getattr__(name):

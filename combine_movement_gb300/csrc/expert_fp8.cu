@@ -327,16 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t done_h = done + 8 * kStages * h, read_h = sums_read + 8 * kSlots * h;
             Ring<kStages> st;
             Ring<kSlots> slot;
-            Ring<kScaleGroups> group;
             bool ok = true;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 for (int kb = 0; kb < kb_count; ++kb, st.next(), slot.next()) {
-                    // (the adding warps need the scales, and wait for this product only)
-                    if (kb % kScaleGroup == 0) {
-                        ok = warp_wait(scales + 8 * group.i, group.round, abort, a.status);
-                        if (!ok) break;
-                        group.next();
-                    }
                     ok = warp_wait(full + 8 * st.i, st.round, abort, a.status) &&
                          warp_wait(read_h + 8 * slot.i, slot.round ^ 1u, abort, a.status);
                     if (!ok) break;
@@ -410,19 +403,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 1706 us instead of 1377), and after a wait that gave up the rest of
             // the tile runs on without waiting or arriving.
             for (int kb0 = 0; kb0 < kb_count; kb0 += kScaleGroup, group.next()) {
+                ok = ok && warp_wait(scales + 8 * group.i, group.round, abort, a.status);
                 uint32_t row_at = row_scale + group.i * sizeof(ctl.row_scale[0]);
                 uint32_t weight_at = weight_scale + group.i * sizeof(ctl.weight_scale[0]);
                 const int kb1 = min(kb0 + kScaleGroup, kb_count);
 #pragma unroll 1
                 for (int kb = kb0; kb < kb1; ++kb) {
+                    const float sa = load_shared_f32(row_at);
+                    const float2 sw = load_shared_f32x2(weight_at);
+                    const float s0 = sa * sw.x, s1 = sa * sw.y;
                     ok = ok && warp_wait(done_h + 8 * st.i, st.round, abort, a.status);
                     st.next();
                     tcgen05_fence_after();
                     uint32_t v[16];
                     tmem_load16(sums, v);
-                    const float sa = load_shared_f32(row_at);
-                    const float2 sw = load_shared_f32x2(weight_at);
-                    const float s0 = sa * sw.x, s1 = sa * sw.y;
                     tmem_load_wait16(v);
                     add_scaled(acc[0], 0, v, s0);
                     tmem_load16(sums + 16, v);
