@@ -75,6 +75,13 @@ constexpr int kRowBoxes = 4;                   // row boxes of 16, 32, 64, 128
 // their own between the scale warp and the adding warps.
 constexpr int kScaleGroup = 4;
 constexpr int kScaleGroups = 4;
+// With a tile's first group goes what the adding warps need to know of the
+// tile when they write it. The scale warp is at most kScaleGroups groups, and
+// so tiles, ahead of the last adding warp.
+constexpr int kTileNotes = 2 * kScaleGroups;
+struct TileNote {
+    int row0, rows, col_tile;
+};
 
 struct Maps {
     CUtensorMap rows[kRowBoxes];
@@ -84,7 +91,7 @@ struct Maps {
 struct Control {
     uint64_t full[kStages];       // the copies have landed
     uint64_t done[2][kStages];    // the stage's product of a half is done: its sums are there
-    uint64_t scales[kScaleGroups];       // a group has landed: the scale warp's lanes
+    uint64_t scales[kScaleGroups];       // a group has landed: the scale warp's lanes, and its note
     uint64_t scales_read[kScaleGroups];  // and has been read: the adding warps
     alignas(16) uint64_t sums_read[2][kSlots];
     uint64_t joined;       // accumulating warps, once per tile
@@ -92,6 +99,7 @@ struct Control {
     uint32_t tmem;
     int32_t abort;
     int32_t warp_sum[32];
+    TileNote notes[kTileNotes];
     uint32_t amax[2][kAccGroups][kTileRows];
     float row_scale[kScaleGroups][kScaleGroup][kTileRows];
     alignas(8) float weight_scale[kScaleGroups][kScaleGroup][2];
@@ -215,6 +223,31 @@ __device__ __forceinline__ void add_scaled(float (&acc)[kAccCols], int i0, const
     }
 }
 
+// p[i] of lane j <-> p[j] of lane i, i and j within each four lanes; `j` is
+// lane mod 4.
+__device__ __forceinline__ void transpose4(uint4 (&p)[4], int j) {
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+        // exchange the halves that differ in bit d of both i and j
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & d) continue;
+            uint4& low = p[i];
+            uint4& high = p[i + d];
+            const bool up = (j & d) != 0;
+            uint4 give = up ? low : high;
+            give.x = __shfl_xor_sync(0xFFFFFFFFu, give.x, d);
+            give.y = __shfl_xor_sync(0xFFFFFFFFu, give.y, d);
+            give.z = __shfl_xor_sync(0xFFFFFFFFu, give.z, d);
+            give.w = __shfl_xor_sync(0xFFFFFFFFu, give.w, d);
+            if (up)
+                low = give;
+            else
+                high = give;
+        }
+    }
+}
+
 template <bool kGateUp>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_kernel(const ExpertArgs a, const __grid_constant__ Maps maps) {
@@ -238,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(done + 8 * (kStages + i), 1);
         }
         for (int i = 0; i < kScaleGroups; ++i) {
-            mbar_init(scales + 8 * i, 32);
+            mbar_init(scales + 8 * i, 32 + 1);
             mbar_init(scales_read + 8 * i, kAccWarps);
         }
         for (int i = 0; i < 2 * kSlots; ++i) mbar_init(sums_read + 8 * i, kAccWarps / 2);
@@ -351,8 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n_blocks = (a.n + kFp8Block - 1) / kFp8Block;
             const uint32_t row_dst = smem_u32(&ctl.row_scale[0][0][lane]);
             Ring<kScaleGroups> group;
+            uint32_t tile_no = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
                 const Tile tile = find_tile(t, cum, a);
                 const int b0 = kGateUp ? tile.col_tile : 2 * tile.col_tile;
                 const int b1 = kGateUp ? b0 + n_blocks / 2 : min(b0 + 1, n_blocks - 1);
@@ -376,6 +410,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         copy_async4(smem_u32(&ctl.weight_scale[group.i][j][lane & 1]), weight + kb0 + j);
                     }
                     copy_async_arrive(scales + 8 * group.i);
+                    if (lane == 0) {
+                        if (kb0 == 0)
+                            ctl.notes[tile_no % kTileNotes] = {tile.row0, tile.rows, tile.col_tile};
+                        mbar_arrive(scales + 8 * group.i);  // (releases the note)
+                    }
                 }
             }
             copy_async_wait_all();
@@ -439,8 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_if(scales_read + 8 * group.i, ok && lane == 0);
             }
             if (!ok) break;
-            // (looked up again rather than kept in registers through the sums)
-            const Tile tile = find_tile(t, cum, a);
+            const TileNote tile = ctl.notes[tile_no % kTileNotes];
             const int row = quarter * 32 + lane;
             const bool store = row < tile.rows;
             const int64_t grow = tile.row0 + row;
@@ -485,19 +523,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (c == 0) a.out_scale[grow * (width / kFp8Block) + tile.col_tile] = bs.scale;
                 }
-            } else if (store) {
-                const int64_t col0 = static_cast<int64_t>(tile.col_tile) * kTileCols + c * kAccCols;
+            } else {
+                // A lane holds 64 bytes of one row and block. Four lanes exchange
+                // 16-byte pieces first, so that a store covers 64 contiguous
+                // bytes of eight rows instead of 16 of 32: its cost goes by rows.
+                const int piece = lane & 3;
+                const int64_t col0 =
+                    static_cast<int64_t>(tile.col_tile) * kTileCols + c * kAccCols + piece * 8;
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b) {
+                    uint4 p[4];
 #pragma unroll
-                    for (int i = 0; i < kAccCols / 8; ++i) {
-                        const int64_t col = col0 + b * kFp8Block + i * 8;
+                    for (int i = 0; i < 4; ++i) {
                         const float* f = &acc[b][i * 8];
-                        if (col < a.n)
-                            st_v4(a.out + grow * a.n + col,
-                                  make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                             pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+                        p[i] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                          pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
                     }
+                    transpose4(p, piece);
+                    const int64_t col = col0 + b * kFp8Block;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = quarter * 32 + (lane & ~3) + i;
+                        if (r < tile.rows && col < a.n)
+                            st_v4(a.out + (tile.row0 + static_cast<int64_t>(r)) * a.n + col, p[i]);
+                    }
+                }
             }
         }
     }
