@@ -305,10 +305,10 @@ ep_status_t run_combine(const uint16_t* rows, int64_t num_recv, const int32_t* s
 // aligned rows (K % 16) and address columns and weight rows with int32.
 ep_status_t check_expert(const uint8_t* a, const float* a_scale, int64_t num_recv,
                          const int32_t* offsets, int E, const uint8_t* w, const float* w_scale,
-                         int64_t N, int64_t K, const int32_t* status) {
+                         int64_t N, int64_t K, bool gated, const int32_t* status) {
     if (num_recv < 0 || E < 1 || K <= 0 || K % 16 != 0) return EP_ERR_INVALID;
     if (E > EP_MAX_EXPERTS || num_recv > kMaxPairs || K > kMaxPairs - 128 ||
-        N > (kMaxPairs - 256) / E)
+        N > (kMaxPairs - 256) / E || ep::expert_tiles_bound(num_recv, E, N, gated) > ep::kMaxTiles)
         return EP_ERR_UNSUPPORTED;
     if (num_recv == 0) return EP_OK;
     if (a == nullptr || a_scale == nullptr || offsets == nullptr || w == nullptr || w_scale == nullptr)
@@ -658,7 +658,8 @@ ep_status_t ep_expert_matmul_fp8(const uint8_t* a, const float* a_scale, int64_t
                                  int32_t* status, void* stream) {
     ep::ApiRange range("ep_expert_matmul_fp8");
     if (N <= 0 || N % 8 != 0) return EP_ERR_INVALID;
-    const ep_status_t st = check_expert(a, a_scale, num_recv, offsets, E, w, w_scale, N, K, status);
+    const ep_status_t st =
+        check_expert(a, a_scale, num_recv, offsets, E, w, w_scale, N, K, false, status);
     if (st != EP_OK || num_recv == 0) return st;
     if (out == nullptr || !aligned(out, 16)) return EP_ERR_INVALID;
     ep::ExpertArgs x = expert_args(a, a_scale, num_recv, offsets, E, w, w_scale, N, K, status);
@@ -673,7 +674,8 @@ ep_status_t ep_expert_gate_up_fp8(const uint8_t* a, const float* a_scale, int64_
     ep::ApiRange range("ep_expert_gate_up_fp8");
     if (I <= 0 || I % 128 != 0) return EP_ERR_INVALID;
     if (I > kMaxPairs / 2) return EP_ERR_UNSUPPORTED;
-    const ep_status_t st = check_expert(a, a_scale, num_recv, offsets, E, w, w_scale, 2 * I, K, status);
+    const ep_status_t st =
+        check_expert(a, a_scale, num_recv, offsets, E, w, w_scale, 2 * I, K, true, status);
     if (st != EP_OK || num_recv == 0) return st;
     if (out_q == nullptr || out_scale == nullptr || !aligned(out_q, 16) || !aligned(out_scale, 4))
         return EP_ERR_INVALID;

@@ -41,6 +41,7 @@
 #include "combine_math.cuh"
 #include "fp8_math.cuh"
 #include "kernels.cuh"
+#include "routing.cuh"
 #include "tcgen05.cuh"
 
 namespace ep {
@@ -64,10 +65,10 @@ constexpr int kCopyWarp = kAccWarps + 2, kScaleWarp = kAccWarps + 3;
 constexpr int kThreads = (kAccWarps + 4) * 32;
 // Registers per thread: the launch's 96 (640 threads) move from the last
 // warpgroup to the four that hold the sums: 512 x 104 + 128 x 64 = 640 x 96.
-constexpr int kAccRegs = 104, kOtherRegs = 64;
-static_assert(kAccWarps * 32 * kAccRegs + 128 * kOtherRegs <= kThreads * 96, "register split");
+constexpr int kAccRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
+static_assert(kAccWarps * 32 * kAccRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs,
+              "register split");
 constexpr uint32_t kTmemCols = kSlots * kTileCols;
-constexpr unsigned kPatienceNs = 100;
 constexpr int kRowBoxes = 4;                   // row boxes of 16, 32, 64, 128
 
 // Scales: of the CTA's 128 rows and of the two weight blocks, for kScaleGroup
@@ -98,7 +99,6 @@ struct Control {
     uint64_t drained[2];   // after an abort: products still in flight
     uint32_t tmem;
     int32_t abort;
-    int32_t warp_sum[32];
     TileNote notes[kTileNotes];
     uint32_t amax[2][kAccGroups][kTileRows];
     float row_scale[kScaleGroups][kScaleGroup][kTileRows];
@@ -126,16 +126,11 @@ __device__ __forceinline__ void store_shared(uint32_t addr, uint32_t v) {
 
 // Wait of a whole warp on a barrier; false, in every lane, once a lane gave up
 // after kWaitLimitNs or another warp did (the word at `abort`). The timer is
-// slow to read, so the first tries go without. A patient wait, for the warps
-// that run ahead of the products, sleeps between its tries: asking on takes
-// issue slots from the adding warps.
-template <bool kPatient>
+// slow to read, so the first tries go without.
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort,
                                           int32_t* status) {
-    for (int i = 0; i < 256; ++i) {
-        if (kPatient) __nanosleep(kPatienceNs);
+    for (int i = 0; i < 256; ++i)
         if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    }
     const uint64_t t0 = global_timer_ns();
     while (true) {
         if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
@@ -147,11 +142,10 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_
         if (__any_sync(0xFFFFFFFFu, late || load_shared(abort) != 0)) return false;
     }
 }
-template <bool kPatient = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort,
                                           int32_t* status) {
     if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    return wait_slow<kPatient>(bar, parity, abort, status);
+    return wait_slow(bar, parity, abort, status);
 }
 
 // Position in a ring of N: index, and the parity of its current round.
@@ -174,6 +168,10 @@ struct Tile {
     int rows;   // 1 .. 128
 };
 
+__device__ __forceinline__ uint32_t row_tiles_of(int rows) {
+    return (static_cast<uint32_t>(rows) + kTileRows - 1) / kTileRows;
+}
+
 // The tiles of expert e are cum[e] .. cum[e + 1], row tiles innermost: tiles
 // that read the same weights run at the same time.
 __device__ __forceinline__ Tile find_tile(int t, const int32_t* cum, const ExpertArgs& a) {
@@ -186,7 +184,7 @@ __device__ __forceinline__ Tile find_tile(int t, const int32_t* cum, const Exper
             hi = mid;
     }
     const int begin = __ldg(a.offsets + lo), end = __ldg(a.offsets + lo + 1);
-    const uint32_t local = t - cum[lo], row_tiles = (end - begin + kTileRows - 1) / kTileRows;
+    const uint32_t local = t - cum[lo], row_tiles = row_tiles_of(end - begin);
     Tile tile;
     tile.expert = lo;
     tile.col_tile = static_cast<int>(local / row_tiles);
@@ -207,8 +205,10 @@ __device__ __forceinline__ int expert_rows(int e, const ExpertArgs& a) {
     return end - begin;
 }
 
-// acc[i0 ..] += s * v for 16 columns, two to an instruction (each rounded as by
-// fmaf; the pairs take as long as single fmas, and half the issue slots).
+// acc[i0 ..] += s * v for 16 columns, two to an instruction, each rounded as by
+// fmaf. (A pair takes three cycles of the fma pipe, two single fmas two; but it
+// takes one issue slot instead of two, and the four warps of a scheduler come
+// to more issue slots than the block's products leave them: 5 % faster.)
 __device__ __forceinline__ void add_scaled(float (&acc)[kAccCols], int i0, const uint32_t (&v)[16],
                                            float s) {
     uint64_t s2;
@@ -289,27 +289,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     griddep_launch_dependents();
 
-    // cum[e] = tiles of the experts before e
+    // cum[e] = tiles of the experts before e. (The host lets kMaxTiles through
+    // at most for offsets that ascend; others may claim rows twice and come to
+    // more, which is refused here.)
     {
         const int per = (a.E + kThreads - 1) / kThreads;
         const int e0 = min(static_cast<int>(threadIdx.x) * per, a.E), e1 = min(e0 + per, a.E);
-        int mine = 0;
-        for (int e = e0; e < e1; ++e) mine += (expert_rows(e, a) + kTileRows - 1) / kTileRows * a.col_tiles;
-        int incl = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-            if (lane >= d) incl += o;
-        }
-        if (lane == 31) ctl.warp_sum[warp] = incl;
-        __syncthreads();
-        int run = incl - mine;
-        for (int w = 0; w < warp; ++w) run += ctl.warp_sum[w];
+        int64_t mine = 0, total = 0;
+        for (int e = e0; e < e1; ++e)
+            mine += static_cast<int64_t>(row_tiles_of(expert_rows(e, a))) * a.col_tiles;
+        int64_t run = block_exclusive_scan(mine, &total);
         for (int e = e0; e < e1; ++e) {
-            cum[e] = run;
-            run += (expert_rows(e, a) + kTileRows - 1) / kTileRows * a.col_tiles;
+            cum[e] = static_cast<int32_t>(min(run, static_cast<int64_t>(kMaxTiles)));
+            run += static_cast<int64_t>(row_tiles_of(expert_rows(e, a))) * a.col_tiles;
         }
-        if (threadIdx.x == kThreads - 1) cum[a.E] = run;
+        if (threadIdx.x == 0) {
+            cum[a.E] = total <= kMaxTiles ? static_cast<int32_t>(total) : 0;
+            if (total > kMaxTiles) set_status(a.status, EP_ERR_BAD_SLOT);
+        }
     }
     tcgen05_fence_before();
     __syncthreads();
@@ -335,8 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kb = 0; kb < kb_count; ++kb, st.next(), ++fills) {
 #pragma unroll 1
                     for (int h = 0; ok && h < 2; ++h)  // both halves are done with the stage
-                        ok = warp_wait<true>(done + 8 * (h * kStages + st.i), st.round ^ 1u, abort,
-                                             a.status);
+                        ok = warp_wait(done + 8 * (h * kStages + st.i), st.round ^ 1u, abort, a.status);
                     if (!ok) break;
                     if (elect_one()) {
                         // rows, then each half's pieces of both weight blocks
@@ -391,12 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int b0 = kGateUp ? tile.col_tile : 2 * tile.col_tile;
                 const int b1 = kGateUp ? b0 + n_blocks / 2 : min(b0 + 1, n_blocks - 1);
                 const int rows = tile.rows;
-                const float* row = a.a_scale + static_cast<int64_t>(tile.row0 + lane) * kb_count;
+                const float* row = a.a_scale + (static_cast<int64_t>(tile.row0) + lane) * kb_count;
                 const float* weight =
                     a.w_scale +
                     (static_cast<int64_t>(tile.expert) * n_blocks + ((lane & 1) == 0 ? b0 : b1)) * kb_count;
                 for (int kb0 = 0; kb0 < kb_count; kb0 += kScaleGroup, group.next()) {
-                    ok = warp_wait<true>(scales_read + 8 * group.i, group.round ^ 1u, abort, a.status);
+                    ok = warp_wait(scales_read + 8 * group.i, group.round ^ 1u, abort, a.status);
                     if (!ok) break;
                     const int count = min(kScaleGroup, kb_count - kb0);
                     uint32_t dst = row_dst + group.i * sizeof(ctl.row_scale[0]);
@@ -481,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const TileNote tile = ctl.notes[tile_no % kTileNotes];
             const int row = quarter * 32 + lane;
             const bool store = row < tile.rows;
-            const int64_t grow = tile.row0 + row;
+            const int64_t grow = static_cast<int64_t>(tile.row0) + row;
             if (kGateUp) {
                 // Approximate exponential and division: off by a few units of
                 // 2^-24 (and |g| of them for the exponential), well inside what
@@ -545,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) {
                         const int r = quarter * 32 + (lane & ~3) + i;
                         if (r < tile.rows && col < a.n)
-                            st_v4(a.out + (tile.row0 + static_cast<int64_t>(r)) * a.n + col, p[i]);
+                            st_v4(a.out + (static_cast<int64_t>(tile.row0) + r) * a.n + col, p[i]);
                     }
                 }
             }
@@ -608,7 +604,29 @@ bool encode_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t width,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The warpgroups' registers come out of those of the launch; with fewer the
+// ones that ask for more would wait forever.
+cudaError_t check_registers(const void* kernel) {
+    cudaFuncAttributes fa{};
+    const cudaError_t err = cudaFuncGetAttributes(&fa, kernel);
+    if (err != cudaSuccess) return err;
+    return fa.numRegs >= kLaunchRegs ? cudaSuccess : cudaErrorInvalidDeviceFunction;
+}
+
+template <bool kGateUp>
+cudaError_t check_registers_once() {
+    static const cudaError_t result =
+        check_registers(reinterpret_cast<const void*>(&expert_kernel<kGateUp>));
+    return result;
+}
+
 }  // namespace
+
+int64_t expert_tiles_bound(int64_t num_recv, int E, int64_t n, bool gated) {
+    const int64_t col_tiles = gated ? n / 2 / kFp8Block : (n + kTileCols - 1) / kTileCols;
+    const int64_t row_tiles = num_recv / kTileRows + (num_recv < E ? num_recv : E);
+    return row_tiles * col_tiles;
+}
 
 cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream) {
     const bool gated = a.out_q != nullptr;
@@ -619,16 +637,14 @@ cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream) {
         if (!encode_map(&maps.rows[i], a.a, a.num_recv, a.k, 16 << i)) return cudaErrorInvalidValue;
     if (!encode_map(&maps.weights, a.w, static_cast<int64_t>(a.E) * a.n, a.k, kPieceRows))
         return cudaErrorInvalidValue;
-    // at most this many tiles, whatever the offsets say
-    const int64_t row_tiles =
-        a.num_recv / kTileRows + (a.num_recv < a.E ? a.num_recv : static_cast<int64_t>(a.E));
-    const int64_t most = row_tiles * a.col_tiles;
-    if (most > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    // at most this many tiles, checked against kMaxTiles by the caller
+    const int64_t most = expert_tiles_bound(a.num_recv, a.E, a.n, gated);
     const int grid = static_cast<int>(most < num_sms ? most : num_sms);
     const size_t smem = 1024 + kStages * kStageBytes + sizeof(int32_t) * (a.E + 1);
     auto kern = gated ? expert_kernel<true> : expert_kernel<false>;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem));
+    cudaError_t err = gated ? check_registers_once<true>() : check_registers_once<false>();
+    if (err != cudaSuccess) return err;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
     return launch_dependent(kern, grid, kThreads, smem, stream, a, maps);
 }

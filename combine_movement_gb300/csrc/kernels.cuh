@@ -258,6 +258,11 @@ struct ExpertArgs {
 
 cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream);
 
+// Tiles of an expert product for any split of num_recv rows, at most; n counts
+// both halves of a gated one. Its tile indices go up to kMaxTiles.
+int64_t expert_tiles_bound(int64_t num_recv, int E, int64_t n, bool gated);
+constexpr int kMaxTiles = 1 << 30;
+
 // Launch a kernel of the hot path. With programmatic dependent launch the
 // launch may start while the previous kernel on the stream finishes: its CTAs
 // become resident and wait in griddep_wait(), which every such kernel calls

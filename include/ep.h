@@ -342,7 +342,8 @@ EP_API ep_status_t ep_dispatch_fp8(const uint16_t* x, int64_t T, int64_t H, int 
  *   w        e4m3 [E][N][K]                w_scale  fp32 [E][ceil(N/128)][ceil(K/128)]
  *   offsets  int32 [E+1], on the device    out      bf16 [num_recv][N]
  * K a multiple of 16, N of 8; a, w and out 16-byte aligned; E * N and K below
- * 2^31 - 256. Offsets that do not ascend from 0 or more to at most num_recv
+ * 2^31 - 256, and (num_recv / 128 + min(num_recv, E)) * ceil(N / 256) at most
+ * 2^30. Offsets that do not ascend from 0 or more to at most num_recv
  * report EP_ERR_BAD_SLOT, and the expert concerned is skipped. The SM budget
  * does not apply (it leaves SMs to work like this); a call into an SM
  * partition's stream uses the partition's SMs. */

@@ -61,7 +61,8 @@ def test_invalid_arguments(ep, call, bad):
 
 @pytest.mark.parametrize("call,big", [
     (matmul, dict(E=5000)), (matmul, dict(R=1 << 31)), (matmul, dict(K=1 << 31)),
-    (matmul, dict(E=4096, N=1 << 20)), (matmul, dict(N=1 << 62)), (matmul, dict(K=1 << 62)),
+    (matmul, dict(E=4096, N=1 << 20)), (matmul, dict(N=1 << 62)),
+    (matmul, dict(E=1, R=(1 << 31) - 1, N=1 << 16)), (gate_up, dict(E=1, R=(1 << 31) - 1, I=1 << 15)), (matmul, dict(K=1 << 62)),
     (gate_up, dict(I=1 << 40)), (gate_up, dict(I=1 << 30)), (gate_up, dict(E=4097)),
     (dispatch, dict(T=1 << 31)), (dispatch, dict(T=1 << 62)), (dispatch, dict(R=1 << 31)),
     (dispatch, dict(H=1 << 31)),

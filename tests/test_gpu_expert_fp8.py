@@ -230,3 +230,26 @@ def test_in_a_cuda_graph(ep):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_shapes(ep, seed):
+    """Random per-expert counts (many empty, a few large), widths and depths."""
+    rng = np.random.default_rng(seed)
+    E = int(rng.integers(1, 80))
+    counts = [int(c) for c in rng.integers(0, 300, E) * (rng.random(E) < 0.5)]
+    counts[int(rng.integers(E))] += 1
+    K = 16 * int(rng.integers(1, 80))
+    check_matmul(ep, counts, 8 * int(rng.integers(1, 100)), K, seed=seed, spare=int(rng.integers(5)))
+    check_gate_up(ep, counts, 128 * int(rng.integers(1, 5)), K, seed=seed, spare=int(rng.integers(5)))
+
+
+def test_overlapping_offsets_stay_in_bounds(ep):
+    """Offsets that go back are reported; whatever is written stays inside."""
+    a, a_scale, offsets, w, w_scale = operands([40, 40, 40, 40], 128, 128, 5, spare=8)
+    bad = torch.tensor([0, 160, 0, 160, 160], dtype=torch.int32, device="cuda")
+    out = torch.zeros((168, 128), dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ep.ep_expert_matmul_fp8(a, a_scale, bad, w, w_scale, out, status)
+    assert ep.ep_get_status(status) == ep.EP_ERR_BAD_SLOT
+    assert bool((out[160:] == 0).all())
