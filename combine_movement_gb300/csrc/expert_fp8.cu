@@ -320,7 +320,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_max_registers_down<kOtherRegs>();
         if (warp == kCopyWarp) {
             // ---- copies: one lane fills the stages in order ----
-            const uint64_t keep = policy_evict_last();
             Ring<kStages> st;
             bool ok = true;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t dst = base + st.i * kStageBytes, bar = full + 8 * st.i;
                         const int x = kb * kTileK;
                         mbar_arrive_expect_tx(bar, bytes);
-                        tensor_load_2d(dst, &maps.rows[box], x, tile.row0, bar, keep);
+                        tensor_load_2d(dst, &maps.rows[box], x, tile.row0, bar);
                         tensor_load_2d(dst + kStageA, &maps.weights, x, w0, bar);
                         tensor_load_2d(dst + kStageA + kPiece, &maps.weights, x, w1, bar);
                         tensor_load_2d(dst + kStageA + 2 * kPiece, &maps.weights, x, w0 + kPieceRows, bar);

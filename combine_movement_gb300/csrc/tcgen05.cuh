@@ -114,16 +114,6 @@ __device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap* map) {
 // Box of `map` at (x, y) -> shared memory, completing its bytes on `bar`. x
 // times the element size is a multiple of 16; out-of-range elements read 0.
 __device__ __forceinline__ void tensor_load_2d(uint32_t dst_smem, const CUtensorMap* map, int32_t x,
-                                               int32_t y, uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile"
-        ".mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst_smem),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-// The same with the default L2 policy.
-__device__ __forceinline__ void tensor_load_2d(uint32_t dst_smem, const CUtensorMap* map, int32_t x,
                                                int32_t y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile"

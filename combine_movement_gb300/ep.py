@@ -142,7 +142,7 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, what: str = "") -> Optional[int]
         return None
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
@@ -317,7 +317,7 @@ def ep_combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tenso
 
 
 def _shape(t: torch.Tensor, shape: Tuple[int, ...], what: str) -> None:
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
 
 
