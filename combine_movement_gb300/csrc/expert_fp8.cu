@@ -12,28 +12,31 @@
 // times two blocks of 128 weight rows (neighbours; for the gated form block j
 // of the gate half and block j of the up half, so that the tile holds a whole
 // quantisation block of h). Per 128 values along K one of four stages of
-// shared memory takes the operands (tensor copies, 128-byte swizzle), and
-// tcgen05.mma of 128 x 128 x 32, four for each half of the tile's columns (64
-// of each weight block), leave the block's plain sums in tensor memory. The
-// scales differ between rows and between blocks along K, so they cannot ride
-// in the tensor core's sum: for each half two warpgroups read the sums back
-// and add them, scaled, into fp32 registers (a thread holds 32 columns of
-// both weight blocks of one row), while the tensor cores work on the other
-// half and on the next block (each half has two places in tensor memory). One
-// warp issues the tensor copies, one for each half the products, one the
-// scales' copies (four bytes each, asynchronous, four blocks ahead).
+// shared memory takes the operands (tensor copies, 128-byte swizzle), and four
+// tcgen05.mma of 128 x 256 x 32 leave the block's plain sums in one of two
+// places in tensor memory. The scales differ between rows and between blocks
+// along K, so they cannot ride in the tensor core's sum: four warpgroups read
+// the sums back and add them, scaled, into fp32 registers (a thread holds 32
+// columns of both weight blocks of one row), while the tensor cores work on
+// the next block. One warp issues the tensor copies, one the products, one the
+// scales' copies (four bytes each, asynchronous, up to sixteen blocks ahead).
 //
 // What bounds it: few rows to an expert, the weights' bytes (256 experts x
 // 7168 x 2048 for 1024 rows: 538 us, 6.9 TB/s; one row each for eight experts
-// of 4096 x 7168: 50 us, 4.7 TB/s, 128 tiles on 152 SMs). Many rows, the adding:
-// a block's products take the tensor cores 512 cycles, a block's adding about
-// 850, mostly latencies (a barrier that is ready takes 70-150 cycles to ask, a
-// load from tensor memory 50-70), with 384 of them in the fma pipe (131072
-// rows x 7168 x 4096 on 128 experts: 3.19 ms, 2.4 PFLOP/s). Measured on the
-// way: eight adding warps with 64 columns of each block, 3.76 ms; a branch
-// around the adding for rows a tile lacks, 25 % slower at 128 rows an expert;
-// pairs of CTAs on tiles of 256 rows (cta_group::2: two thirds of the bytes
-// from L2) 3-5 % faster at 1000 rows an expert, 18-36 % slower below 130.
+// of 4096 x 7168: 42 us, 5.6 TB/s). Many rows, the adding: a block's products
+// take the tensor cores 512 cycles, a block's adding about 800, mostly
+// latencies (a barrier that is ready takes 70-150 cycles to ask, a load from
+// tensor memory 50-70) with 384 of them in the fma pipe (131072 rows x 7168 x
+// 4096 on 128 experts: 3.1 ms, 2.5 PFLOP/s; run for seconds, the board's
+// power limit brings it to 3.7 ms). Measured on the way:
+//  - eight adding warps with 64 columns of each block: 3.76 ms;
+//  - a branch around the adding for rows a tile lacks: 25 % slower at 128 rows
+//    an expert;
+//  - a product of 128 x 128 for each half of the columns, which two warpgroups
+//    add: 1.5-3 % slower (the products then read their rows twice, all of
+//    shared memory's bandwidth);
+//  - pairs of CTAs on tiles of 256 rows (cta_group::2: two thirds of the bytes
+//    from L2): 2-6 % faster at 1000 rows an expert, 5-30 % slower below 130.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -51,18 +54,15 @@ constexpr int kTileRows = 128;
 constexpr int kTileK = 128;                    // bytes and values of one stage row
 constexpr int kTileCols = 2 * kFp8Block;       // weight rows of a tile
 constexpr uint32_t kStageA = kTileRows * kTileK;
-constexpr int kPieceRows = kFp8Block / 2;      // weight rows per copy: a half's part of a block
-constexpr uint32_t kPiece = kPieceRows * kTileK;
-constexpr uint32_t kStageBytes = kStageA + 4 * kPiece;
+constexpr uint32_t kStageB = kFp8Block * kTileK;  // one of the tile's two weight blocks
+constexpr uint32_t kStageBytes = kStageA + 2 * kStageB;
 constexpr int kStages = 4;
-constexpr int kHalfCols = kTileCols / 2;       // columns of one product: 64 of each weight block
-constexpr int kSlots = 2;                      // of each half in tensor memory
+constexpr int kSlots = 2;                      // of a block's sums in tensor memory
 constexpr int kAccWarps = 16;
-constexpr int kAccGroups = kAccWarps / 4;      // warpgroups, two for each half
-constexpr int kAccCols = kHalfCols / 4;        // of each weight block, in one thread
-constexpr int kProductWarp = kAccWarps;        // and the next, one for each half
-constexpr int kCopyWarp = kAccWarps + 2, kScaleWarp = kAccWarps + 3;
-constexpr int kThreads = (kAccWarps + 4) * 32;
+constexpr int kAccGroups = kAccWarps / 4;      // warpgroups
+constexpr int kAccCols = kFp8Block / kAccGroups;  // of each weight block, in one thread
+constexpr int kProductWarp = kAccWarps, kCopyWarp = kAccWarps + 1, kScaleWarp = kAccWarps + 2;
+constexpr int kThreads = (kAccWarps + 4) * 32;  // the last warp idles
 // Registers per thread: the launch's 96 (640 threads) move from the last
 // warpgroup to the four that hold the sums: 512 x 104 + 128 x 64 = 640 x 96.
 constexpr int kAccRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
@@ -91,12 +91,12 @@ struct Maps {
 
 struct Control {
     uint64_t full[kStages];       // the copies have landed
-    uint64_t done[2][kStages];    // the stage's product of a half is done: its sums are there
+    uint64_t done[kStages];       // the stage's product is done: stage free, sums there
     uint64_t scales[kScaleGroups];       // a group has landed: the scale warp's lanes, and its note
     uint64_t scales_read[kScaleGroups];  // and has been read: the adding warps
-    alignas(16) uint64_t sums_read[2][kSlots];
+    alignas(16) uint64_t sums_read[kSlots];
     uint64_t joined;       // accumulating warps, once per tile
-    uint64_t drained[2];   // after an abort: products still in flight
+    uint64_t drained;      // after an abort: products still in flight
     uint32_t tmem;
     int32_t abort;
     TileNote notes[kTileNotes];
@@ -268,16 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(done + 8 * i, 1);
-            mbar_init(done + 8 * (kStages + i), 1);
         }
         for (int i = 0; i < kScaleGroups; ++i) {
             mbar_init(scales + 8 * i, 32 + 1);
             mbar_init(scales_read + 8 * i, kAccWarps);
         }
-        for (int i = 0; i < 2 * kSlots; ++i) mbar_init(sums_read + 8 * i, kAccWarps / 2);
+        for (int i = 0; i < kSlots; ++i) mbar_init(sums_read + 8 * i, kAccWarps);
         mbar_init(joined, kAccWarps);
-        mbar_init(smem_u32(&ctl.drained[0]), 1);
-        mbar_init(smem_u32(&ctl.drained[1]), 1);
+        mbar_init(smem_u32(&ctl.drained), 1);
         ctl.abort = 0;
         fence_mbar_init();
     }
@@ -325,51 +323,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 const Tile tile = find_tile(t, cum, a);
                 const int box = tile.rows > 64 ? 3 : tile.rows > 32 ? 2 : tile.rows > 16 ? 1 : 0;
-                const uint32_t bytes = (16u << box) * kTileK + 4 * kPiece;
+                const uint32_t bytes = (16u << box) * kTileK + 2 * kStageB;
                 const int w0 = tile.expert * a.n + tile.col_tile * (kGateUp ? kFp8Block : kTileCols);
                 const int w1 = w0 + (kGateUp ? a.n / 2 : kFp8Block);
                 for (int kb = 0; kb < kb_count; ++kb, st.next(), ++fills) {
-#pragma unroll 1
-                    for (int h = 0; ok && h < 2; ++h)  // both halves are done with the stage
-                        ok = warp_wait(done + 8 * (h * kStages + st.i), st.round ^ 1u, abort, a.status);
+                    ok = warp_wait(done + 8 * st.i, st.round ^ 1u, abort, a.status);
                     if (!ok) break;
                     if (elect_one()) {
-                        // rows, then each half's pieces of both weight blocks
                         const uint32_t dst = base + st.i * kStageBytes, bar = full + 8 * st.i;
                         const int x = kb * kTileK;
                         mbar_arrive_expect_tx(bar, bytes);
                         tensor_load_2d(dst, &maps.rows[box], x, tile.row0, bar);
                         tensor_load_2d(dst + kStageA, &maps.weights, x, w0, bar);
-                        tensor_load_2d(dst + kStageA + kPiece, &maps.weights, x, w1, bar);
-                        tensor_load_2d(dst + kStageA + 2 * kPiece, &maps.weights, x, w0 + kPieceRows, bar);
-                        tensor_load_2d(dst + kStageA + 3 * kPiece, &maps.weights, x, w1 + kPieceRows, bar);
+                        tensor_load_2d(dst + kStageA + kStageB, &maps.weights, x, w1, bar);
                     }
                     __syncwarp();
                 }
             }
-        } else if (warp != kScaleWarp) {
-            // ---- products of one half ----
-            constexpr uint32_t kDesc = mma_desc_e4m3(kTileRows, kHalfCols);
-            const uint32_t h = warp - kProductWarp;
+        } else if (warp == kProductWarp) {
+            // ---- products: one lane ----
+            constexpr uint32_t kDesc = mma_desc_e4m3(kTileRows, kTileCols);
             const uint64_t desc0 = operand_desc(base);
-            const uint32_t done_h = done + 8 * kStages * h, read_h = sums_read + 8 * kSlots * h;
             Ring<kStages> st;
             Ring<kSlots> slot;
             bool ok = true;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 for (int kb = 0; kb < kb_count; ++kb, st.next(), slot.next()) {
                     ok = warp_wait(full + 8 * st.i, st.round, abort, a.status) &&
-                         warp_wait(read_h + 8 * slot.i, slot.round ^ 1u, abort, a.status);
+                         warp_wait(sums_read + 8 * slot.i, slot.round ^ 1u, abort, a.status);
                     if (!ok) break;
                     tcgen05_fence_after();
                     if (elect_one()) {
                         const uint64_t da = desc0 + st.i * (kStageBytes >> 4);
-                        const uint64_t db = da + ((kStageA + h * 2 * kPiece) >> 4);
-                        const uint32_t sums = tmem + (2 * slot.i + h) * kHalfCols;
+                        const uint64_t db = da + (kStageA >> 4);
 #pragma unroll
                         for (int k = 0; k < kTileK / 32; ++k)
-                            mma_e4m3(sums, da + 2 * k, db + 2 * k, kDesc, k > 0);
-                        mma_commit(done_h + 8 * st.i);
+                            mma_e4m3(tmem + slot.i * kTileCols, da + 2 * k, db + 2 * k, kDesc, k > 0);
+                        mma_commit(done + 8 * st.i);
                     }
                     __syncwarp();
                 }
@@ -417,13 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---- scaled sums: thread = one row, columns [32 c, 32 c + 32) of both blocks ----
         set_max_registers_up<kAccRegs>();
-        const int c = warp >> 2, h = c >> 1, quarter = warp & 3;
+        const int c = warp >> 2, quarter = warp & 3;
         const uint32_t row_scale = smem_u32(&ctl.row_scale[0][0][quarter * 32 + lane]);
         const uint32_t weight_scale = smem_u32(ctl.weight_scale);
-        uint32_t sums = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + h * kHalfCols +
-                        (c & 1) * kAccCols;
-        uint32_t read = sums_read + 8 * kSlots * h;
-        const uint32_t done_h = done + 8 * kStages * h;
+        uint32_t sums = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c * kAccCols;
+        uint32_t read = sums_read;
         Ring<kScaleGroups> group;
         Ring<kStages> st;
         uint32_t tile_no = 0;
@@ -446,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float sa = load_shared_f32(row_at);
                     const float2 sw = load_shared_f32x2(weight_at);
                     const float s0 = sa * sw.x, s1 = sa * sw.y;
-                    ok = ok && warp_wait(done_h + 8 * st.i, st.round, abort, a.status);
+                    ok = ok && warp_wait(done + 8 * st.i, st.round, abort, a.status);
                     st.next();
                     tcgen05_fence_after();
                     uint32_t v[16];
@@ -456,17 +444,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_load16(sums + 16, v);
                     tmem_load_wait16(v);
                     add_scaled(acc[0], 16, v, s0);
-                    tmem_load16(sums + 64, v);
+                    tmem_load16(sums + kFp8Block, v);
                     tmem_load_wait16(v);
                     add_scaled(acc[1], 0, v, s1);
-                    tmem_load16(sums + 80, v);
+                    tmem_load16(sums + kFp8Block + 16, v);
                     tmem_load_wait16(v);
                     tcgen05_fence_before();
                     mbar_arrive_if(read, ok && lane == 0);
                     add_scaled(acc[1], 16, v, s1);
                     row_at += sizeof(ctl.row_scale[0][0]);
                     weight_at += sizeof(ctl.weight_scale[0][0]);
-                    sums ^= kTileCols;  // the half's other place: tmem starts at a multiple of 512
+                    sums ^= kTileCols;  // the other place: tmem starts at a multiple of 512
                     read ^= 8u;         // sums_read is 16-byte aligned
                 }
                 __syncwarp();
@@ -556,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kCopyWarp && lane == 0)
             mbar_drain_bounded<kStages>(full, fills > kStages ? fills - kStages : 0u,
                                         static_cast<int64_t>(fills) - 1);
-        if (warp == kProductWarp || warp == kProductWarp + 1) {
-            const uint32_t bar = smem_u32(&ctl.drained[warp - kProductWarp]);
+        if (warp == kProductWarp) {
+            const uint32_t bar = smem_u32(&ctl.drained);
             if (elect_one()) mma_commit(bar);
             __syncwarp();
             mbar_wait_bounded(bar, 0);
@@ -634,7 +622,7 @@ cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream) {
     Maps maps;
     for (int i = 0; i < kRowBoxes; ++i)
         if (!encode_map(&maps.rows[i], a.a, a.num_recv, a.k, 16 << i)) return cudaErrorInvalidValue;
-    if (!encode_map(&maps.weights, a.w, static_cast<int64_t>(a.E) * a.n, a.k, kPieceRows))
+    if (!encode_map(&maps.weights, a.w, static_cast<int64_t>(a.E) * a.n, a.k, kFp8Block))
         return cudaErrorInvalidValue;
     // at most this many tiles, checked against kMaxTiles by the caller
     const int64_t most = expert_tiles_bound(a.num_recv, a.E, a.n, gated);
