@@ -318,12 +318,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_max_registers_down<kOtherRegs>();
         if (warp == kCopyWarp) {
             // ---- copies: one lane fills the stages in order ----
+            // Of a tile with few rows only those are copied, and the stage's others
+            // cleared once: products of whatever the last tile left there cost
+            // power, and with it clock rate. Four bits a stage: the row box that
+            // may hold something.
+            uint32_t row_fill = 0x33333333u;
+            static_assert(kStages <= 8, "four bits a stage");
             Ring<kStages> st;
             bool ok = true;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
                 const Tile tile = find_tile(t, cum, a);
                 const int box = tile.rows > 64 ? 3 : tile.rows > 32 ? 2 : tile.rows > 16 ? 1 : 0;
-                const uint32_t bytes = (16u << box) * kTileK + 2 * kStageB;
                 const int w0 = tile.expert * a.n + tile.col_tile * (kGateUp ? kFp8Block : kTileCols);
                 const int w1 = w0 + (kGateUp ? a.n / 2 : kFp8Block);
                 for (int kb = 0; kb < kb_count; ++kb, st.next(), ++fills) {
@@ -332,12 +337,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one()) {
                         const uint32_t dst = base + st.i * kStageBytes, bar = full + 8 * st.i;
                         const int x = kb * kTileK;
-                        mbar_arrive_expect_tx(bar, bytes);
+                        const int filled = max(box, static_cast<int>(row_fill >> (4 * st.i)) & 15);
+                        mbar_arrive_expect_tx(bar, (16u << filled) * kTileK + 2 * kStageB);
                         tensor_load_2d(dst, &maps.rows[box], x, tile.row0, bar);
+                        for (int i = box; i < filled; ++i)  // (rows past the last read as zeros)
+                            tensor_load_2d(dst + (16u << i) * kTileK, &maps.rows[i], 0,
+                                           static_cast<int>(a.num_recv), bar);
                         tensor_load_2d(dst + kStageA, &maps.weights, x, w0, bar);
                         tensor_load_2d(dst + kStageA + kStageB, &maps.weights, x, w1, bar);
                     }
                     __syncwarp();
+                    row_fill = (row_fill & ~(15u << (4 * st.i))) | (static_cast<uint32_t>(box) << (4 * st.i));
                 }
             }
         } else if (warp == kProductWarp) {
