@@ -26,6 +26,10 @@
  *                      fp32 fused-multiply-add chain starting from +0.0f, of
  *                      topk_w[t,k] * float(expert_out[slot[t,k], :]) )
  *
+ * Beside the movement: its gradients (ep_combine_grad, ep_dispatch_grad), a
+ * dispatch that quantises rows to 8 bits (ep_dispatch_fp8) and the experts'
+ * products on such rows (ep_expert_gate_up_fp8, ep_expert_matmul_fp8).
+ *
  * The pages describe neither the layout call nor combine; the stable order,
  * the masking rule and the combine arithmetic above are this library's
  * readings (plainest reading of the MoE problem the pages state), chosen so
