@@ -121,6 +121,33 @@ def test_unused_rows_bring_nothing_into_the_gradients(mods):
     assert bool((rows.grad[~used] == 0).all()) and bool((rows.grad[used] != 0).any())
 
 
+def test_same_bits_on_streams_partitions_and_overlap_modes(mods):
+    """The layer on three streams and both streams of an SM partition at once,
+    and under each launch-overlap mode: the results of a quiet GPU."""
+    ep, moe = mods
+    x, idx, w, gate_up, down = layer(300, 512, 16, 4, 256, seed=11, mask=0.1)
+    args = (x, idx, w, *moe.quantize_weights(gate_up), *moe.quantize_weights(down))
+    want = moe.forward_fp8(*args)
+    part, rest, _, _ = ep.ep_sm_partition(24)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    streams += [torch.cuda.ExternalStream(part), torch.cuda.ExternalStream(rest)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(moe.forward_fp8(*args))
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want) for y in got)
+    try:
+        for mode in (1, 2):
+            ep.ep_set_launch_overlap(mode)
+            for _ in range(10):
+                assert torch.equal(moe.forward_fp8(*args), want)
+    finally:
+        ep.ep_set_launch_overlap(0)
+
+
 def test_command(mods, capsys, monkeypatch):
     import json
     import sys
