@@ -17,9 +17,9 @@
 // it) the entries go round the groups of the budget.
 //
 // Bound by memory: T = 4096, H = 7168, top-8 reads 470 MB of expert rows, writes as
-// many and reads 59 MB of dy in 152.8 us, 6.5 TB/s, 0.96 of a plain copy's
+// many and reads 59 MB of dy in 151.4 us, 6.6 TB/s, 0.97 of a plain copy's
 // rate (with one CTA per SM 163 us; two entries to a warp 156 us). T = 128,
-// H = 1024, top-2: about the launch, 7.6 us.
+// H = 1024, top-2: about the launch, 6.5 us.
 #include <cuda_runtime.h>
 
 #include "../../include/ep.h"

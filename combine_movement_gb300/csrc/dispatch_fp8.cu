@@ -15,7 +15,7 @@
 // Bound by the writes: T = 4096, H = 7168, top-8 moves 301 MB (a fifth of it reads) in
 // 46.6 us, 6.5 TB/s, 0.95 of a plain copy's rate; with one CTA per SM it took
 // 54 us (some SMs write a quarter slower than others), with two or four units
-// to a warp 50 and 53 us. T = 128: about the launch, 7 us.
+// to a warp 50 and 53 us. T = 128: about the launch, 6 us.
 #include <cuda_runtime.h>
 
 #include "../../include/ep.h"

@@ -22,14 +22,14 @@
 // scales' copies (four bytes each, asynchronous, up to sixteen blocks ahead).
 //
 // What bounds it: few rows to an expert, the weights' bytes (256 experts x
-// 7168 x 2048 for 1024 rows: 538 us, 6.9 TB/s; one row each for eight experts
-// of 4096 x 7168: 42 us, 5.6 TB/s). Many rows, the adding: a block's products
+// 7168 x 2048 for 1024 rows: 520-537 us, 7 TB/s; one row each for eight experts
+// of 4096 x 7168: 41 us, 5.7 TB/s). Many rows, the adding: a block's products
 // take the tensor cores 512 cycles, a block's adding about 800, mostly
 // latencies (a barrier that is ready takes 70-150 cycles to ask, a load from
 // tensor memory 50-70) with 384 of them in the fma pipe (131072 rows x 7168 x
-// 4096 on 128 experts: 3.1 ms, 2.5 PFLOP/s; run for seconds, the board's
-// power limit brings it to 3.7 ms). Measured on the way:
-//  - eight adding warps with 64 columns of each block: 3.76 ms;
+// 4096 on 128 experts: 3.0 ms, 2.6 PFLOP/s; run for seconds, the board's
+// power limit brings it to 3.5 ms). Measured on the way:
+//  - eight adding warps with 64 columns of each block: 18 % slower;
 //  - a branch around the adding for rows a tile lacks: 25 % slower at 128 rows
 //    an expert;
 //  - a product of 128 x 128 for each half of the columns, which two warpgroups
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kProductWarp) tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
     if (warp == kCopyWarp && lane == 0) {
-        for (int i = 0; i < kRowBoxes; ++i) prefetch_tensor_map(&maps.rows[i]);
+        for (int i = 0; i < a.row_boxes; ++i) prefetch_tensor_map(&maps.rows[i]);
         prefetch_tensor_map(&maps.weights);
     }
     griddep_wait();
@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // cleared once: products of whatever the last tile left there cost
             // power, and with it clock rate. Four bits a stage: the row box that
             // may hold something.
-            uint32_t row_fill = 0x33333333u;
+            // (At first, boxes that no tile fills are left as they are.)
+            uint32_t row_fill = 0x11111111u * static_cast<uint32_t>(a.row_boxes - 1);
             static_assert(kStages <= 8, "four bits a stage");
             Ring<kStages> st;
             bool ok = true;
@@ -630,7 +631,10 @@ cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream) {
     a.k_blocks = static_cast<int>((a.k + kFp8Block - 1) / kFp8Block);
     a.col_tiles = gated ? a.n / 2 / kFp8Block : (a.n + kTileCols - 1) / kTileCols;
     Maps maps;
-    for (int i = 0; i < kRowBoxes; ++i)
+    // no tile has more rows than there are: row boxes up to those are all it needs
+    a.row_boxes = 1;
+    while (a.row_boxes < kRowBoxes && (8 << a.row_boxes) < a.num_recv) ++a.row_boxes;
+    for (int i = 0; i < a.row_boxes; ++i)
         if (!encode_map(&maps.rows[i], a.a, a.num_recv, a.k, 16 << i)) return cudaErrorInvalidValue;
     if (!encode_map(&maps.weights, a.w, static_cast<int64_t>(a.E) * a.n, a.k, kFp8Block))
         return cudaErrorInvalidValue;

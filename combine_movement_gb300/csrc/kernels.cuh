@@ -254,6 +254,7 @@ struct ExpertArgs {
     // set by launch_expert
     int k_blocks;
     int col_tiles;
+    int row_boxes;             // row boxes of 16, 32, ... that the rows can fill
 };
 
 cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream);

@@ -33,6 +33,7 @@ EP_MAX_EXPERTS = 4096
 
 # Values that share one scale in the 8-bit operands.
 FP8_BLOCK = 128
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 
 
 def _header_define(name: str) -> int:
@@ -316,9 +317,32 @@ def ep_combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tenso
     _check(code, "ep_combine")
 
 
-def _shape(t: torch.Tensor, shape: Tuple[int, ...], what: str) -> None:
+# Arguments of the expert and gradient calls: the address of a tensor of this
+# type and shape, checked in one expression (the host's part of a call is
+# longer than the device's of a small one). Where it lies, its caller
+# checks.
+def _arg(t: torch.Tensor, dtype, shape: Tuple[int, ...], what: str) -> int:
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
-        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    raise ValueError(f"{what}: expected a contiguous tensor")
+
+
+def _opt(t: Optional[torch.Tensor], dtype, shape: Tuple[int, ...], what: str) -> Optional[int]:
+    if t is None:
+        return None
+    p = _arg(t, dtype, shape, what)
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    return p
+
+
+def _off_gpu(**tensors: torch.Tensor) -> ValueError:
+    what = ", ".join(k for k, t in tensors.items() if not t.is_cuda)
+    return ValueError(f"{what}: expected a CUDA tensor")
 
 
 def ep_dispatch_fp8(x: torch.Tensor, slot: torch.Tensor, recv_q: torch.Tensor,
@@ -328,16 +352,18 @@ def ep_dispatch_fp8(x: torch.Tensor, slot: torch.Tensor, recv_q: torch.Tensor,
                     status: Optional[torch.Tensor] = None, stream=None) -> None:
     T, H = x.shape
     K, R = slot.shape[1], recv_q.shape[0]
-    _shape(slot, (T, K), "slot")
-    _shape(recv_q, (R, H), "recv_q")
-    _shape(recv_scale, (R, -(-H // FP8_BLOCK)), "recv_scale")
+    px, ps = _arg(x, _BF16, (T, H), "x"), _arg(slot, _I32, (T, K), "slot")
+    pq = _arg(recv_q, _E4M3, (R, H), "recv_q")
+    pc = _arg(recv_scale, _F32, (R, -(-H // FP8_BLOCK)), "recv_scale")
+    if not (x.is_cuda and slot.is_cuda and recv_q.is_cuda and recv_scale.is_cuda):
+        raise _off_gpu(x=x, slot=slot, recv_q=recv_q, recv_scale=recv_scale)
     code = lib.ep_dispatch_fp8(
-        _ptr(x, torch.bfloat16, "x"), T, H, K, _ptr(slot, torch.int32, "slot"),
-        _ptr(topk_w, torch.float32, "topk_w"), R, _ptr(recv_q, torch.float8_e4m3fn, "recv_q"),
-        _ptr(recv_scale, torch.float32, "recv_scale"), _ptr(recv_w, torch.float32, "recv_w"),
-        _ptr(recv_src, torch.int32, "recv_src"), _ptr(status, torch.int32, "status"),
-        _stream(stream))
-    _check(code, "ep_dispatch_fp8")
+        px, T, H, K, ps, None if topk_w is None else _opt(topk_w, _F32, (T, K), "topk_w"), R, pq, pc,
+        None if recv_w is None else _opt(recv_w, _F32, (R,), "recv_w"),
+        None if recv_src is None else _opt(recv_src, _I32, (R,), "recv_src"),
+        None if status is None else _ptr(status, _I32, "status"), _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_dispatch_fp8")
 
 
 def ep_combine_grad(dy: torch.Tensor, expert_out: torch.Tensor, slot: torch.Tensor,
@@ -346,75 +372,79 @@ def ep_combine_grad(dy: torch.Tensor, expert_out: torch.Tensor, slot: torch.Tens
                     stream=None) -> None:
     T, H = dy.shape
     K, R = slot.shape[1], expert_out.shape[0]
-    _shape(expert_out, (R, H), "expert_out")
-    _shape(slot, (T, K), "slot")
-    _shape(topk_w, (T, K), "topk_w")
-    if d_expert_out is not None:
-        _shape(d_expert_out, (R, H), "d_expert_out")
-    if d_topk_w is not None:
-        _shape(d_topk_w, (T, K), "d_topk_w")
+    rows, pairs = (R, H), (T, K)
+    py, pe = _arg(dy, _BF16, (T, H), "dy"), _arg(expert_out, _BF16, rows, "expert_out")
+    ps, pw = _arg(slot, _I32, pairs, "slot"), _arg(topk_w, _F32, pairs, "topk_w")
+    pde = None if d_expert_out is None else _arg(d_expert_out, _BF16, rows, "d_expert_out")
+    pdw = None if d_topk_w is None else _arg(d_topk_w, _F32, pairs, "d_topk_w")
+    if not (dy.is_cuda and expert_out.is_cuda and slot.is_cuda and topk_w.is_cuda
+            and (pde is None or d_expert_out.is_cuda) and (pdw is None or d_topk_w.is_cuda)):
+        raise ValueError("ep_combine_grad: expected a CUDA tensor for every argument")
     code = lib.ep_combine_grad(
-        _ptr(dy, torch.bfloat16, "dy"), _ptr(expert_out, torch.bfloat16, "expert_out"), R,
-        _ptr(slot, torch.int32, "slot"), _ptr(topk_w, torch.float32, "topk_w"), T, H, K,
-        _ptr(d_expert_out, torch.bfloat16, "d_expert_out"),
-        _ptr(d_topk_w, torch.float32, "d_topk_w"), _ptr(status, torch.int32, "status"),
+        py, pe, R, ps, pw, T, H, K, pde, pdw, None if status is None else _ptr(status, _I32, "status"),
         _stream(stream))
-    _check(code, "ep_combine_grad")
+    if code != EP_OK:
+        raise EPError(code, "ep_combine_grad")
 
 
 def ep_dispatch_grad(d_recv: torch.Tensor, slot: torch.Tensor, dx: torch.Tensor,
                      status: Optional[torch.Tensor] = None, stream=None) -> None:
     T, H = dx.shape
     K, R = slot.shape[1], d_recv.shape[0]
-    _shape(d_recv, (R, H), "d_recv")
-    _shape(slot, (T, K), "slot")
-    code = lib.ep_dispatch_grad(
-        _ptr(d_recv, torch.bfloat16, "d_recv"), R, _ptr(slot, torch.int32, "slot"), T, H, K,
-        _ptr(dx, torch.bfloat16, "dx"), _ptr(status, torch.int32, "status"), _stream(stream))
-    _check(code, "ep_dispatch_grad")
-
-
-def _expert_operands(a, a_scale, offsets, w, w_scale):
-    """Checks the operands of an expert product against each other and
-    returns (num_recv, E, rows of w, K)."""
-    (R, K), (E, N) = a.shape, w.shape[:2]
-    kb = -(-K // FP8_BLOCK)
-    _shape(a_scale, (R, kb), "a_scale")
-    _shape(offsets, (E + 1,), "offsets")
-    _shape(w, (E, N, K), "w")
-    _shape(w_scale, (E, -(-N // FP8_BLOCK), kb), "w_scale")
-    return R, E, N, K
+    pd, ps = _arg(d_recv, _BF16, (R, H), "d_recv"), _arg(slot, _I32, (T, K), "slot")
+    px = _arg(dx, _BF16, (T, H), "dx")
+    if not (d_recv.is_cuda and slot.is_cuda and dx.is_cuda):
+        raise _off_gpu(d_recv=d_recv, slot=slot, dx=dx)
+    code = lib.ep_dispatch_grad(pd, R, ps, T, H, K, px,
+                                None if status is None else _ptr(status, _I32, "status"),
+                                _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_dispatch_grad")
 
 
 def ep_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor,
                          w: torch.Tensor, w_scale: torch.Tensor, out: torch.Tensor,
                          status: Optional[torch.Tensor] = None, stream=None) -> None:
-    R, E, N, K = _expert_operands(a, a_scale, offsets, w, w_scale)
-    _shape(out, (R, N), "out")
+    R, K = a.shape
+    E, N = w.shape[:2]
+    kb = -(-K // FP8_BLOCK)
+    pa, ps = _arg(a, _E4M3, (R, K), "a"), _arg(a_scale, _F32, (R, kb), "a_scale")
+    po, pw = _arg(offsets, _I32, (E + 1,), "offsets"), _arg(w, _E4M3, (E, N, K), "w")
+    pws = _arg(w_scale, _F32, (E, -(-N // FP8_BLOCK), kb), "w_scale")
+    py = _arg(out, _BF16, (R, N), "out")
+    if not (a.is_cuda and a_scale.is_cuda and offsets.is_cuda and w.is_cuda and w_scale.is_cuda
+            and out.is_cuda):
+        raise _off_gpu(a=a, a_scale=a_scale, offsets=offsets, w=w, w_scale=w_scale, out=out)
     code = lib.ep_expert_matmul_fp8(
-        _ptr(a, torch.float8_e4m3fn, "a"), _ptr(a_scale, torch.float32, "a_scale"), R,
-        _ptr(offsets, torch.int32, "offsets"), E, _ptr(w, torch.float8_e4m3fn, "w"),
-        _ptr(w_scale, torch.float32, "w_scale"), N, K, _ptr(out, torch.bfloat16, "out"),
-        _ptr(status, torch.int32, "status"), _stream(stream))
-    _check(code, "ep_expert_matmul_fp8")
+        pa, ps, R, po, E, pw, pws, N, K, py, None if status is None else _ptr(status, _I32, "status"),
+        _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_expert_matmul_fp8")
 
 
 def ep_expert_gate_up_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor,
                           w: torch.Tensor, w_scale: torch.Tensor, out_q: torch.Tensor,
                           out_scale: torch.Tensor, status: Optional[torch.Tensor] = None,
                           stream=None) -> None:
-    R, E, N, K = _expert_operands(a, a_scale, offsets, w, w_scale)
+    R, K = a.shape
+    E, N = w.shape[:2]
     if N % 2:
         raise ValueError(f"w: expected a gate half and an up half, got {N} rows")
-    _shape(out_q, (R, N // 2), "out_q")
-    _shape(out_scale, (R, -(-N // 2 // FP8_BLOCK)), "out_scale")
+    kb, width = -(-K // FP8_BLOCK), N // 2
+    pa, ps = _arg(a, _E4M3, (R, K), "a"), _arg(a_scale, _F32, (R, kb), "a_scale")
+    po, pw = _arg(offsets, _I32, (E + 1,), "offsets"), _arg(w, _E4M3, (E, N, K), "w")
+    pws = _arg(w_scale, _F32, (E, -(-N // FP8_BLOCK), kb), "w_scale")
+    pq = _arg(out_q, _E4M3, (R, width), "out_q")
+    pqs = _arg(out_scale, _F32, (R, -(-width // FP8_BLOCK)), "out_scale")
+    if not (a.is_cuda and a_scale.is_cuda and offsets.is_cuda and w.is_cuda and w_scale.is_cuda
+            and out_q.is_cuda and out_scale.is_cuda):
+        raise _off_gpu(a=a, a_scale=a_scale, offsets=offsets, w=w, w_scale=w_scale, out_q=out_q,
+                       out_scale=out_scale)
     code = lib.ep_expert_gate_up_fp8(
-        _ptr(a, torch.float8_e4m3fn, "a"), _ptr(a_scale, torch.float32, "a_scale"), R,
-        _ptr(offsets, torch.int32, "offsets"), E, _ptr(w, torch.float8_e4m3fn, "w"),
-        _ptr(w_scale, torch.float32, "w_scale"), N // 2, K,
-        _ptr(out_q, torch.float8_e4m3fn, "out_q"), _ptr(out_scale, torch.float32, "out_scale"),
-        _ptr(status, torch.int32, "status"), _stream(stream))
-    _check(code, "ep_expert_gate_up_fp8")
+        pa, ps, R, po, E, pw, pws, width, K, pq, pqs,
+        None if status is None else _ptr(status, _I32, "status"), _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_expert_gate_up_fp8")
 
 
 def ep_sm_partition(num_sms: int) -> Tuple[int, Optional[int], int, int]:
