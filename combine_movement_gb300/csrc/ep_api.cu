@@ -343,7 +343,7 @@ ep_status_t run_expert(const ep::ExpertArgs& x, cudaStream_t stream) {
     if (!device_limits(&sm_count, &smem_optin)) return EP_ERR_CUDA;
     const int part = ep::partition_sms(stream);
     const ep::CallBytes call_bytes(x.num_recv * x.k);
-    return from_cuda(ep::launch_expert(x, part > 0 ? part : sm_count, stream));
+    return from_cuda(ep::launch_expert(x, part > 0 ? part : sm_count, part > 0, stream));
 }
 
 }  // namespace

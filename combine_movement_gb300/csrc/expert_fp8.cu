@@ -23,11 +23,11 @@
 //
 // What bounds it: few rows to an expert, the weights' bytes (256 experts x
 // 7168 x 2048 for 1024 rows: 520-537 us, 7 TB/s; one row each for eight experts
-// of 4096 x 7168: 41 us, 5.7 TB/s). Many rows, the adding: a block's products
+// of 4096 x 7168: 41-43 us, 5.6 TB/s). Many rows, the adding: a block's products
 // take the tensor cores 512 cycles, a block's adding about 800, mostly
 // latencies (a barrier that is ready takes 70-150 cycles to ask, a load from
 // tensor memory 50-70) with 384 of them in the fma pipe (131072 rows x 7168 x
-// 4096 on 128 experts: 3.0 ms, 2.6 PFLOP/s; run for seconds, the board's
+// 4096 on 128 experts: 3.0-3.1 ms, 2.5 PFLOP/s; run for seconds, the board's
 // power limit brings it to 3.5 ms). Measured on the way:
 //  - eight adding warps with 64 columns of each block: 18 % slower;
 //  - a branch around the adding for rows a tile lacks: 25 % slower at 128 rows
@@ -84,6 +84,12 @@ struct TileNote {
     int row0, rows, col_tile;
 };
 
+// A tile shared by a cluster: its fp32 sums, [row][column], in the stages' place;
+// a row's pitch keeps both ways through them free of bank conflicts.
+constexpr uint32_t kSharedPitch = kTileCols * 4 + 16;
+static_assert(kTileRows * kSharedPitch <= kStages * kStageBytes, "shared sums");
+constexpr int kMaxSplit = 8;
+
 struct Maps {
     CUtensorMap rows[kRowBoxes];
     CUtensorMap weights;
@@ -122,6 +128,39 @@ __device__ __forceinline__ float2 load_shared_f32x2(uint32_t addr) {
 }
 __device__ __forceinline__ void store_shared(uint32_t addr, uint32_t v) {
     asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void store_shared_v4(uint32_t addr, float4 v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ float4 load_shared_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 load_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Cluster barrier, reached by a warp's lanes in their roles' branches. Every
+// thread passes it twice, whatever its CTA found to do: the hardware's barrier
+// has no limit of its own, the waits before it have.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Wait of a whole warp on a barrier; false, in every lane, once a lane gave up
@@ -248,7 +287,95 @@ __device__ __forceinline__ void transpose4(uint4 (&p)[4], int j) {
     }
 }
 
-template <bool kGateUp>
+// The kParts CTAs' sums of the rows r = rank mod kParts, joined into this
+// CTA's; always eight 16-byte loads of a thread in flight.
+template <int kParts>
+__device__ __forceinline__ void sum_parts(uint32_t sums, int rows, int rank) {
+    constexpr int kPieces = kTileCols / 4, kAtOnce = 8 / kParts, kStep = kAccWarps * 32;
+    const int pieces = (rows + kParts - 1 - rank) / kParts * kPieces;  // (0 of 0 rows)
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < pieces; i0 += kAtOnce * kStep) {
+        uint32_t addr[kAtOnce];
+        float4 v[kAtOnce][kParts];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int i = i0 + j * kStep;
+            addr[j] = sums + (i / kPieces * kParts + rank) * kSharedPitch + i % kPieces * 16;
+            if (i >= pieces) continue;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) v[j][p] = load_cluster_v4(cluster_map(addr[j], p));
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            if (i0 + j * kStep >= pieces) continue;
+            float4 sum = v[j][0];
+#pragma unroll
+            for (int p = 1; p < kParts; ++p) {
+                sum.x += v[j][p].x;
+                sum.y += v[j][p].y;
+                sum.z += v[j][p].z;
+                sum.w += v[j][p].w;
+            }
+            store_shared_v4(addr[j], sum);  // (only this CTA reads these rows of its own)
+        }
+    }
+}
+
+// The sums of a tile that the cluster's CTAs took parts of K of: each CTA
+// lays its own out in shared memory, and CTA p joins those of the rows
+// r = p mod split, in the order of the parts, so that a row's result does not
+// depend on its place. `row` is the thread's, `at` where its columns start in
+// a row; `rows` 0 after a wait that gave up.
+__device__ __forceinline__ void join_parts(float (&acc)[2][kAccCols], uint32_t sums, int rows, int row,
+                                           uint32_t at, int rank, int split) {
+    const uint32_t own = sums + row * kSharedPitch + at;
+    if (row < rows) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < kAccCols; i += 4)
+                store_shared_v4(own + b * kFp8Block * 4 + i * 4,
+                                make_float4(acc[b][i], acc[b][i + 1], acc[b][i + 2], acc[b][i + 3]));
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (split == 2)
+        sum_parts<2>(sums, rows, rank);
+    else if (split == 4)
+        sum_parts<4>(sums, rows, rank);
+    else
+        sum_parts<8>(sums, rows, rank);
+    cluster_arrive();  // the other CTAs' sums have been read; waited for at the end
+    asm volatile("bar.sync 1, %0;" ::"n"(kAccWarps * 32) : "memory");
+    // (other rows' threads read something that is not stored)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < kAccCols; i += 4) {
+            const float4 v = load_shared_v4(own + b * kFp8Block * 4 + i * 4);
+            acc[b][i] = v.x;
+            acc[b][i + 1] = v.y;
+            acc[b][i + 2] = v.z;
+            acc[b][i + 3] = v.w;
+        }
+}
+
+// A CTA's first tile and the step to its next; a cluster has one tile, t0. The
+// grid's registers are read where they are used: the adding warps have none to
+// keep them in (kept, they cost the large products 1 % cool, 4 % at the power
+// limit).
+template <bool kSplit>
+__device__ __forceinline__ int first_tile(int t0) {
+    return kSplit ? t0 : static_cast<int>(blockIdx.x);
+}
+template <bool kSplit>
+__device__ __forceinline__ int tile_step(int tiles) {
+    return kSplit ? tiles : static_cast<int>(gridDim.x);
+}
+
+// kSplit: a tile's blocks along K go to the CTAs of a cluster, a tile to a
+// cluster; else a CTA takes whole tiles, one after the other.
+template <bool kGateUp, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     expert_kernel(const ExpertArgs a, const __grid_constant__ Maps maps) {
     extern __shared__ uint8_t smem_raw[];
@@ -312,6 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = ctl.tmem;
     const int tiles = cum[a.E];
     const int kb_count = a.k_blocks;
+    const int split = kSplit ? a.split : 1;
+    const int part = kSplit ? static_cast<int>(cluster_rank()) : 0;
+    const int t0 = kSplit ? static_cast<int>(blockIdx.x) / split : 0;
+    // this CTA's blocks along K
+    const int kb_first = kSplit ? static_cast<int>(static_cast<int64_t>(kb_count) * part / split) : 0;
+    const int kb_end =
+        kSplit ? static_cast<int>(static_cast<int64_t>(kb_count) * (part + 1) / split) : kb_count;
     uint32_t fills = 0;  // stages filled so far (the copying warp's)
 
     if (warp >= kAccWarps) {
@@ -327,12 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             static_assert(kStages <= 8, "four bits a stage");
             Ring<kStages> st;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int t = first_tile<kSplit>(t0); ok && t < tiles; t += tile_step<kSplit>(tiles)) {
                 const Tile tile = find_tile(t, cum, a);
                 const int box = tile.rows > 64 ? 3 : tile.rows > 32 ? 2 : tile.rows > 16 ? 1 : 0;
                 const int w0 = tile.expert * a.n + tile.col_tile * (kGateUp ? kFp8Block : kTileCols);
                 const int w1 = w0 + (kGateUp ? a.n / 2 : kFp8Block);
-                for (int kb = 0; kb < kb_count; ++kb, st.next(), ++fills) {
+                for (int kb = kb_first; kb < kb_end; ++kb, st.next(), ++fills) {
                     ok = warp_wait(done + 8 * st.i, st.round ^ 1u, abort, a.status);
                     if (!ok) break;
                     if (elect_one()) {
@@ -358,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring<kStages> st;
             Ring<kSlots> slot;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                for (int kb = 0; kb < kb_count; ++kb, st.next(), slot.next()) {
+            for (int t = first_tile<kSplit>(t0); ok && t < tiles; t += tile_step<kSplit>(tiles)) {
+                for (int kb = kb_first; kb < kb_end; ++kb, st.next(), slot.next()) {
                     ok = warp_wait(full + 8 * st.i, st.round, abort, a.status) &&
                          warp_wait(sums_read + 8 * slot.i, slot.round ^ 1u, abort, a.status);
                     if (!ok) break;
@@ -382,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring<kScaleGroups> group;
             uint32_t tile_no = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
+            for (int t = first_tile<kSplit>(t0); ok && t < tiles; t += tile_step<kSplit>(tiles), ++tile_no) {
                 const Tile tile = find_tile(t, cum, a);
                 const int b0 = kGateUp ? tile.col_tile : 2 * tile.col_tile;
                 const int b1 = kGateUp ? b0 + n_blocks / 2 : min(b0 + 1, n_blocks - 1);
@@ -391,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float* weight =
                     a.w_scale +
                     (static_cast<int64_t>(tile.expert) * n_blocks + ((lane & 1) == 0 ? b0 : b1)) * kb_count;
-                for (int kb0 = 0; kb0 < kb_count; kb0 += kScaleGroup, group.next()) {
+                for (int kb0 = kb_first; kb0 < kb_end; kb0 += kScaleGroup, group.next()) {
                     ok = warp_wait(scales_read + 8 * group.i, group.round ^ 1u, abort, a.status);
                     if (!ok) break;
-                    const int count = min(kScaleGroup, kb_count - kb0);
+                    const int count = min(kScaleGroup, kb_end - kb0);
                     uint32_t dst = row_dst + group.i * sizeof(ctl.row_scale[0]);
 #pragma unroll 1
                     for (int i = lane; i < rows; i += 32, dst += 32 * 4) {
@@ -407,13 +541,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     copy_async_arrive(scales + 8 * group.i);
                     if (lane == 0) {
-                        if (kb0 == 0)
+                        if (kb0 == kb_first)
                             ctl.notes[tile_no % kTileNotes] = {tile.row0, tile.rows, tile.col_tile};
                         mbar_arrive(scales + 8 * group.i);  // (releases the note)
                     }
                 }
             }
             copy_async_wait_all();
+        }
+        if (kSplit) {
+            cluster_arrive();
+            cluster_wait();
+            cluster_arrive();
         }
     } else {
         // ---- scaled sums: thread = one row, columns [32 c, 32 c + 32) of both blocks ----
@@ -427,7 +566,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         Ring<kStages> st;
         uint32_t tile_no = 0;
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++tile_no) {
+        if (kSplit && t0 >= tiles) {
+            cluster_arrive();
+            cluster_wait();
+            cluster_arrive();
+        }
+        for (int t = first_tile<kSplit>(t0); ok && t < tiles; t += tile_step<kSplit>(tiles), ++tile_no) {
             float acc[2][kAccCols];
 #pragma unroll
             for (int i = 0; i < kAccCols; ++i) acc[0][i] = acc[1][i] = 0.0f;
@@ -435,11 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // add along (with a branch around that, 32768 rows on 256 experts took
             // 1706 us instead of 1377), and after a wait that gave up the rest of
             // the tile runs on without waiting or arriving.
-            for (int kb0 = 0; kb0 < kb_count; kb0 += kScaleGroup, group.next()) {
+            for (int kb0 = kb_first; kb0 < kb_end; kb0 += kScaleGroup, group.next()) {
                 ok = ok && warp_wait(scales + 8 * group.i, group.round, abort, a.status);
                 uint32_t row_at = row_scale + group.i * sizeof(ctl.row_scale[0]);
                 uint32_t weight_at = weight_scale + group.i * sizeof(ctl.weight_scale[0]);
-                const int kb1 = min(kb0 + kScaleGroup, kb_count);
+                const int kb1 = min(kb0 + kScaleGroup, kb_end);
 #pragma unroll 1
                 for (int kb = kb0; kb < kb1; ++kb) {
                     const float sa = load_shared_f32(row_at);
@@ -471,10 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 mbar_arrive_if(scales_read + 8 * group.i, ok && lane == 0);
             }
+            const int row = quarter * 32 + lane;
+            const int rank = kSplit ? static_cast<int>(cluster_rank()) : 0;
+            if (kSplit)
+                join_parts(acc, base, ok ? ctl.notes[0].rows : 0, row, c * kAccCols * 4, rank, split);
             if (!ok) break;
             const TileNote tile = ctl.notes[tile_no % kTileNotes];
-            const int row = quarter * 32 + lane;
-            const bool store = row < tile.rows;
+            const bool store = row < tile.rows && row % split == rank;
             const int64_t grow = static_cast<int64_t>(tile.row0) + row;
             if (kGateUp) {
                 // Approximate exponential and division: off by a few units of
@@ -538,16 +685,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = quarter * 32 + (lane & ~3) + i;
-                        if (r < tile.rows && col < a.n)
+                        if (r < tile.rows && r % split == rank && col < a.n)
                             st_v4(a.out + (static_cast<int64_t>(tile.row0) + r) * a.n + col, p[i]);
                     }
                 }
             }
+            // (With the step alone the loop's state was kept over join_parts, and
+            // 228 bytes of sums spilled: 5 % of a split call.)
+            if (kSplit) break;
         }
     }
     __syncwarp();
     tcgen05_fence_before();
     __syncthreads();
+    if (kSplit) cluster_wait();  // no CTA reads this one's sums any more
     // After a wait that gave up: no copy may land once the CTA has exited, and
     // no product may run once its tensor memory is released. (Otherwise every
     // copy and product has been waited for.)
@@ -611,11 +762,76 @@ cudaError_t check_registers(const void* kernel) {
     return fa.numRegs >= kLaunchRegs ? cudaSuccess : cudaErrorInvalidDeviceFunction;
 }
 
-template <bool kGateUp>
+template <bool kGateUp, bool kSplit>
 cudaError_t check_registers_once() {
     static const cudaError_t result =
-        check_registers(reinterpret_cast<const void*>(&expert_kernel<kGateUp>));
+        check_registers(reinterpret_cast<const void*>(&expert_kernel<kGateUp, kSplit>));
     return result;
+}
+
+template <bool kGateUp, bool kSplit>
+cudaError_t launch(const ExpertArgs& a, const Maps& maps, int grid, size_t smem, cudaStream_t stream) {
+    auto kern = expert_kernel<kGateUp, kSplit>;
+    cudaError_t err = check_registers_once<kGateUp, kSplit>();
+    if (err != cudaSuccess) return err;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    return launch_dependent_clusters(kern, grid, a.split, kThreads, smem, stream, a, maps);
+}
+
+// Clusters of `split` (2, 4, 8) CTAs that the device holds at a time: fewer than
+// SMs / split, because a cluster's lie in one part (GPC) of it.
+int64_t resident_clusters(int split) {
+    struct Table {
+        int n[kMaxSplit + 1] = {};
+        Table() {
+            auto kern = expert_kernel<false, true>;
+            const size_t smem = 1024 + kStages * kStageBytes;
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem)) != cudaSuccess) {
+                (void)cudaGetLastError();
+                return;
+            }
+            for (int split = 2; split <= kMaxSplit; split *= 2) {
+                cudaLaunchConfig_t cfg{};
+                cfg.gridDim = dim3(static_cast<unsigned>(split));
+                cfg.blockDim = dim3(kThreads);
+                cfg.dynamicSmemBytes = smem;
+                cudaLaunchAttribute attr{};
+                attr.id = cudaLaunchAttributeClusterDimension;
+                attr.val.clusterDim.x = static_cast<unsigned>(split);
+                attr.val.clusterDim.y = 1;
+                attr.val.clusterDim.z = 1;
+                cfg.attrs = &attr;
+                cfg.numAttrs = 1;
+                if (cudaOccupancyMaxActiveClusters(&n[split], kern, &cfg) != cudaSuccess) {
+                    (void)cudaGetLastError();
+                    n[split] = 0;
+                }
+            }
+        }
+    };
+    static const Table table;
+    return table.n[split];
+}
+
+// CTAs to share a tile's blocks along K, where `most` tiles leave SMs idle. A
+// block takes a CTA 0.38 us then (the copies' latency over four stages); the
+// cluster's launch, its barriers and the joining take 2-3.5 us for few rows
+// and 4-5.5 us for 128, so at least 12 (16) blocks have to go to other CTAs:
+// one row of 7168 x 2 x 2048 took 26.2 us with 16 CTAs, 17.4 with clusters of
+// two, 13.6 of four; of 2048 x 7168 10.0, 9.6, 8.5; with two experts of those
+// and clusters of two 11.9 instead of 11.4 (not split); with 128 rows to each
+// of 16 tiles 56 blocks deep 27.2, 19.7, 15.7, but 14.1 instead of 11.9 16
+// blocks deep (not split). Clusters of 3, 5, 6 and 7 were between these or, at
+// 28 tiles, 30 % slower than four. A partition's SMs may not hold a cluster.
+int split_for(const ExpertArgs& a, int64_t most, int num_sms, bool partition) {
+    if (partition || 2 * most > num_sms) return 1;
+    int split = 1;
+    while (split < kMaxSplit && most <= resident_clusters(2 * split)) split *= 2;
+    const int rows = static_cast<int>(a.num_recv < kTileRows ? a.num_recv : kTileRows);
+    const int passed_on = a.k_blocks - (a.k_blocks + split - 1) / split;
+    return passed_on >= 12 + rows / 32 ? split : 1;
 }
 
 }  // namespace
@@ -626,7 +842,7 @@ int64_t expert_tiles_bound(int64_t num_recv, int E, int64_t n, bool gated) {
     return row_tiles * col_tiles;
 }
 
-cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_expert(ExpertArgs a, int num_sms, bool partition, cudaStream_t stream) {
     const bool gated = a.out_q != nullptr;
     a.k_blocks = static_cast<int>((a.k + kFp8Block - 1) / kFp8Block);
     a.col_tiles = gated ? a.n / 2 / kFp8Block : (a.n + kTileCols - 1) / kTileCols;
@@ -640,14 +856,14 @@ cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     // at most this many tiles, checked against kMaxTiles by the caller
     const int64_t most = expert_tiles_bound(a.num_recv, a.E, a.n, gated);
-    const int grid = static_cast<int>(most < num_sms ? most : num_sms);
+    a.split = split_for(a, most, num_sms, partition);
+    const int grid = static_cast<int>(a.split > 1 ? most * a.split : most < num_sms ? most : num_sms);
     const size_t smem = 1024 + kStages * kStageBytes + sizeof(int32_t) * (a.E + 1);
-    auto kern = gated ? expert_kernel<true> : expert_kernel<false>;
-    cudaError_t err = gated ? check_registers_once<true>() : check_registers_once<false>();
-    if (err != cudaSuccess) return err;
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
-    return launch_dependent(kern, grid, kThreads, smem, stream, a, maps);
+    if (a.split > 1)
+        return gated ? launch<true, true>(a, maps, grid, smem, stream)
+                     : launch<false, true>(a, maps, grid, smem, stream);
+    return gated ? launch<true, false>(a, maps, grid, smem, stream)
+                 : launch<false, false>(a, maps, grid, smem, stream);
 }
 
 }  // namespace ep

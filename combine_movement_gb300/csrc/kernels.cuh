@@ -255,9 +255,11 @@ struct ExpertArgs {
     int k_blocks;
     int col_tiles;
     int row_boxes;             // row boxes of 16, 32, ... that the rows can fill
+    int split;                 // CTAs that share a tile's blocks along K (a cluster)
 };
 
-cudaError_t launch_expert(ExpertArgs a, int num_sms, cudaStream_t stream);
+// `partition`: num_sms are those of an SM partition, not the device's.
+cudaError_t launch_expert(ExpertArgs a, int num_sms, bool partition, cudaStream_t stream);
 
 // Tiles of an expert product for any split of num_recv rows, at most; n counts
 // both halves of a gated one. Its tile indices go up to kMaxTiles.
@@ -308,19 +310,29 @@ class CallBytes {
 };
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(KArgs...), int grid, int block, size_t smem,
-                             cudaStream_t stream, Args&&... args) {
+cudaError_t launch_dependent_clusters(void (*kernel)(KArgs...), int grid, int cluster, int block,
+                                      size_t smem, cudaStream_t stream, Args&&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = launch_overlap_allowed(stream) ? 1 : 0;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = launch_overlap_allowed(stream) ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), int grid, int block, size_t smem,
+                             cudaStream_t stream, Args&&... args) {
+    return launch_dependent_clusters(kernel, grid, 1, block, smem, stream, std::forward<Args>(args)...);
 }
 
 // Dynamic shared memory that makes a CTA the only one resident on its SM

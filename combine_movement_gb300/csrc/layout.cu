@@ -302,20 +302,9 @@ constexpr int kClusterCtas = 8;  // portable cluster size
 // Non-portable cluster size for the wider variant (plan_layout_wide_cluster).
 constexpr int kWideClusterCtas = 16;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// shared::cluster address of `local` (this CTA's shared memory) in CTA `rank`
-__device__ __forceinline__ uint32_t cluster_map(uint32_t local, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-    return r;
 }
 __device__ __forceinline__ int32_t ld_cluster(uint32_t addr) {
     int32_t v;
