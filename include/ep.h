@@ -348,9 +348,12 @@ EP_API ep_status_t ep_dispatch_fp8(const uint16_t* x, int64_t T, int64_t H, int 
  * K a multiple of 16, N of 8; a, w and out 16-byte aligned; E * N and K below
  * 2^31 - 256, and (num_recv / 128 + min(num_recv, E)) * ceil(N / 256) at most
  * 2^30. Offsets that do not ascend from 0 or more to at most num_recv
- * report EP_ERR_BAD_SLOT, and the expert concerned is skipped. The SM budget
- * does not apply (it leaves SMs to work like this); a call into an SM
- * partition's stream uses the partition's SMs. */
+ * report EP_ERR_BAD_SLOT, and the expert concerned is skipped (where others
+ * claim rows twice, some of those may be left out too). The SM budget does not
+ * apply (it leaves SMs to work like this); a call into an SM partition's
+ * stream uses the partition's SMs. The order of a row's fp32 sums depends on
+ * num_recv, E, N, K and whether the stream is a partition's, on nothing else:
+ * equal calls give equal bits. */
 EP_API ep_status_t ep_expert_matmul_fp8(const uint8_t* a, const float* a_scale, int64_t num_recv,
                                         const int32_t* offsets, int E, const uint8_t* w,
                                         const float* w_scale, int64_t N, int64_t K, uint16_t* out,
