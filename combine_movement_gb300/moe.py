@@ -59,6 +59,10 @@ def forward_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     return ep.combine(out, slot, topk_w, status)
 
 
+# The movement's differentiable functions. Each one's backward is made of the
+# others (dispatch is linear, combine bilinear), so that every derivative has
+# a graph of its own where one is asked for (create_graph).
+
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, slot, num_recv):
@@ -69,42 +73,90 @@ class _Dispatch(torch.autograd.Function):
         # writes at T = 4096, H = 7168, top-8; which rows need it is known only on
         # the device.)
         recv_x = x.new_zeros((num_recv, x.shape[1]))
-        ep.ep_dispatch(x.contiguous(), slot, recv_x)
+        ep.ep_dispatch(x, slot, recv_x)
         return recv_x
 
     @staticmethod
     def backward(ctx, d_recv):
         (slot,) = ctx.saved_tensors
-        return ep.dispatch_grad(d_recv.contiguous(), slot), None, None
+        return _DispatchGrad.apply(d_recv.contiguous(), slot), None, None
+
+
+class _DispatchGrad(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, d_recv, slot):
+        ctx.save_for_backward(slot)
+        ctx.num_recv = d_recv.shape[0]
+        return ep.dispatch_grad(d_recv, slot)
+
+    @staticmethod
+    def backward(ctx, g):
+        (slot,) = ctx.saved_tensors
+        return _Dispatch.apply(g.contiguous(), slot, ctx.num_recv), None
 
 
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, expert_out, slot, topk_w):
-        expert_out = expert_out.contiguous()
         ctx.save_for_backward(expert_out, slot, topk_w)
         return ep.combine(expert_out, slot, topk_w)
 
     @staticmethod
     def backward(ctx, dy):
         expert_out, slot, topk_w = ctx.saved_tensors
-        # zeros: rows no entry maps to have no gradient
-        d_rows = torch.zeros_like(expert_out) if ctx.needs_input_grad[0] else None
-        d_w = torch.empty_like(topk_w) if ctx.needs_input_grad[2] else None
-        if d_rows is not None or d_w is not None:
-            ep.ep_combine_grad(dy.contiguous(), expert_out, slot, topk_w, d_rows, d_w)
+        need_rows, _, need_w = ctx.needs_input_grad
+        d_rows, d_w = _CombineGrad.apply(dy.contiguous(), expert_out, slot, topk_w, need_rows, need_w)
         return d_rows, None, d_w
 
 
+class _CombineGrad(torch.autograd.Function):
+    """(d_expert_out, d_topk_w) of combine; None for one that is not needed."""
+
+    @staticmethod
+    def forward(ctx, dy, expert_out, slot, topk_w, need_rows, need_w):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(dy, expert_out, slot, topk_w)
+        # zeros: rows no entry maps to have no gradient
+        d_rows = torch.zeros_like(expert_out) if need_rows else None
+        d_w = torch.empty_like(topk_w) if need_w else None
+        if need_rows or need_w:
+            ep.ep_combine_grad(dy, expert_out, slot, topk_w, d_rows, d_w)
+        return d_rows, d_w
+
+    @staticmethod
+    def backward(ctx, g_rows, g_w):
+        # d_rows[slot] = w dy and d_w = <dy, expert_out[slot]>, by each factor.
+        # dy's two parts are rounded to bf16 before their sum is, as any two
+        # gradients of a bf16 tensor that autograd adds.
+        dy, expert_out, slot, topk_w = ctx.saved_tensors
+        need_dy, need_rows, _, need_w = ctx.needs_input_grad[:4]
+        d_dy = d_rows = d_w = None
+        if g_rows is not None:
+            g_rows = g_rows.contiguous()
+            if need_dy:
+                d_dy = _Combine.apply(g_rows, slot, topk_w)
+            if need_w:
+                _, d_w = _CombineGrad.apply(dy, g_rows, slot, topk_w, False, True)
+        if g_w is not None:
+            g_w = g_w.contiguous()
+            if need_dy:
+                part = _Combine.apply(expert_out, slot, g_w)
+                d_dy = part if d_dy is None else d_dy + part
+            if need_rows:
+                d_rows, _ = _CombineGrad.apply(dy, expert_out, slot, g_w, True, False)
+        return d_dy, d_rows, None, d_w, None, None
+
+
 def dispatch(x: torch.Tensor, slot: torch.Tensor, num_recv: int) -> torch.Tensor:
-    """``ep.dispatch`` with a gradient for x. Rows of the result that no entry
-    maps to are zero."""
-    return _Dispatch.apply(x, slot, num_recv)
+    """``ep.dispatch`` with a gradient for x, of any order. Rows of the result
+    that no entry maps to are zero."""
+    return _Dispatch.apply(x.contiguous(), slot, num_recv)
 
 
 def combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tensor) -> torch.Tensor:
-    """``ep.combine`` with gradients for the expert rows and the weights."""
-    return _Combine.apply(expert_out, slot, topk_w)
+    """``ep.combine`` with gradients for the expert rows and the weights, of any
+    order."""
+    return _Combine.apply(expert_out.contiguous(), slot, topk_w)
 
 
 def _main() -> None:
