@@ -5,8 +5,9 @@ torch tensors become device pointers, the stream becomes its cudaStream_t
 handle. Every step of layout, dispatch and combine runs in the library's CUDA
 kernels; importing this module without the built library raises.
 
-Convenience wrappers (``get_dispatch_layout``, ``dispatch``, ``combine``)
-allocate outputs with torch and call the same entry points.
+Convenience wrappers (``get_dispatch_layout``, ``dispatch``, ``combine`` and
+those of the expert and gradient calls) allocate outputs with torch, on the
+stream that the call runs on, and call the same entry points.
 """
 from __future__ import annotations
 
@@ -470,17 +471,41 @@ def ep_get_status(status: torch.Tensor, stream=None) -> int:
 # --------------------------------------------------------------------------
 # allocating conveniences
 
+def _empty(shape, dtype, device, stream, keep: bool = True) -> torch.Tensor:
+    """torch.empty for an output (``keep``) or a workspace of a call on `stream`.
+
+    The memory comes from that stream's own part of the allocator: memory of
+    the current stream's may still be in use by work pending there, and a
+    result dropped early would go back to it while the call still runs. An
+    output may be used on the current stream too, so that stream is recorded
+    for it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(stream)  # (0 names the default stream)
+        stream = (torch.cuda.ExternalStream(raw, device) if raw
+                  else torch.cuda.default_stream(device))
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if keep:
+        t.record_stream(current)
+    return t
+
+
 def get_dispatch_layout(topk_idx: torch.Tensor, num_experts: int,
                         status: Optional[torch.Tensor] = None, stream=None
                         ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Returns (counts[E], offsets[E+1], slot[T,K]) as int32 CUDA tensors."""
     dev = topk_idx.device
     T, K = topk_idx.shape
-    counts = torch.empty(num_experts, dtype=torch.int32, device=dev)
-    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-    slot = torch.empty((T, K), dtype=torch.int32, device=dev)
+    counts = _empty(num_experts, torch.int32, dev, stream)
+    offsets = _empty(num_experts + 1, torch.int32, dev, stream)
+    slot = _empty((T, K), torch.int32, dev, stream)
     nbytes = ep_layout_workspace_bytes(T, K, num_experts)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    ws = _empty(nbytes, torch.uint8, dev, stream, keep=False) if nbytes else None
     ep_get_dispatch_layout(topk_idx, num_experts, counts, offsets, slot, ws, status, stream)
     return counts, offsets, slot
 
@@ -489,11 +514,11 @@ def dispatch(x: torch.Tensor, slot: torch.Tensor, num_recv: int,
              topk_w: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
              stream=None):
     """Returns recv_x [num_recv, H] (and recv_w, recv_src when topk_w is given)."""
-    recv_x = torch.empty((num_recv, x.shape[1]), dtype=x.dtype, device=x.device)
+    recv_x = _empty((num_recv, x.shape[1]), x.dtype, x.device, stream)
     recv_w = recv_src = None
     if topk_w is not None:
-        recv_w = torch.empty(num_recv, dtype=torch.float32, device=x.device)
-        recv_src = torch.empty(num_recv, dtype=torch.int32, device=x.device)
+        recv_w = _empty(num_recv, torch.float32, x.device, stream)
+        recv_src = _empty(num_recv, torch.int32, x.device, stream)
     ep_dispatch(x, slot, recv_x, topk_w, recv_w, recv_src, status, stream)
     return (recv_x, recv_w, recv_src) if topk_w is not None else recv_x
 
@@ -501,7 +526,7 @@ def dispatch(x: torch.Tensor, slot: torch.Tensor, num_recv: int,
 def combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tensor,
             status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     T = slot.shape[0]
-    y = torch.empty((T, expert_out.shape[1]), dtype=expert_out.dtype, device=expert_out.device)
+    y = _empty((T, expert_out.shape[1]), expert_out.dtype, expert_out.device, stream)
     ep_combine(expert_out, slot, topk_w, y, status, stream)
     return y
 
@@ -512,12 +537,12 @@ def dispatch_fp8(x: torch.Tensor, slot: torch.Tensor, num_recv: int,
     """Returns recv_q [num_recv, H] (e4m3) and recv_scale [num_recv, ceil(H / 128)]
     (and recv_w, recv_src when topk_w is given)."""
     H, dev = x.shape[1], x.device
-    recv_q = torch.empty((num_recv, H), dtype=torch.float8_e4m3fn, device=dev)
-    recv_scale = torch.empty((num_recv, -(-H // FP8_BLOCK)), dtype=torch.float32, device=dev)
+    recv_q = _empty((num_recv, H), _E4M3, dev, stream)
+    recv_scale = _empty((num_recv, -(-H // FP8_BLOCK)), _F32, dev, stream)
     recv_w = recv_src = None
     if topk_w is not None:
-        recv_w = torch.empty(num_recv, dtype=torch.float32, device=dev)
-        recv_src = torch.empty(num_recv, dtype=torch.int32, device=dev)
+        recv_w = _empty(num_recv, _F32, dev, stream)
+        recv_src = _empty(num_recv, _I32, dev, stream)
     ep_dispatch_fp8(x, slot, recv_q, recv_scale, topk_w, recv_w, recv_src, status, stream)
     return (recv_q, recv_scale) if topk_w is None else (recv_q, recv_scale, recv_w, recv_src)
 
@@ -527,8 +552,8 @@ def combine_grad(dy: torch.Tensor, expert_out: torch.Tensor, slot: torch.Tensor,
                  ) -> Tuple[torch.Tensor, torch.Tensor]:
     """Returns (d_expert_out [num_recv, H], d_topk_w [T, K]). Rows no entry
     maps to are left as allocated."""
-    d_expert_out = torch.empty_like(expert_out)
-    d_topk_w = torch.empty_like(topk_w)
+    d_expert_out = _empty(expert_out.shape, expert_out.dtype, expert_out.device, stream)
+    d_topk_w = _empty(topk_w.shape, topk_w.dtype, topk_w.device, stream)
     ep_combine_grad(dy, expert_out, slot, topk_w, d_expert_out, d_topk_w, status, stream)
     return d_expert_out, d_topk_w
 
@@ -536,7 +561,7 @@ def combine_grad(dy: torch.Tensor, expert_out: torch.Tensor, slot: torch.Tensor,
 def dispatch_grad(d_recv: torch.Tensor, slot: torch.Tensor, status: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """Returns dx [T, H], each token's receive-row gradients summed."""
-    dx = torch.empty((slot.shape[0], d_recv.shape[1]), dtype=d_recv.dtype, device=d_recv.device)
+    dx = _empty((slot.shape[0], d_recv.shape[1]), d_recv.dtype, d_recv.device, stream)
     ep_dispatch_grad(d_recv, slot, dx, status, stream)
     return dx
 
@@ -546,7 +571,7 @@ def expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Ten
                       status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Each expert's rows times its weights: bf16 [num_recv, N]. Rows no
     expert has (from offsets[E] on) are left as allocated."""
-    out = torch.empty((a.shape[0], w.shape[1]), dtype=torch.bfloat16, device=a.device)
+    out = _empty((a.shape[0], w.shape[1]), _BF16, a.device, stream)
     ep_expert_matmul_fp8(a, a_scale, offsets, w, w_scale, out, status, stream)
     return out
 
@@ -558,7 +583,7 @@ def expert_gate_up_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Te
     """silu(gate) * up of each expert's rows, quantised again: (e4m3
     [num_recv, I], fp32 scales [num_recv, I / 128]); the next product's rows."""
     R, width = a.shape[0], w.shape[1] // 2
-    out_q = torch.empty((R, width), dtype=torch.float8_e4m3fn, device=a.device)
-    out_scale = torch.empty((R, -(-width // FP8_BLOCK)), dtype=torch.float32, device=a.device)
+    out_q = _empty((R, width), _E4M3, a.device, stream)
+    out_scale = _empty((R, -(-width // FP8_BLOCK)), _F32, a.device, stream)
     ep_expert_gate_up_fp8(a, a_scale, offsets, w, w_scale, out_q, out_scale, status, stream)
     return out_q, out_scale
