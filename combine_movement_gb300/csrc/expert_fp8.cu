@@ -262,6 +262,13 @@ __device__ __forceinline__ void add_scaled(float (&acc)[kAccCols], int i0, const
     }
 }
 
+// 1 / v for v in [1, 2], within one unit.
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // p[i] of lane j <-> p[j] of lane i, i and j within each four lanes; `j` is
 // lane mod 4.
 __device__ __forceinline__ void transpose4(uint4 (&p)[4], int j) {
@@ -624,7 +631,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool store = row < tile.rows && row % split == rank;
             const int64_t grow = static_cast<int64_t>(tile.row0) + row;
             if (kGateUp) {
-                // Approximate exponential and division: off by a few units of
+                // silu(g) = g / (1 + e^-g) = g e^g / (1 + e^g): the one whose
+                // exponential does not overflow, so that the divisor lies in
+                // [1, 2] for every g and small values shrink into fp32's
+                // subnormals. (As g / (1 + e^-g) alone an approximate division
+                // gives 0 from g = -87.3 on, where the divisor passes 2^126.)
+                // Approximate exponential and reciprocal: off by a few units of
                 // 2^-24 (and |g| of them for the exponential), well inside what
                 // the sums before and the e4m3 rounding after are off by; exact
                 // ones took 2 us of a tile, and 8 us where lanes without a row
@@ -634,7 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kAccCols; ++i) {
                         const float g = acc[0][i];
-                        acc[0][i] = __fdividef(g, 1.0f + __expf(-g)) * acc[1][i];
+                        const float t = __expf(-fabsf(g));
+                        acc[0][i] = (g < 0.0f ? g * t : g) * reciprocal(1.0f + t) * acc[1][i];
                         top = max(top, abs_bits(acc[0][i]));
                     }
                 }

@@ -362,7 +362,10 @@ EP_API ep_status_t ep_expert_matmul_fp8(const uint8_t* a, const float* a_scale, 
 /* The experts' first product with its activation: w holds a gate half (rows
  * 0 .. I-1 of each expert) and an up half (rows I .. 2I-1);
  *   h[r, i] = silu(y[r, i]) * y[r, I + i],  silu(g) = g / (1 + exp(-g))
- * with y the product above in fp32, and h quantised in blocks of 128:
+ * with y the product above in fp32; silu's exponential and division are
+ * approximate, so that h is off by up to (8 + 2 |g|) 2^-23 of its value, and
+ * where exp(-|g|) is below 2^-126 by the spacing of fp32's subnormals besides.
+ * h is quantised in blocks of 128:
  *   m = max(max |h| of the block, 1e-30)  out_scale = m / 448
  *   out_q = e4m3_rne(h * (448 / m))
  *   w        e4m3 [E][2I][K]               w_scale  fp32 [E][2I/128][ceil(K/128)]
