@@ -615,7 +615,7 @@ ep_status_t ep_combine_grad(const uint16_t* dy, const uint16_t* expert_out, int6
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int n = sms_for_stream(sm_count, s);
     a.whole_gpu = n >= sm_count;
-    return from_cuda(ep::launch_combine_grad(a, n, s));
+    return from_cuda(ep::launch_combine_grad(a, n, sms_in_effect(sm_count), s));
 }
 
 ep_status_t ep_dispatch_fp8(const uint16_t* x, int64_t T, int64_t H, int K, const int32_t* slot,

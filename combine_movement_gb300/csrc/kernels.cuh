@@ -227,7 +227,10 @@ struct CombineGradArgs {
     bool whole_gpu;              // the budget covers every SM of the device
 };
 
-cudaError_t launch_combine_grad(const CombineGradArgs& a, int num_sms, cudaStream_t stream);
+// On num_sms SMs; `budget`: the SM budget, of which a partition's stream may
+// have fewer.
+cudaError_t launch_combine_grad(const CombineGradArgs& a, int num_sms, int budget,
+                                cudaStream_t stream);
 
 // Combine with the expert rows staged through a per-warp bulk-copy ring
 // (combine_tma.cu); K <= 8 only.

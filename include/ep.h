@@ -299,7 +299,8 @@ EP_API ep_status_t ep_combine(const uint16_t* expert_out, int64_t num_recv,
  *   d_expert_out  bf16 [num_recv][H]   d_topk_w      fp32 [T][K]
  * Either output may be null (not both). Masked entries get d_topk_w = 0;
  * rows of d_expert_out no entry maps to are left untouched. The same inputs
- * and SM budget give the same bits every time. */
+ * and SM budget give the same bits every time and on every stream of a device
+ * (no budget: the device's SMs). */
 EP_API ep_status_t ep_combine_grad(const uint16_t* dy, const uint16_t* expert_out, int64_t num_recv,
                                    const int32_t* slot, const float* topk_w, int64_t T, int64_t H,
                                    int K, uint16_t* d_expert_out, float* d_topk_w, int32_t* status,
