@@ -40,10 +40,13 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "../../include/ep.h"
 #include "combine_math.cuh"
 #include "fp8_math.cuh"
 #include "kernels.cuh"
+#include "per_device.cuh"
 #include "routing.cuh"
 #include "tcgen05.cuh"
 
@@ -738,16 +741,19 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// The driver's, looked up once (a failure is not kept).
 EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return static_cast<EncodeFn>(nullptr);
-        return reinterpret_cast<EncodeFn>(p);
-    }();
+    static std::atomic<EncodeFn> known{nullptr};
+    EncodeFn fn = known.load(std::memory_order_acquire);
+    if (fn != nullptr) return fn;
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    fn = reinterpret_cast<EncodeFn>(p);
+    known.store(fn, std::memory_order_release);
     return fn;
 }
 
@@ -768,64 +774,60 @@ bool encode_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t width,
 
 // The warpgroups' registers come out of those of the launch; with fewer the
 // ones that ask for more would wait forever.
-cudaError_t check_registers(const void* kernel) {
-    cudaFuncAttributes fa{};
-    const cudaError_t err = cudaFuncGetAttributes(&fa, kernel);
+template <bool kGateUp, bool kSplit>
+cudaError_t check_registers(int device) {
+    static PerDevice<bool> enough;
+    bool ok = false;
+    const cudaError_t err = enough.get(device, &ok, [](bool* found) {
+        cudaFuncAttributes fa{};
+        const cudaError_t e = cudaFuncGetAttributes(&fa, expert_kernel<kGateUp, kSplit>);
+        *found = fa.numRegs >= kLaunchRegs;
+        return e;
+    });
     if (err != cudaSuccess) return err;
-    return fa.numRegs >= kLaunchRegs ? cudaSuccess : cudaErrorInvalidDeviceFunction;
+    return ok ? cudaSuccess : cudaErrorInvalidDeviceFunction;
 }
 
 template <bool kGateUp, bool kSplit>
-cudaError_t check_registers_once() {
-    static const cudaError_t result =
-        check_registers(reinterpret_cast<const void*>(&expert_kernel<kGateUp, kSplit>));
-    return result;
-}
-
-template <bool kGateUp, bool kSplit>
-cudaError_t launch(const ExpertArgs& a, const Maps& maps, int grid, size_t smem, cudaStream_t stream) {
+cudaError_t launch(const ExpertArgs& a, const Maps& maps, int device, int grid, size_t smem,
+                   cudaStream_t stream) {
     auto kern = expert_kernel<kGateUp, kSplit>;
-    cudaError_t err = check_registers_once<kGateUp, kSplit>();
+    cudaError_t err = check_registers<kGateUp, kSplit>(device);
     if (err != cudaSuccess) return err;
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
     return launch_dependent_clusters(kern, grid, a.split, kThreads, smem, stream, a, maps);
 }
 
-// Clusters of `split` (2, 4, 8) CTAs that the device holds at a time: fewer than
-// SMs / split, because a cluster's lie in one part (GPC) of it.
-int64_t resident_clusters(int split) {
-    struct Table {
-        int n[kMaxSplit + 1] = {};
-        Table() {
-            auto kern = expert_kernel<false, true>;
-            const size_t smem = 1024 + kStages * kStageBytes;
-            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem)) != cudaSuccess) {
-                (void)cudaGetLastError();
-                return;
-            }
-            for (int split = 2; split <= kMaxSplit; split *= 2) {
-                cudaLaunchConfig_t cfg{};
-                cfg.gridDim = dim3(static_cast<unsigned>(split));
-                cfg.blockDim = dim3(kThreads);
-                cfg.dynamicSmemBytes = smem;
-                cudaLaunchAttribute attr{};
-                attr.id = cudaLaunchAttributeClusterDimension;
-                attr.val.clusterDim.x = static_cast<unsigned>(split);
-                attr.val.clusterDim.y = 1;
-                attr.val.clusterDim.z = 1;
-                cfg.attrs = &attr;
-                cfg.numAttrs = 1;
-                if (cudaOccupancyMaxActiveClusters(&n[split], kern, &cfg) != cudaSuccess) {
-                    (void)cudaGetLastError();
-                    n[split] = 0;
-                }
-            }
+// Clusters of 2, 4, 8 CTAs (n[2], n[4], n[8]) that a device holds at a time:
+// fewer than SMs / size, because a cluster's lie in one part (GPC) of it.
+struct ResidentClusters {
+    int n[kMaxSplit + 1];
+};
+
+cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
+    static PerDevice<ResidentClusters> table;
+    return table.get(device, clusters, [](ResidentClusters* found) {
+        auto kern = expert_kernel<false, true>;
+        const size_t smem = 1024 + kStages * kStageBytes;
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+        for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(static_cast<unsigned>(split));
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = static_cast<unsigned>(split);
+            attr.val.clusterDim.y = 1;
+            attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            err = cudaOccupancyMaxActiveClusters(&found->n[split], kern, &cfg);
         }
-    };
-    static const Table table;
-    return table.n[split];
+        return err;
+    });
 }
 
 // CTAs to share a tile's blocks along K, where `most` tiles leave SMs idle. A
@@ -838,13 +840,21 @@ int64_t resident_clusters(int split) {
 // of 16 tiles 56 blocks deep 27.2, 19.7, 15.7, but 14.1 instead of 11.9 16
 // blocks deep (not split). Clusters of 3, 5, 6 and 7 were between these or, at
 // 28 tiles, 30 % slower than four. A partition's SMs may not hold a cluster.
-int split_for(const ExpertArgs& a, int64_t most, int num_sms, bool partition) {
-    if (partition || 2 * most > num_sms) return 1;
-    int split = 1;
-    while (split < kMaxSplit && most <= resident_clusters(2 * split)) split *= 2;
+// (The split sets the order of the sums: a device that cannot be asked is an
+// error, not a reason for another one.)
+cudaError_t split_for(const ExpertArgs& a, int64_t most, int device, int num_sms, bool partition,
+                      int* split) {
+    *split = 1;
+    if (partition || 2 * most > num_sms) return cudaSuccess;
+    ResidentClusters clusters{};
+    const cudaError_t err = resident_clusters(device, &clusters);
+    if (err != cudaSuccess) return err;
+    int n = 1;
+    while (n < kMaxSplit && most <= clusters.n[2 * n]) n *= 2;
     const int rows = static_cast<int>(a.num_recv < kTileRows ? a.num_recv : kTileRows);
-    const int passed_on = a.k_blocks - (a.k_blocks + split - 1) / split;
-    return passed_on >= 12 + rows / 32 ? split : 1;
+    const int passed_on = a.k_blocks - (a.k_blocks + n - 1) / n;
+    if (passed_on >= 12 + rows / 32) *split = n;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -869,14 +879,17 @@ cudaError_t launch_expert(ExpertArgs a, int num_sms, bool partition, cudaStream_
         return cudaErrorInvalidValue;
     // at most this many tiles, checked against kMaxTiles by the caller
     const int64_t most = expert_tiles_bound(a.num_recv, a.E, a.n, gated);
-    a.split = split_for(a, most, num_sms, partition);
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err == cudaSuccess) err = split_for(a, most, device, num_sms, partition, &a.split);
+    if (err != cudaSuccess) return err;
     const int grid = static_cast<int>(a.split > 1 ? most * a.split : most < num_sms ? most : num_sms);
     const size_t smem = 1024 + kStages * kStageBytes + sizeof(int32_t) * (a.E + 1);
     if (a.split > 1)
-        return gated ? launch<true, true>(a, maps, grid, smem, stream)
-                     : launch<false, true>(a, maps, grid, smem, stream);
-    return gated ? launch<true, false>(a, maps, grid, smem, stream)
-                 : launch<false, false>(a, maps, grid, smem, stream);
+        return gated ? launch<true, true>(a, maps, device, grid, smem, stream)
+                     : launch<false, true>(a, maps, device, grid, smem, stream);
+    return gated ? launch<true, false>(a, maps, device, grid, smem, stream)
+                 : launch<false, false>(a, maps, device, grid, smem, stream);
 }
 
 }  // namespace ep

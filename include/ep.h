@@ -353,8 +353,10 @@ EP_API ep_status_t ep_dispatch_fp8(const uint16_t* x, int64_t T, int64_t H, int 
  * claim rows twice, some of those may be left out too). The SM budget does not
  * apply (it leaves SMs to work like this); a call into an SM partition's
  * stream uses the partition's SMs. The order of a row's fp32 sums depends on
- * num_recv, E, N, K and whether the stream is a partition's, on nothing else:
- * equal calls give equal bits. */
+ * num_recv, E, N, K, whether the stream is a partition's, and the device (its
+ * SMs, and how many clusters of CTAs it holds at a time), on nothing else: equal
+ * calls on one device give equal bits; another card, even of the same kind,
+ * may give others where the tiles are few. */
 EP_API ep_status_t ep_expert_matmul_fp8(const uint8_t* a, const float* a_scale, int64_t num_recv,
                                         const int32_t* offsets, int E, const uint8_t* w,
                                         const float* w_scale, int64_t N, int64_t K, uint16_t* out,
