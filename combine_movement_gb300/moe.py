@@ -50,7 +50,15 @@ def forward_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     x bf16 [T, H], topk_idx int64 [T, K] (-1: unused), topk_w fp32 [T, K];
     w_gate_up e4m3 [E, 2I, H] and w_down e4m3 [E, H, I] with their scales, as
     ``quantize_weights`` makes them. Everything is enqueued on the current
-    stream; nothing waits for the device."""
+    stream; nothing waits for the device. There is no gradient: where an input
+    asks for one, a backward pass through the result raises."""
+    args = (x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s_down, status)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args):
+        return _ForwardFp8.apply(*args)
+    return _forward_fp8(*args)
+
+
+def _forward_fp8(x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s_down, status):
     T, K = topk_idx.shape
     _, offsets, slot = ep.get_dispatch_layout(topk_idx, w_gate_up.shape[0], status)
     a, a_scale = ep.dispatch_fp8(x, slot, T * K, status=status)
@@ -59,9 +67,23 @@ def forward_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     return ep.combine(out, slot, topk_w, status)
 
 
+class _ForwardFp8(torch.autograd.Function):
+    """The layer in a graph, whose backward says that it has none."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return _forward_fp8(*args)
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise RuntimeError("forward_fp8 has no gradient: train with moe.dispatch, experts of "
+                           "your own and moe.combine")
+
+
 # The movement's differentiable functions. Each one's backward is made of the
 # others (dispatch is linear, combine bilinear), so that every derivative has
 # a graph of its own where one is asked for (create_graph).
+
 
 class _Dispatch(torch.autograd.Function):
     @staticmethod
