@@ -592,10 +592,14 @@ ep_status_t ep_combine_grad(const uint16_t* dy, const uint16_t* expert_out, int6
                             const int32_t* slot, const float* topk_w, int64_t T, int64_t H, int K,
                             uint16_t* d_expert_out, float* d_topk_w, int32_t* status, void* stream) {
     ep::ApiRange range("ep_combine_grad");
-    const ep_status_t st = check_combine(expert_out, num_recv, slot, T, H, K, dy, status);
+    // the receive rows it cannot do without: expert_out for d_topk_w, else those
+    // it writes
+    const ep_status_t st = check_combine(d_topk_w != nullptr ? expert_out : d_expert_out, num_recv,
+                                         slot, T, H, K, dy, status);
     if (st != EP_OK || T == 0) return st;
     if (topk_w == nullptr || (d_expert_out == nullptr && d_topk_w == nullptr)) return EP_ERR_INVALID;
-    if (!aligned(topk_w, 4) || !aligned(d_expert_out, 16) || !aligned(d_topk_w, 4))
+    if (!aligned(topk_w, 4) || !aligned(expert_out, 16) || !aligned(d_expert_out, 16) ||
+        !aligned(d_topk_w, 4))
         return EP_ERR_INVALID;
     const ep::CallBytes call_bytes(T * K * 2 * H);
     int sm_count = 0, smem_optin = 0;

@@ -367,18 +367,22 @@ def ep_dispatch_fp8(x: torch.Tensor, slot: torch.Tensor, recv_q: torch.Tensor,
         raise EPError(code, "ep_dispatch_fp8")
 
 
-def ep_combine_grad(dy: torch.Tensor, expert_out: torch.Tensor, slot: torch.Tensor,
+def ep_combine_grad(dy: torch.Tensor, expert_out: Optional[torch.Tensor], slot: torch.Tensor,
                     topk_w: torch.Tensor, d_expert_out: Optional[torch.Tensor],
                     d_topk_w: Optional[torch.Tensor], status: Optional[torch.Tensor] = None,
                     stream=None) -> None:
+    """expert_out may be None where d_topk_w is."""
     T, H = dy.shape
-    K, R = slot.shape[1], expert_out.shape[0]
+    if expert_out is None and d_expert_out is None:
+        raise ValueError("expert_out: expected a tensor")
+    K, R = slot.shape[1], (d_expert_out if expert_out is None else expert_out).shape[0]
     rows, pairs = (R, H), (T, K)
-    py, pe = _arg(dy, _BF16, (T, H), "dy"), _arg(expert_out, _BF16, rows, "expert_out")
+    py = _arg(dy, _BF16, (T, H), "dy")
+    pe = None if expert_out is None else _arg(expert_out, _BF16, rows, "expert_out")
     ps, pw = _arg(slot, _I32, pairs, "slot"), _arg(topk_w, _F32, pairs, "topk_w")
     pde = None if d_expert_out is None else _arg(d_expert_out, _BF16, rows, "d_expert_out")
     pdw = None if d_topk_w is None else _arg(d_topk_w, _F32, pairs, "d_topk_w")
-    if not (dy.is_cuda and expert_out.is_cuda and slot.is_cuda and topk_w.is_cuda
+    if not (dy.is_cuda and (pe is None or expert_out.is_cuda) and slot.is_cuda and topk_w.is_cuda
             and (pde is None or d_expert_out.is_cuda) and (pdw is None or d_topk_w.is_cuda)):
         raise ValueError("ep_combine_grad: expected a CUDA tensor for every argument")
     code = lib.ep_combine_grad(

@@ -120,28 +120,35 @@ class _DispatchGrad(torch.autograd.Function):
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, expert_out, slot, topk_w):
-        ctx.save_for_backward(expert_out, slot, topk_w)
+        # the rows (470 MB at T = 4096, H = 7168, top-8) are for the weights'
+        # gradient alone
+        rows = expert_out if ctx.needs_input_grad[2] else None
+        ctx.save_for_backward(rows, slot, topk_w)
+        ctx.num_recv = expert_out.shape[0]
         return ep.combine(expert_out, slot, topk_w)
 
     @staticmethod
     def backward(ctx, dy):
         expert_out, slot, topk_w = ctx.saved_tensors
         need_rows, _, need_w = ctx.needs_input_grad
-        d_rows, d_w = _CombineGrad.apply(dy.contiguous(), expert_out, slot, topk_w, need_rows, need_w)
+        d_rows, d_w = _CombineGrad.apply(dy.contiguous(), expert_out, slot, topk_w,
+                                         ctx.num_recv if need_rows else None, need_w)
         return d_rows, None, d_w
 
 
 class _CombineGrad(torch.autograd.Function):
-    """(d_expert_out, d_topk_w) of combine; None for one that is not needed."""
+    """(d_expert_out of num_recv rows, d_topk_w) of combine; None for the one
+    that is not needed (num_recv None, need_w False). expert_out may be None
+    without need_w."""
 
     @staticmethod
-    def forward(ctx, dy, expert_out, slot, topk_w, need_rows, need_w):
+    def forward(ctx, dy, expert_out, slot, topk_w, num_recv, need_w):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(dy, expert_out, slot, topk_w)
         # zeros: rows no entry maps to have no gradient
-        d_rows = torch.zeros_like(expert_out) if need_rows else None
+        d_rows = None if num_recv is None else dy.new_zeros((num_recv, dy.shape[1]))
         d_w = torch.empty_like(topk_w) if need_w else None
-        if need_rows or need_w:
+        if d_rows is not None or need_w:
             ep.ep_combine_grad(dy, expert_out, slot, topk_w, d_rows, d_w)
         return d_rows, d_w
 
@@ -158,14 +165,14 @@ class _CombineGrad(torch.autograd.Function):
             if need_dy:
                 d_dy = _Combine.apply(g_rows, slot, topk_w)
             if need_w:
-                _, d_w = _CombineGrad.apply(dy, g_rows, slot, topk_w, False, True)
+                _, d_w = _CombineGrad.apply(dy, g_rows, slot, topk_w, None, True)
         if g_w is not None:
             g_w = g_w.contiguous()
             if need_dy:
                 part = _Combine.apply(expert_out, slot, g_w)
                 d_dy = part if d_dy is None else d_dy + part
             if need_rows:
-                d_rows, _ = _CombineGrad.apply(dy, expert_out, slot, g_w, True, False)
+                d_rows, _ = _CombineGrad.apply(dy, None, slot, g_w, expert_out.shape[0], False)
         return d_dy, d_rows, None, d_w, None, None
 
 
