@@ -597,9 +597,8 @@ ep_status_t ep_combine_grad(const uint16_t* dy, const uint16_t* expert_out, int6
     const ep_status_t st = check_combine(d_topk_w != nullptr ? expert_out : d_expert_out, num_recv,
                                          slot, T, H, K, dy, status);
     if (st != EP_OK || T == 0) return st;
-    if (topk_w == nullptr || (d_expert_out == nullptr && d_topk_w == nullptr)) return EP_ERR_INVALID;
-    if (!aligned(topk_w, 4) || !aligned(expert_out, 16) || !aligned(d_expert_out, 16) ||
-        !aligned(d_topk_w, 4))
+    if (topk_w == nullptr || !aligned(topk_w, 4) || !aligned(expert_out, 16) ||
+        !aligned(d_expert_out, 16) || !aligned(d_topk_w, 4))
         return EP_ERR_INVALID;
     const ep::CallBytes call_bytes(T * K * 2 * H);
     int sm_count = 0, smem_optin = 0;

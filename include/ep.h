@@ -297,7 +297,7 @@ EP_API ep_status_t ep_combine(const uint16_t* expert_out, int64_t num_recv,
  *   d_topk_w[t,k] = sum over h of dy[t,h] * expert_out[slot[t,k], h]  (fp32)
  *   dy            bf16 [T][H]          expert_out    bf16 [num_recv][H]
  *   d_expert_out  bf16 [num_recv][H]   d_topk_w      fp32 [T][K]
- * Either output may be null (not both); expert_out may be
+ * Either output may be null (not both, unless num_recv is 0); expert_out may be
  * null where d_topk_w is. Masked entries get d_topk_w = 0;
  * rows of d_expert_out no entry maps to are left untouched. The same inputs
  * and SM budget give the same bits every time and on every stream of a device

@@ -26,7 +26,8 @@ def test_refused(ep, bad):
 
 
 # (past the checks; what follows needs a GPU)
-@pytest.mark.parametrize("good", [dict(e=None, dw=None), dict(de=None), dict(dw=None)])
+@pytest.mark.parametrize("good", [dict(e=None, dw=None), dict(de=None), dict(dw=None),
+                                  dict(R=0, e=None, de=None, dw=None)])
 @pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up")
 def test_accepted(ep, good):
     assert call(ep, **good) == ep.EP_ERR_CUDA

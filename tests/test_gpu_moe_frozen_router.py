@@ -57,3 +57,18 @@ def test_the_call_without_rows(mods, T, H, K):
     ep.ep_combine_grad(dy, None, slot, w, got, None)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_no_rows_at_all(mods):
+    """A buffer of no rows has no address: still an output, with nothing in it."""
+    ep, moe = mods
+    slot = torch.full((5, 2), -1, dtype=torch.int32, device="cuda")
+    w = torch.rand((5, 2), device="cuda")
+    rows = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    y = moe.combine(rows, slot, w)
+    y.sum().backward()
+    assert rows.grad.shape == (0, 64) and bool((y == 0).all())
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    slot[3, 1] = 0  # past the end of no rows
+    ep.ep_combine_grad(torch.zeros_like(y.detach()), None, slot, w, rows.detach(), None, status)
+    assert ep.ep_get_status(status) == ep.EP_ERR_BAD_SLOT
