@@ -41,6 +41,13 @@ def quantize_weights(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     return q, torch.stack(scales)
 
 
+# The movement's calls take their sizes from one tensor; the others' are checked
+# here, before anything reads past one.
+def _check_shape(t: torch.Tensor, shape: Tuple[int, ...], what: str) -> None:
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+
+
 def forward_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
                 w_gate_up: torch.Tensor, s_gate_up: torch.Tensor, w_down: torch.Tensor,
                 s_down: torch.Tensor, status: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -60,6 +67,8 @@ def forward_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
 
 def _forward_fp8(x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s_down, status):
     T, K = topk_idx.shape
+    _check_shape(topk_w, (T, K), "topk_w")
+    _check_shape(x, (T, x.shape[-1]), "x")
     _, offsets, slot = ep.get_dispatch_layout(topk_idx, w_gate_up.shape[0], status)
     a, a_scale = ep.dispatch_fp8(x, slot, T * K, status=status)
     h, h_scale = ep.expert_gate_up_fp8(a, a_scale, offsets, w_gate_up, s_gate_up, status)
@@ -179,12 +188,15 @@ class _CombineGrad(torch.autograd.Function):
 def dispatch(x: torch.Tensor, slot: torch.Tensor, num_recv: int) -> torch.Tensor:
     """``ep.dispatch`` with a gradient for x, of any order. Rows of the result
     that no entry maps to are zero."""
+    _check_shape(slot, (x.shape[0], slot.shape[-1]), "slot")
     return _Dispatch.apply(x.contiguous(), slot, num_recv)
 
 
 def combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tensor) -> torch.Tensor:
     """``ep.combine`` with gradients for the expert rows and the weights, of any
     order."""
+    _check_shape(slot, (topk_w.shape[0], slot.shape[-1]), "slot")
+    _check_shape(topk_w, tuple(slot.shape), "topk_w")
     return _Combine.apply(expert_out.contiguous(), slot, topk_w)
 
 
