@@ -588,6 +588,29 @@ ep_status_t ep_dispatch_grad(const uint16_t* d_recv, int64_t num_recv, const int
                        static_cast<cudaStream_t>(stream));
 }
 
+ep_status_t ep_clear_unused_rows(uint16_t* rows, int64_t num_recv, const int32_t* slot, int64_t T,
+                                 int64_t H, int K, int32_t* status, void* stream) {
+    ep::ApiRange range("ep_clear_unused_rows");
+    if (T < 0 || H <= 0 || H % 8 != 0 || K < 1 || K > EP_MAX_TOPK || num_recv < 0)
+        return EP_ERR_INVALID;
+    if (!pairs_fit(T, K) || num_recv > kMaxPairs || !row_fits(H)) return EP_ERR_UNSUPPORTED;
+    if (num_recv == 0) return EP_OK;
+    if (rows == nullptr || (T > 0 && slot == nullptr)) return EP_ERR_INVALID;
+    if (!aligned(rows, 16) || !aligned(slot, 4) || !aligned(status, 4)) return EP_ERR_INVALID;
+    const ep::CallBytes call_bytes(T * K * 2 * H);
+    int sm_count = 0, smem_optin = 0;
+    if (!device_limits(&sm_count, &smem_optin)) return EP_ERR_CUDA;
+    ep::ClearRowsArgs a{};
+    a.rows = rows;
+    a.num_recv = num_recv;
+    a.H = H;
+    a.slot = slot;
+    a.entries = T * K;
+    a.status = status;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return from_cuda(ep::launch_clear_rows(a, sms_for_stream(sm_count, s), s));
+}
+
 ep_status_t ep_combine_grad(const uint16_t* dy, const uint16_t* expert_out, int64_t num_recv,
                             const int32_t* slot, const float* topk_w, int64_t T, int64_t H, int K,
                             uint16_t* d_expert_out, float* d_topk_w, int32_t* status, void* stream) {

@@ -232,6 +232,20 @@ struct CombineGradArgs {
 cudaError_t launch_combine_grad(const CombineGradArgs& a, int num_sms, int budget,
                                 cudaStream_t stream);
 
+// Zeros in the rows of a receive buffer that no entry maps to (clear_rows.cu).
+struct ClearRowsArgs {
+    uint16_t* rows;      // bf16 [num_recv][H]
+    int64_t num_recv;
+    int64_t H;
+    const int32_t* slot;
+    int64_t entries;     // T * K
+    int32_t* status;
+    // set by launch_clear_rows
+    int log_ctas;        // the grid's
+};
+
+cudaError_t launch_clear_rows(ClearRowsArgs a, int num_sms, cudaStream_t stream);
+
 // Combine with the expert rows staged through a per-warp bulk-copy ring
 // (combine_tma.cu); K <= 8 only.
 bool combine_tma_supported(int K);

@@ -117,6 +117,8 @@ def _load() -> ctypes.CDLL:
     lib.ep_combine_grad.restype = i32
     lib.ep_dispatch_grad.argtypes = [p, i64, p, i64, i64, i32, p, p, p]
     lib.ep_dispatch_grad.restype = i32
+    lib.ep_clear_unused_rows.argtypes = [p, i64, p, i64, i64, i32, p, p]
+    lib.ep_clear_unused_rows.restype = i32
     lib.ep_expert_matmul_fp8.argtypes = [p, p, i64, p, i32, p, p, i64, i64, p, p, p]
     lib.ep_expert_matmul_fp8.restype = i32
     lib.ep_expert_gate_up_fp8.argtypes = [p, p, i64, p, i32, p, p, i64, i64, p, p, p, p]
@@ -405,6 +407,19 @@ def ep_dispatch_grad(d_recv: torch.Tensor, slot: torch.Tensor, dx: torch.Tensor,
                                 _stream(stream))
     if code != EP_OK:
         raise EPError(code, "ep_dispatch_grad")
+
+
+def ep_clear_unused_rows(rows: torch.Tensor, slot: torch.Tensor,
+                         status: Optional[torch.Tensor] = None, stream=None) -> None:
+    (R, H), (T, K) = rows.shape, slot.shape
+    pr, ps = _arg(rows, _BF16, (R, H), "rows"), _arg(slot, _I32, (T, K), "slot")
+    if not (rows.is_cuda and slot.is_cuda):
+        raise _off_gpu(rows=rows, slot=slot)
+    code = lib.ep_clear_unused_rows(pr, R, ps, T, H, K,
+                                    None if status is None else _ptr(status, _I32, "status"),
+                                    _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_clear_unused_rows")
 
 
 def ep_expert_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor,

@@ -89,28 +89,45 @@ class _ForwardFp8(torch.autograd.Function):
                            "your own and moe.combine")
 
 
+def _dispatch(x, slot, num_recv):
+    recv_x = ep.dispatch(x, slot, num_recv)
+    # what the experts make of rows no entry maps to meets a zero gradient in
+    # their backward, and zero times whatever the memory held (NaN, infinities)
+    # is not zero
+    ep.ep_clear_unused_rows(recv_x, slot)
+    return recv_x
+
+
+def _combine_grad(dy, expert_out, slot, topk_w, num_recv, need_w):
+    """(d_expert_out of num_recv rows, d_topk_w) of combine; None for the one
+    that is not needed (num_recv None, need_w False). expert_out may be None
+    without need_w."""
+    d_rows = None if num_recv is None else dy.new_empty((num_recv, dy.shape[1]))
+    d_w = torch.empty_like(topk_w) if need_w else None
+    if d_rows is not None or need_w:
+        ep.ep_combine_grad(dy, expert_out, slot, topk_w, d_rows, d_w)
+    if d_rows is not None:  # rows no entry maps to have no gradient
+        ep.ep_clear_unused_rows(d_rows, slot)
+    return d_rows, d_w
+
+
 # The movement's differentiable functions. Each one's backward is made of the
 # others (dispatch is linear, combine bilinear), so that every derivative has
-# a graph of its own where one is asked for (create_graph).
+# a graph of its own where one is asked for (create_graph, which leaves the
+# gradient mode on in a backward).
 
 
 class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, slot, num_recv):
         ctx.save_for_backward(slot)
-        # zeros: what the experts make of rows no entry maps to meets a zero
-        # gradient in their backward, and zero times whatever the memory held
-        # (NaN, infinities) is not zero. (Clearing all rows costs 470 MB of
-        # writes at T = 4096, H = 7168, top-8; which rows need it is known only on
-        # the device.)
-        recv_x = x.new_zeros((num_recv, x.shape[1]))
-        ep.ep_dispatch(x, slot, recv_x)
-        return recv_x
+        return _dispatch(x, slot, num_recv)
 
     @staticmethod
     def backward(ctx, d_recv):
         (slot,) = ctx.saved_tensors
-        return _DispatchGrad.apply(d_recv.contiguous(), slot), None, None
+        grad = _DispatchGrad.apply if torch.is_grad_enabled() else ep.dispatch_grad
+        return grad(d_recv.contiguous(), slot), None, None
 
 
 class _DispatchGrad(torch.autograd.Function):
@@ -140,26 +157,18 @@ class _Combine(torch.autograd.Function):
     def backward(ctx, dy):
         expert_out, slot, topk_w = ctx.saved_tensors
         need_rows, _, need_w = ctx.needs_input_grad
-        d_rows, d_w = _CombineGrad.apply(dy.contiguous(), expert_out, slot, topk_w,
-                                         ctx.num_recv if need_rows else None, need_w)
+        grad = _CombineGrad.apply if torch.is_grad_enabled() else _combine_grad
+        d_rows, d_w = grad(dy.contiguous(), expert_out, slot, topk_w,
+                           ctx.num_recv if need_rows else None, need_w)
         return d_rows, None, d_w
 
 
 class _CombineGrad(torch.autograd.Function):
-    """(d_expert_out of num_recv rows, d_topk_w) of combine; None for the one
-    that is not needed (num_recv None, need_w False). expert_out may be None
-    without need_w."""
-
     @staticmethod
     def forward(ctx, dy, expert_out, slot, topk_w, num_recv, need_w):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(dy, expert_out, slot, topk_w)
-        # zeros: rows no entry maps to have no gradient
-        d_rows = None if num_recv is None else dy.new_zeros((num_recv, dy.shape[1]))
-        d_w = torch.empty_like(topk_w) if need_w else None
-        if d_rows is not None or need_w:
-            ep.ep_combine_grad(dy, expert_out, slot, topk_w, d_rows, d_w)
-        return d_rows, d_w
+        return _combine_grad(dy, expert_out, slot, topk_w, num_recv, need_w)
 
     @staticmethod
     def backward(ctx, g_rows, g_w):

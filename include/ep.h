@@ -317,6 +317,18 @@ EP_API ep_status_t ep_dispatch_grad(const uint16_t* d_recv, int64_t num_recv, co
                                     int64_t T, int64_t H, int K, uint16_t* dx, int32_t* status,
                                     void* stream);
 
+/* Zeros in the rows of a receive buffer that no (t,k) maps to, which ep_dispatch
+ * and ep_combine_grad leave as they are (masked entries, and buffers of more
+ * rows than there are entries, have such rows). For what is computed from the
+ * whole buffer: in the experts' weight gradients such a row of recv_x meets
+ * its row of d_expert_out, and zero times an old NaN is not zero.
+ *   rows  bf16 [num_recv][H]           slot  int32 [T][K]
+ * Rows an entry maps to are left untouched. Runs on the SM budget. T == 0 is
+ * valid: every row is cleared. */
+EP_API ep_status_t ep_clear_unused_rows(uint16_t* rows, int64_t num_recv, const int32_t* slot,
+                                        int64_t T, int64_t H, int K, int32_t* status,
+                                        void* stream);
+
 /* ---- the experts, in 8 bits --------------------------------------------------
  * Rows and weights as e4m3 bytes with one fp32 scale for each block of 128
  * values, so that value = byte * scale: rows in blocks of 1 x 128 along
