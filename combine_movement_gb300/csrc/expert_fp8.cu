@@ -36,7 +36,8 @@
 //    add: 1.5-3 % slower (the products then read their rows twice, all of
 //    shared memory's bandwidth);
 //  - pairs of CTAs on tiles of 256 rows (cta_group::2: two thirds of the bytes
-//    from L2): 2-6 % faster at 1000 rows an expert, 5-30 % slower below 130.
+//    from L2): 4-5 % faster at 1000 rows an expert, 18-33 % slower at 128 and
+//    fewer.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
