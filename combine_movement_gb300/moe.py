@@ -6,7 +6,8 @@ with its activation, their down product, combine.
 
 ``dispatch`` and ``combine`` are the bf16 movement as differentiable
 functions, for training with experts of the caller's own; their backward
-passes are ``ep_dispatch_grad`` and ``ep_combine_grad``.
+passes are ``ep_dispatch_grad`` and ``ep_combine_grad``, and receive rows that
+no entry maps to are zero in both directions (``ep_clear_unused_rows``).
 
 ``python -m combine_movement_gb300.moe`` builds a layer with random weights,
 runs a batch through it, compares some tokens with the layer in fp32 and
