@@ -346,6 +346,42 @@ ep_status_t run_expert(const ep::ExpertArgs& x, cudaStream_t stream) {
     return from_cuda(ep::launch_expert(x, part > 0 ? part : sm_count, part > 0, stream));
 }
 
+// Host checks shared by ep_route and its gradient.
+ep_status_t check_route(const void* logits, int logits_type, int64_t T, int E, int K, int score,
+                        const void* idx, const void* w) {
+    if (T < 0 || E < 1 || K < 1 || K > EP_MAX_TOPK || K > E) return EP_ERR_INVALID;
+    if ((logits_type != EP_BF16 && logits_type != EP_F32) ||
+        (score != EP_SCORE_SOFTMAX && score != EP_SCORE_SIGMOID))
+        return EP_ERR_INVALID;
+    if (E > EP_MAX_EXPERTS || !pairs_fit(T, K)) return EP_ERR_UNSUPPORTED;
+    if (T == 0) return EP_OK;
+    if (logits == nullptr || idx == nullptr || w == nullptr) return EP_ERR_INVALID;
+    if (!aligned(logits, logits_type == EP_F32 ? 4 : 2) || !aligned(idx, 8) || !aligned(w, 4))
+        return EP_ERR_INVALID;
+    return EP_OK;
+}
+
+// Host checks of a dense product: `n` of w's rows, `cols` of the output's columns.
+constexpr int64_t kMaxLinear = kMaxPairs - 256;
+ep_status_t check_linear(int64_t M, int64_t N, int64_t K, bool gated, const int32_t* status) {
+    if (M < 0 || N <= 0 || K <= 0 || K % 8 != 0 || !aligned(status, 4)) return EP_ERR_INVALID;
+    if (M > kMaxLinear || N > kMaxLinear / (gated ? 2 : 1) || K > kMaxLinear)
+        return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+bool linear_fits(int64_t m, int64_t n) {
+    return ((m + 127) / 128) * ((n + 63) / 64) <= ep::kMaxTiles;
+}
+
+ep_status_t run_linear(const ep::LinearArgs& x, cudaStream_t stream) {
+    int sm_count = 0, smem_optin = 0;
+    if (!device_limits(&sm_count, &smem_optin)) return EP_ERR_CUDA;
+    const int part = ep::partition_sms(stream);
+    const ep::CallBytes call_bytes(2 * x.m * (x.a_by_k ? x.n : x.k));
+    return from_cuda(ep::launch_linear(x, part > 0 ? part : sm_count, part > 0, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -709,6 +745,193 @@ ep_status_t ep_expert_gate_up_fp8(const uint8_t* a, const float* a_scale, int64_
     x.out_q = out_q;
     x.out_scale = out_scale;
     return run_expert(x, static_cast<cudaStream_t>(stream));
+}
+
+ep_status_t ep_route(const void* logits, int logits_type, int64_t T, int E, int K, const float* bias,
+                     int score, int groups, int topk_groups, int group_score, int renormalize,
+                     float scale, int64_t* topk_idx, float* topk_w, void* stream) {
+    ep::ApiRange range("ep_route");
+    const ep_status_t st = check_route(logits, logits_type, T, E, K, score, topk_idx, topk_w);
+    if (st != EP_OK && st != EP_ERR_UNSUPPORTED) return st;
+    if (groups < 1 || E % groups != 0 || topk_groups < 1 || topk_groups > groups ||
+        static_cast<int64_t>(topk_groups) * (E / groups) < K ||
+        (group_score != EP_GROUP_MAX && group_score != EP_GROUP_TOP2))
+        return EP_ERR_INVALID;
+    if (st != EP_OK || groups > EP_MAX_GROUPS) return EP_ERR_UNSUPPORTED;
+    if (!aligned(bias, 4)) return EP_ERR_INVALID;
+    if (T == 0) return EP_OK;
+    ep::RouteArgs a{};
+    a.logits = logits;
+    a.bf16_logits = logits_type == EP_BF16;
+    a.T = T;
+    a.E = E;
+    a.K = K;
+    a.bias = bias;
+    a.softmax = score == EP_SCORE_SOFTMAX;
+    // every group stays: as without groups
+    a.groups = topk_groups == groups ? 1 : groups;
+    a.topk_groups = topk_groups == groups ? 1 : topk_groups;
+    a.group_top2 = group_score == EP_GROUP_TOP2;
+    a.renormalize = renormalize != 0;
+    a.scale = scale;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    return from_cuda(ep::launch_route(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_route_grad(const float* d_topk_w, const void* logits, int logits_type,
+                          const int64_t* topk_idx, int64_t T, int E, int K, int score,
+                          int renormalize, float scale, void* d_logits, int32_t* status,
+                          void* stream) {
+    ep::ApiRange range("ep_route_grad");
+    const ep_status_t st = check_route(logits, logits_type, T, E, K, score, topk_idx, d_topk_w);
+    if (st != EP_OK) return st;
+    if (!aligned(status, 4)) return EP_ERR_INVALID;
+    if (T == 0) return EP_OK;
+    if (d_logits == nullptr || !aligned(d_logits, logits_type == EP_F32 ? 4 : 2))
+        return EP_ERR_INVALID;
+    ep::RouteArgs a{};
+    a.logits = logits;
+    a.bf16_logits = logits_type == EP_BF16;
+    a.T = T;
+    a.E = E;
+    a.K = K;
+    a.softmax = score == EP_SCORE_SOFTMAX;
+    a.renormalize = renormalize != 0;
+    a.scale = scale;
+    a.topk_idx = const_cast<int64_t*>(topk_idx);
+    a.d_topk_w = d_topk_w;
+    a.d_logits = d_logits;
+    a.status = status;
+    return from_cuda(ep::launch_route_grad(a, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_linear(const uint16_t* x, int64_t M, int64_t K, const uint16_t* w, int64_t N,
+                      const float* bias, int activation, const void* residual, int y_type, void* y,
+                      uint16_t* z, int32_t* status, void* stream) {
+    ep::ApiRange range("ep_linear");
+    if (activation < EP_ACT_NONE || activation > EP_ACT_SWIGLU ||
+        (y_type != EP_BF16 && y_type != EP_F32))
+        return EP_ERR_INVALID;
+    const bool gated = activation == EP_ACT_SWIGLU;
+    const ep_status_t st = check_linear(M, N, K, gated, status);
+    if (st != EP_OK) return st;
+    if (!linear_fits(M, N)) return EP_ERR_UNSUPPORTED;
+    if (M == 0) return EP_OK;
+    if (x == nullptr || w == nullptr || y == nullptr) return EP_ERR_INVALID;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(residual, 16) ||
+        !aligned(z, 16) || !aligned(bias, 4))
+        return EP_ERR_INVALID;
+    ep::LinearArgs a{};
+    a.a = x;
+    a.b = w;
+    a.a_pitch = K;
+    a.b_pitch = K;
+    a.m = M;
+    a.n = N;
+    a.k = K;
+    a.bias = bias;
+    a.act = activation;
+    a.residual = residual;
+    a.out_f32 = y_type == EP_F32;
+    a.out = y;
+    a.z = z;
+    a.status = status;
+    return run_linear(a, static_cast<cudaStream_t>(stream));
+}
+
+ep_status_t ep_linear_act_grad(const void* dy, int dy_type, const uint16_t* z, int64_t M, int64_t N,
+                               int activation, uint16_t* dz, int64_t pitch, float* d_bias,
+                               void* stream) {
+    ep::ApiRange range("ep_linear_act_grad");
+    if (activation < EP_ACT_NONE || activation > EP_ACT_SWIGLU ||
+        (dy_type != EP_BF16 && dy_type != EP_F32))
+        return EP_ERR_INVALID;
+    const bool gated = activation == EP_ACT_SWIGLU;
+    const ep_status_t st = check_linear(M, N, 8, gated, nullptr);
+    if (st != EP_OK) return st;
+    // (strips of 32 columns and more are the grid's second dimension)
+    if (N > 65535 * 32) return EP_ERR_UNSUPPORTED;
+    if (dz != nullptr && (pitch % 8 != 0 || pitch < (gated ? 2 * N : N))) return EP_ERR_INVALID;
+    if (dz != nullptr && pitch > kMaxPairs) return EP_ERR_UNSUPPORTED;
+    if (!aligned(dy, 16) || !aligned(z, 16) || !aligned(dz, 16) || !aligned(d_bias, 4))
+        return EP_ERR_INVALID;
+    if (M > 0 && (dy == nullptr || (activation != EP_ACT_NONE && z == nullptr)))
+        return EP_ERR_INVALID;
+    if (d_bias == nullptr && (M == 0 || dz == nullptr)) return M == 0 ? EP_OK : EP_ERR_INVALID;
+    const ep::CallBytes call_bytes(2 * M * N);
+    int sm_count = 0, smem_optin = 0;
+    if (!device_limits(&sm_count, &smem_optin)) return EP_ERR_CUDA;
+    ep::ActGradArgs a{};
+    a.dy = dy;
+    a.dy_f32 = dy_type == EP_F32;
+    a.z = z;
+    a.m = M;
+    a.n = N;
+    a.act = activation;
+    a.dz = dz;
+    a.pitch = pitch;
+    a.d_bias = d_bias;
+    return from_cuda(ep::launch_act_grad(a, sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+ep_status_t ep_linear_grad_input(const uint16_t* dz, int64_t pitch, int64_t M, int64_t N,
+                                 const uint16_t* w, int64_t K, uint16_t* dx, int32_t* status,
+                                 void* stream) {
+    ep::ApiRange range("ep_linear_grad_input");
+    const ep_status_t st = check_linear(M, N, K, false, status);
+    if (st != EP_OK) return st;
+    if (pitch % 8 != 0 || pitch < N) return EP_ERR_INVALID;
+    if (!linear_fits(M, K) || pitch > kMaxPairs) return EP_ERR_UNSUPPORTED;
+    if (M == 0) return EP_OK;
+    if (dz == nullptr || w == nullptr || dx == nullptr) return EP_ERR_INVALID;
+    if (!aligned(dz, 16) || !aligned(w, 16) || !aligned(dx, 16)) return EP_ERR_INVALID;
+    ep::LinearArgs a{};
+    a.a = dz;
+    a.b = w;
+    a.b_by_k = true;
+    a.a_pitch = pitch;
+    a.b_pitch = K;
+    a.m = M;
+    a.n = K;
+    a.k = N;
+    a.out = dx;
+    a.status = status;
+    return run_linear(a, static_cast<cudaStream_t>(stream));
+}
+
+ep_status_t ep_linear_grad_weight(const uint16_t* dz, int64_t pitch, int64_t M, int64_t N,
+                                  const uint16_t* x, int64_t K, int d_w_type, void* d_w,
+                                  int accumulate, int32_t* status, void* stream) {
+    ep::ApiRange range("ep_linear_grad_weight");
+    if (d_w_type != EP_BF16 && d_w_type != EP_F32) return EP_ERR_INVALID;
+    const ep_status_t st = check_linear(M, N, K, false, status);
+    if (st != EP_OK) return st;
+    if (pitch % 8 != 0 || pitch < N) return EP_ERR_INVALID;
+    if (!linear_fits(N, K) || pitch > kMaxPairs) return EP_ERR_UNSUPPORTED;
+    if (d_w == nullptr || !aligned(d_w, 16)) return EP_ERR_INVALID;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        if (accumulate) return EP_OK;
+        const size_t bytes = (d_w_type == EP_F32 ? 4 : 2) * static_cast<size_t>(N) * K;
+        return from_cuda(cudaMemsetAsync(d_w, 0, bytes, s));
+    }
+    if (dz == nullptr || x == nullptr || !aligned(dz, 16) || !aligned(x, 16)) return EP_ERR_INVALID;
+    ep::LinearArgs a{};
+    a.a = dz;
+    a.b = x;
+    a.a_by_k = true;
+    a.b_by_k = true;
+    a.a_pitch = pitch;
+    a.b_pitch = K;
+    a.m = N;
+    a.n = K;
+    a.k = M;
+    a.residual = accumulate ? d_w : nullptr;
+    a.out_f32 = d_w_type == EP_F32;
+    a.out = d_w;
+    a.status = status;
+    return run_linear(a, s);
 }
 
 ep_status_t ep_get_status(const int32_t* status, void* stream) {

@@ -41,15 +41,13 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-
 #include "../../include/ep.h"
 #include "combine_math.cuh"
 #include "fp8_math.cuh"
 #include "kernels.cuh"
 #include "per_device.cuh"
+#include "product.cuh"
 #include "routing.cuh"
-#include "tcgen05.cuh"
 
 namespace ep {
 namespace {
@@ -113,94 +111,6 @@ struct Control {
     uint32_t amax[2][kAccGroups][kTileRows];
     float row_scale[kScaleGroups][kScaleGroup][kTileRows];
     alignas(8) float weight_scale[kScaleGroups][kScaleGroup][2];
-};
-
-__device__ __forceinline__ uint32_t load_shared(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float load_shared_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float2 load_shared_f32x2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ void store_shared(uint32_t addr, uint32_t v) {
-    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ void store_shared_v4(uint32_t addr, float4 v) {
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z),
-                 "f"(v.w)
-                 : "memory");
-}
-__device__ __forceinline__ float4 load_shared_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 load_cluster_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// Cluster barrier, reached by a warp's lanes in their roles' branches. Every
-// thread passes it twice, whatever its CTA found to do: the hardware's barrier
-// has no limit of its own, the waits before it have.
-__device__ __forceinline__ void cluster_arrive() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// Wait of a whole warp on a barrier; false, in every lane, once a lane gave up
-// after kWaitLimitNs or another warp did (the word at `abort`). The timer is
-// slow to read, so the first tries go without.
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort,
-                                          int32_t* status) {
-    for (int i = 0; i < 256; ++i)
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-        const bool late = global_timer_ns() - t0 > kWaitLimitNs;
-        if (late) {
-            store_shared(abort, 1);
-            set_status(status, EP_ERR_TIMEOUT);
-        }
-        if (__any_sync(0xFFFFFFFFu, late || load_shared(abort) != 0)) return false;
-    }
-}
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort,
-                                          int32_t* status) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    return wait_slow(bar, parity, abort, status);
-}
-
-// Position in a ring of N: index, and the parity of its current round.
-template <int N>
-struct Ring {
-    uint32_t i = 0, round = 0;
-    __device__ __forceinline__ void next() {
-        if (++i == N) {
-            i = 0;
-            round ^= 1u;
-        }
-    }
 };
 
 // One tile: up to 128 rows of an expert times two blocks of its weight rows.
@@ -735,27 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tcgen05_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-}
-
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's, looked up once (a failure is not kept).
-EncodeFn encode_fn() {
-    static std::atomic<EncodeFn> known{nullptr};
-    EncodeFn fn = known.load(std::memory_order_acquire);
-    if (fn != nullptr) return fn;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-        return nullptr;
-    fn = reinterpret_cast<EncodeFn>(p);
-    known.store(fn, std::memory_order_release);
-    return fn;
 }
 
 // A byte matrix [rows][width], read in boxes of box_rows x 128 bytes laid out

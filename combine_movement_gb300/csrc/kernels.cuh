@@ -283,6 +283,74 @@ cudaError_t launch_expert(ExpertArgs a, int num_sms, bool partition, cudaStream_
 int64_t expert_tiles_bound(int64_t num_recv, int E, int64_t n, bool gated);
 constexpr int kMaxTiles = 1 << 30;
 
+// ---- the router --------------------------------------------------------------
+
+struct RouteArgs {
+    const void* logits;        // fp32 or bf16 [T][E]
+    bool bf16_logits;
+    int64_t T;
+    int E;
+    int K;
+    const float* bias;         // [E], nullable
+    bool softmax;              // else sigmoid
+    int groups;
+    int topk_groups;
+    bool group_top2;           // a group is worth its two largest, else its largest
+    bool renormalize;
+    float scale;
+    int64_t* topk_idx;         // [T][K]; the gradient reads it
+    float* topk_w;             // [T][K]
+    // the gradient's
+    const float* d_topk_w;     // [T][K]
+    void* d_logits;            // [T][E], the logits' type
+    int32_t* status;
+};
+
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+cudaError_t launch_route_grad(const RouteArgs& a, cudaStream_t stream);
+
+// ---- dense products ----------------------------------------------------------
+
+// d[m, n] = sum over k of a[m, k] * b[n, k], and an epilogue (linear.cu).
+struct LinearArgs {
+    const uint16_t* a;         // bf16 [m][k], or [k][m] where a_by_k
+    const uint16_t* b;         // bf16 [n][k], or [k][n] where b_by_k
+    bool a_by_k, b_by_k;
+    int64_t a_pitch, b_pitch;  // values from one row to the next, multiples of 8
+    int64_t m, n, k;           // n: of d's columns (gated: of one half)
+    const float* bias;         // [n] (gated: [2n]), nullable
+    int act;                   // ep_activation_t
+    const void* residual;      // [m][n] of out's type, nullable
+    bool out_f32;              // else bf16
+    void* out;                 // [m][n]
+    uint16_t* z;               // bf16 [m][n] (gated: [m][2n]), nullable
+    int32_t* status;
+    // set by launch_linear
+    int k_blocks;
+    int64_t row_tiles, col_tiles;
+    int split;                 // CTAs that share a tile's blocks along k (a cluster)
+};
+
+// `partition`: num_sms are those of an SM partition, not the device's.
+cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_t stream);
+
+// Tiles of an m x n output (gated: n columns of each half); up to kMaxTiles.
+int64_t linear_tiles(int64_t m, int64_t n, bool gated);
+
+// dz = dy act'(z) and its column sums (linear_grad.cu).
+struct ActGradArgs {
+    const void* dy;            // bf16 or fp32 [m][n]
+    bool dy_f32;
+    const uint16_t* z;         // bf16 [m][n] (gated: [m][2n]); unused without act
+    int64_t m, n;              // n: of dy's columns
+    int act;
+    uint16_t* dz;              // bf16 [m][pitch], nullable
+    int64_t pitch;
+    float* d_bias;             // [n] (gated: [2n]), nullable
+};
+
+cudaError_t launch_act_grad(const ActGradArgs& a, int num_sms, cudaStream_t stream);
+
 // Launch a kernel of the hot path. With programmatic dependent launch the
 // launch may start while the previous kernel on the stream finishes: its CTAs
 // become resident and wait in griddep_wait(), which every such kernel calls

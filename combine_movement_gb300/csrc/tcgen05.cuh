@@ -1,5 +1,5 @@
 // tcgen05.cuh -- inline-PTX primitives of the fifth-generation tensor cores
-// on sm_103a (tensor memory, tcgen05.mma on e4m3 operands, 2-D tensor copies),
+// on sm_103a (tensor memory, tcgen05.mma on e4m3 and bf16 operands, 2-D tensor copies),
 // next to the bulk-copy primitives of ptx.cuh. Written from the public PTX
 // ISA.
 #pragma once
@@ -70,6 +70,17 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t smem_addr) {
     return kLeading | kStride | kVersion | kSwizzle128 | ((smem_addr & 0x3FFFFu) >> 4);
 }
 
+// The same of a tile whose rows run along M (or N): groups of 64 bf16 values
+// along it, each 64 rows of 128 bytes along K, 8192 bytes apart; groups of 8
+// rows 1024 bytes apart. A step of 16 values along K adds 2048 to the address.
+__device__ __forceinline__ uint64_t operand_desc_by_k(uint32_t smem_addr) {
+    constexpr uint64_t kLeading = uint64_t{8192 >> 4} << 16;
+    constexpr uint64_t kStride = uint64_t{1024 >> 4} << 32;
+    constexpr uint64_t kVersion = uint64_t{1} << 46;
+    constexpr uint64_t kSwizzle128 = uint64_t{2} << 61;
+    return kLeading | kStride | kVersion | kSwizzle128 | ((smem_addr & 0x3FFFFu) >> 4);
+}
+
 // Instruction descriptor: fp32 accumulators, both operands e4m3 and K-major.
 constexpr uint32_t mma_desc_e4m3(uint32_t m, uint32_t n) {
     return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
@@ -82,6 +93,24 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+
+// Instruction descriptor: fp32 accumulators, both operands bf16, each K-major or
+// (by_k) with its rows along M or N.
+constexpr uint32_t mma_desc_bf16(uint32_t m, uint32_t n, bool a_by_k, bool b_by_k) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_by_k ? 1u << 15 : 0u) | (b_by_k ? 1u << 16 : 0u) |
+           ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// D[tmem] = A B^T (+ D where `accumulate`), 16 values along K; one thread.
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t desc,
+                                         bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(accumulate))
         : "memory");
 }

@@ -6,8 +6,8 @@ handle. Every step of layout, dispatch and combine runs in the library's CUDA
 kernels; importing this module without the built library raises.
 
 Convenience wrappers (``get_dispatch_layout``, ``dispatch``, ``combine`` and
-those of the expert and gradient calls) allocate outputs with torch, on the
-stream that the call runs on, and call the same entry points.
+those of the expert, router, product and gradient calls) allocate outputs with
+torch, on the stream that the call runs on, and call the same entry points.
 """
 from __future__ import annotations
 
@@ -31,6 +31,12 @@ EP_ERR_WORKSPACE = 7
 
 EP_MAX_TOPK = 32
 EP_MAX_EXPERTS = 4096
+EP_MAX_GROUPS = 32
+
+# Names of the C ABI's choices.
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 
 # Values that share one scale in the 8-bit operands.
 FP8_BLOCK = 128
@@ -123,6 +129,19 @@ def _load() -> ctypes.CDLL:
     lib.ep_expert_matmul_fp8.restype = i32
     lib.ep_expert_gate_up_fp8.argtypes = [p, p, i64, p, i32, p, p, i64, i64, p, p, p, p]
     lib.ep_expert_gate_up_fp8.restype = i32
+    f32 = ctypes.c_float
+    lib.ep_route.argtypes = [p, i32, i64, i32, i32, p, i32, i32, i32, i32, i32, f32, p, p, p]
+    lib.ep_route.restype = i32
+    lib.ep_route_grad.argtypes = [p, p, i32, p, i64, i32, i32, i32, i32, f32, p, p, p]
+    lib.ep_route_grad.restype = i32
+    lib.ep_linear.argtypes = [p, i64, i64, p, i64, p, i32, p, i32, p, p, p, p]
+    lib.ep_linear.restype = i32
+    lib.ep_linear_act_grad.argtypes = [p, i32, p, i64, i64, i32, p, i64, p, p]
+    lib.ep_linear_act_grad.restype = i32
+    lib.ep_linear_grad_input.argtypes = [p, i64, i64, i64, p, i64, p, p, p]
+    lib.ep_linear_grad_input.restype = i32
+    lib.ep_linear_grad_weight.argtypes = [p, i64, i64, i64, p, i64, i32, p, i32, p, p]
+    lib.ep_linear_grad_weight.restype = i32
     lib.ep_sm_partition.argtypes = [i32, ctypes.POINTER(p), ctypes.POINTER(p),
                                     ctypes.POINTER(i32), ctypes.POINTER(i32)]
     lib.ep_sm_partition.restype = i32
@@ -467,6 +486,152 @@ def ep_expert_gate_up_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch
         raise EPError(code, "ep_expert_gate_up_fp8")
 
 
+# The router's and the dense products' tensors are all on the current device,
+# whose stream the call runs on.
+def _on_gpu(name: str, *tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor for every argument")
+    current = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"{name}: expected every tensor on the current device ({current}), "
+                             f"got one on {t.device}")
+
+
+def _choice(table: dict, key: str, what: str) -> int:
+    if key not in table:
+        raise ValueError(f"{what}: expected one of {', '.join(table)}, got {key!r}")
+    return table[key]
+
+
+def _type(t: torch.Tensor, what: str) -> int:
+    """ep_type_t of a tensor that may be bf16 or fp32."""
+    if t.dtype is _BF16:
+        return 0
+    if t.dtype is _F32:
+        return 1
+    raise ValueError(f"{what}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _rows(t: torch.Tensor, what: str) -> Tuple[int, int]:
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected two dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def ep_route(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+             bias: Optional[torch.Tensor] = None, score: str = "softmax", groups: int = 1,
+             topk_groups: int = 1, group_score: str = "max", renormalize: bool = True,
+             scale: float = 1.0, stream=None) -> None:
+    (T, E), (_, K) = _rows(logits, "logits"), _rows(topk_idx, "topk_idx")
+    kind = _type(logits, "logits")
+    pl = _arg(logits, logits.dtype, (T, E), "logits")
+    pi, pw = _arg(topk_idx, torch.int64, (T, K), "topk_idx"), _arg(topk_w, _F32, (T, K), "topk_w")
+    pb = None if bias is None else _arg(bias, _F32, (E,), "bias")
+    how, worth = _choice(SCORES, score, "score"), _choice(GROUP_SCORES, group_score, "group_score")
+    _on_gpu("ep_route", logits, topk_idx, topk_w, bias)
+    code = lib.ep_route(pl, kind, T, E, K, pb, how, groups, topk_groups, worth,
+                        1 if renormalize else 0, scale, pi, pw, _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_route")
+
+
+def ep_route_grad(d_topk_w: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
+                  d_logits: torch.Tensor, score: str = "softmax", renormalize: bool = True,
+                  scale: float = 1.0, status: Optional[torch.Tensor] = None, stream=None) -> None:
+    (T, E), (_, K) = _rows(logits, "logits"), _rows(topk_idx, "topk_idx")
+    kind = _type(logits, "logits")
+    pl = _arg(logits, logits.dtype, (T, E), "logits")
+    pd = _arg(d_topk_w, _F32, (T, K), "d_topk_w")
+    pi = _arg(topk_idx, torch.int64, (T, K), "topk_idx")
+    po = _arg(d_logits, logits.dtype, (T, E), "d_logits")
+    how = _choice(SCORES, score, "score")
+    _on_gpu("ep_route_grad", d_topk_w, logits, topk_idx, d_logits, status)
+    code = lib.ep_route_grad(pd, pl, kind, pi, T, E, K, how, 1 if renormalize else 0, scale, po,
+                             None if status is None else _ptr(status, _I32, "status"),
+                             _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_route_grad")
+
+
+def ep_linear(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor,
+              bias: Optional[torch.Tensor] = None, activation: str = "none",
+              residual: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None) -> None:
+    (M, K), (wide, _) = _rows(x, "x"), _rows(w, "w")
+    act = _choice(ACTIVATIONS, activation, "activation")
+    N = wide
+    if activation == "swiglu":
+        if wide % 2:
+            raise ValueError(f"w: expected a gate half and an up half, got {wide} rows")
+        N = wide // 2
+    kind = _type(y, "y")
+    px, pw = _arg(x, _BF16, (M, K), "x"), _arg(w, _BF16, (wide, K), "w")
+    py = _arg(y, y.dtype, (M, N), "y")
+    pb = None if bias is None else _arg(bias, _F32, (wide,), "bias")
+    pr = None if residual is None else _arg(residual, y.dtype, (M, N), "residual")
+    pz = None if z is None else _arg(z, _BF16, (M, wide), "z")
+    _on_gpu("ep_linear", x, w, y, bias, residual, z, status)
+    code = lib.ep_linear(px, M, K, pw, N, pb, act, pr, kind, py, pz,
+                         None if status is None else _ptr(status, _I32, "status"), _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_linear")
+
+
+def linear_pitch(n: int) -> int:
+    """Columns of the dz of a product with n weight rows: its rows start on 16 bytes."""
+    return -(-n // 8) * 8
+
+
+def ep_linear_act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], dz: Optional[torch.Tensor],
+                       d_bias: Optional[torch.Tensor] = None, activation: str = "none",
+                       stream=None) -> None:
+    """z may be None without an activation; dz is [M, linear_pitch(rows of w)]."""
+    M, N = _rows(dy, "dy")
+    act = _choice(ACTIVATIONS, activation, "activation")
+    wide, kind = 2 * N if activation == "swiglu" else N, _type(dy, "dy")
+    if z is None and activation != "none":
+        raise ValueError("z: expected a tensor")
+    pd = _arg(dy, dy.dtype, (M, N), "dy")
+    pz = None if z is None else _arg(z, _BF16, (M, wide), "z")
+    po = None if dz is None else _arg(dz, _BF16, (M, linear_pitch(wide)), "dz")
+    pb = None if d_bias is None else _arg(d_bias, _F32, (wide,), "d_bias")
+    _on_gpu("ep_linear_act_grad", dy, z, dz, d_bias)
+    code = lib.ep_linear_act_grad(pd, kind, pz, M, N, act, po, linear_pitch(wide), pb,
+                                  _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_linear_act_grad")
+
+
+def ep_linear_grad_input(dz: torch.Tensor, w: torch.Tensor, dx: torch.Tensor,
+                         status: Optional[torch.Tensor] = None, stream=None) -> None:
+    (M, pitch), (N, K) = _rows(dz, "dz"), _rows(w, "w")
+    pd = _arg(dz, _BF16, (M, linear_pitch(N)), "dz")
+    pw, px = _arg(w, _BF16, (N, K), "w"), _arg(dx, _BF16, (M, K), "dx")
+    _on_gpu("ep_linear_grad_input", dz, w, dx, status)
+    code = lib.ep_linear_grad_input(pd, pitch, M, N, pw, K, px,
+                                    None if status is None else _ptr(status, _I32, "status"),
+                                    _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_linear_grad_input")
+
+
+def ep_linear_grad_weight(dz: torch.Tensor, x: torch.Tensor, d_w: torch.Tensor,
+                          accumulate: bool = False, status: Optional[torch.Tensor] = None,
+                          stream=None) -> None:
+    (M, pitch), (N, K) = _rows(dz, "dz"), _rows(d_w, "d_w")
+    kind = _type(d_w, "d_w")
+    pd = _arg(dz, _BF16, (M, linear_pitch(N)), "dz")
+    px, pw = _arg(x, _BF16, (M, K), "x"), _arg(d_w, d_w.dtype, (N, K), "d_w")
+    _on_gpu("ep_linear_grad_weight", dz, x, d_w, status)
+    code = lib.ep_linear_grad_weight(pd, pitch, M, N, px, K, kind, pw, 1 if accumulate else 0,
+                                     None if status is None else _ptr(status, _I32, "status"),
+                                     _stream(stream))
+    if code != EP_OK:
+        raise EPError(code, "ep_linear_grad_weight")
+
+
 def ep_sm_partition(num_sms: int) -> Tuple[int, Optional[int], int, int]:
     """(stream, rest_stream, sms, rest_sms) of an SM partition of at least
     num_sms SMs on the current device; the streams are raw cudaStream_t
@@ -606,3 +771,36 @@ def expert_gate_up_fp8(a: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Te
     out_scale = _empty((R, -(-width // FP8_BLOCK)), _F32, a.device, stream)
     ep_expert_gate_up_fp8(a, a_scale, offsets, w, w_scale, out_q, out_scale, status, stream)
     return out_q, out_scale
+
+
+def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
+          score: str = "softmax", groups: int = 1, topk_groups: int = 1, group_score: str = "max",
+          renormalize: bool = True, scale: float = 1.0, stream=None
+          ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Returns (topk_idx int64 [T, k], topk_w fp32 [T, k])."""
+    T, dev = logits.shape[0], logits.device
+    topk_idx = _empty((T, k), torch.int64, dev, stream)
+    topk_w = _empty((T, k), _F32, dev, stream)
+    ep_route(logits, topk_idx, topk_w, bias, score, groups, topk_groups, group_score, renormalize,
+             scale, stream)
+    return topk_idx, topk_w
+
+
+def route_grad(d_topk_w: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
+               score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+               status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Returns d_logits [T, E], of the logits' type."""
+    d_logits = _empty(logits.shape, logits.dtype, logits.device, stream)
+    ep_route_grad(d_topk_w, logits, topk_idx, d_logits, score, renormalize, scale, status, stream)
+    return d_logits
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           activation: str = "none", residual: Optional[torch.Tensor] = None,
+           out_dtype: torch.dtype = torch.bfloat16, status: Optional[torch.Tensor] = None,
+           stream=None) -> torch.Tensor:
+    """act(x w^T + bias) + residual: [M, N] of out_dtype (bf16 or fp32)."""
+    n = w.shape[0] // 2 if activation == "swiglu" else w.shape[0]
+    y = _empty((x.shape[0], n), out_dtype, x.device, stream)
+    ep_linear(x, w, y, bias, activation, residual, None, status, stream)
+    return y

@@ -9,6 +9,12 @@ functions, for training with experts of the caller's own; their backward
 passes are ``ep_dispatch_grad`` and ``ep_combine_grad``, and receive rows that
 no entry maps to are zero in both directions (``ep_clear_unused_rows``).
 
+``route`` makes the routing table and its weights from a router's logits;
+``linear`` is a product in bf16 with bias, activation and residual, for those
+logits and for an expert that every token goes through: with h =
+linear(x, gate_up, activation="swiglu"), linear(h, down, residual=y) adds it to
+combine's y. Both are differentiable.
+
 ``python -m combine_movement_gb300.moe`` builds a layer with random weights,
 runs a batch through it, compares some tokens with the layer in fp32 and
 prints the time of each call as one JSON line.
@@ -208,6 +214,86 @@ def combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tensor) 
     _check_shape(slot, (topk_w.shape[0], slot.shape[-1]), "slot")
     _check_shape(topk_w, tuple(slot.shape), "topk_w")
     return _Combine.apply(expert_out.contiguous(), slot, topk_w)
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, bias, kind):
+        idx, w = ep.route(logits, k, bias, **kind)
+        ctx.save_for_backward(logits, idx)
+        ctx.kind = {n: kind[n] for n in ("score", "renormalize", "scale")}
+        ctx.mark_non_differentiable(idx)
+        return idx, w
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, _, d_w):
+        logits, idx = ctx.saved_tensors
+        return ep.route_grad(d_w.contiguous(), logits, idx, **ctx.kind), None, None, None
+
+
+def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
+          score: str = "softmax", groups: int = 1, topk_groups: int = 1, group_score: str = "max",
+          renormalize: bool = True, scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``ep.route`` -- (topk_idx int64 [T, k], topk_w fp32 [T, k]), what layout and
+    combine take -- with a gradient of topk_w for the logits, once (a second
+    derivative raises). The bias, for the choice alone, has none."""
+    _check_shape(logits, (logits.shape[0], logits.shape[-1]), "logits")
+    return _Route.apply(logits.contiguous(), k, None if bias is None else bias.detach(),
+                        dict(score=score, groups=groups, topk_groups=topk_groups,
+                             group_score=group_score, renormalize=renormalize, scale=scale))
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, activation, out_dtype):
+        M, wide = x.shape[0], w.shape[0]
+        y = x.new_empty((M, wide // 2 if activation == "swiglu" else wide), dtype=out_dtype)
+        need = any(ctx.needs_input_grad[:3])
+        z = x.new_empty((M, wide)) if need and activation != "none" else None
+        ep.ep_linear(x, w, y, bias, activation, residual, z)
+        # the rows are for the weight's gradient alone, the weight for the rows'
+        ctx.save_for_backward(x if ctx.needs_input_grad[1] else None,
+                              w if ctx.needs_input_grad[0] else None, z)
+        ctx.activation, ctx.wide = activation, wide
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, z = ctx.saved_tensors
+        need_x, need_w, need_bias, need_residual = ctx.needs_input_grad[:4]
+        dy, wide, act = dy.contiguous(), ctx.wide, ctx.activation
+        M = dy.shape[0]
+        dx = d_w = d_bias = None
+        dz = dy
+        if act != "none" or dy.dtype is not torch.bfloat16 or wide % 8:
+            dz = dy.new_empty((M, ep.linear_pitch(wide)), dtype=torch.bfloat16)
+        if need_bias:
+            d_bias = dy.new_empty(wide, dtype=torch.float32)
+        if (need_x or need_w) and dz is not dy or need_bias:
+            ep.ep_linear_act_grad(dy, z, None if dz is dy else dz, d_bias, act)
+        if need_x:
+            dx = dz.new_empty((M, w.shape[1]))
+            ep.ep_linear_grad_input(dz, w, dx)
+        if need_w:
+            d_w = dz.new_empty((wide, x.shape[1]))
+            ep.ep_linear_grad_weight(dz, x, d_w)
+        return dx, d_w, d_bias, dy if need_residual else None, None, None
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           activation: str = "none", residual: Optional[torch.Tensor] = None,
+           out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """act(x w^T + bias) + residual with gradients for all four, once (a second
+    derivative raises): x bf16 [M, K], w bf16 [N, K] (swiglu: [2N, K], the gate
+    half first), bias fp32, residual [M, N] of out_dtype, which is bf16 or, for a
+    router's logits, fp32. Keeps x w^T + bias in bf16 where an activation's
+    gradient wants it, and rounds what comes back through the activation to bf16
+    before the gradients' products."""
+    _check_shape(x, (x.shape[0], w.shape[-1]), "x")
+    return _Linear.apply(x.contiguous(), w.contiguous(), bias,
+                         None if residual is None else residual.contiguous(), activation, out_dtype)
 
 
 def _main() -> None:

@@ -28,7 +28,10 @@
  *
  * Beside the movement: its gradients (ep_combine_grad, ep_dispatch_grad), a
  * dispatch that quantises rows to 8 bits (ep_dispatch_fp8) and the experts'
- * products on such rows (ep_expert_gate_up_fp8, ep_expert_matmul_fp8).
+ * products on such rows (ep_expert_gate_up_fp8, ep_expert_matmul_fp8). Around
+ * them: the router that makes topk_idx and topk_w from logits (ep_route), dense
+ * products in bf16 for its logits and for experts that every token goes
+ * through (ep_linear), and their gradients.
  *
  * The pages describe neither the layout call nor combine; the stable order,
  * the masking rule and the combine arithmetic above are this library's
@@ -100,6 +103,9 @@ typedef enum {
     EP_ERR_BAD_SLOT = 6,     /* device: slot >= num_recv (receive buffer too small) */
     EP_ERR_WORKSPACE = 7     /* host: layout workspace smaller than required */
 } ep_status_t;
+
+/* Types of the tensors that may be one or the other. */
+typedef enum { EP_BF16 = 0, EP_F32 = 1 } ep_type_t;
 
 /* SM budget, after DeepEP's Buffer.set_num_sms ([DeepEP-TMA] "Minimal SM
  * Occupancy Configuration"): dispatch and combine launch one CTA per SM on at
@@ -393,6 +399,122 @@ EP_API ep_status_t ep_expert_gate_up_fp8(const uint8_t* a, const float* a_scale,
                                          const int32_t* offsets, int E, const uint8_t* w,
                                          const float* w_scale, int64_t I, int64_t K, uint8_t* out_q,
                                          float* out_scale, int32_t* status, void* stream);
+
+/* ---- the router --------------------------------------------------------------
+ * What makes the routing table and its weights from a router's logits (the
+ * pages start from the table). */
+
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t;
+typedef enum { EP_GROUP_MAX = 0, EP_GROUP_TOP2 = 1 } ep_group_score_t;
+
+#define EP_MAX_GROUPS 32
+
+/* The K experts of every token and their weights. With l the token's logits:
+ *   s[e]  = exp(l[e]) / sum over all experts of exp(l)    (EP_SCORE_SOFTMAX)
+ *           1 / (1 + exp(-l[e]))                          (EP_SCORE_SIGMOID)
+ *   c[e]  = l[e] without a bias, s[e] + bias[e] with one
+ *   group g: experts g * E/groups .. ; its worth is its largest c
+ *           (EP_GROUP_MAX) or the sum of its two largest c, without a bias of
+ *           its two largest s (EP_GROUP_TOP2); the topk_groups best stay
+ *   topk_idx[t, :] = the K experts of the groups that stay with the largest c,
+ *           descending
+ *   topk_w[t, k]   = scale * s[topk_idx[t,k]], with renormalize divided by the
+ *           sum of the K chosen scores
+ *   logits    fp32 or bf16 [T][E]      bias    fp32 [E], nullable
+ *   topk_idx  int64 [T][K]             topk_w  fp32 [T][K]
+ * The bias decides the choice alone and has no part in the weights. Equal
+ * values, of experts or of groups, go to the lower index; which of two is the
+ * larger is decided on values computed in 64 bits from the logits and the bias
+ * as they are. An expert whose logit or bias is -infinity is not chosen;
+ * entries that no expert is left for are -1 with weight 0, which every call of
+ * the movement skips. NaN counts as larger than every number, so that it is
+ * chosen and shows in the weights. Weights are off by at most 16 units of 2^-23
+ * of their value, softmax weights that are not renormalised by E / 32 more.
+ * 1 <= K <= min(32, E), groups divides E, groups <= EP_MAX_GROUPS, and the
+ * groups that stay hold at least K experts. (groups 1: no groups.) The
+ * SM budget does not apply, as for the layout. T == 0 is valid. */
+EP_API ep_status_t ep_route(const void* logits, int logits_type, int64_t T, int E, int K,
+                            const float* bias, int score, int groups, int topk_groups,
+                            int group_score, int renormalize, float scale, int64_t* topk_idx,
+                            float* topk_w, void* stream);
+
+/* The gradient of topk_w, for the logits (the choice itself and the bias have
+ * none). With g[k] = scale * d_topk_w[t,k] over the chosen entries and p[k] =
+ * topk_w[t,k] / scale:
+ *   softmax       d[e] = s[e] * (sum over k with idx[k] = e of g[k] - sum_j g[j] p[j])
+ *   softmax, renormalised   d[idx[k]] += p[k] * (g[k] - sum_j g[j] p[j])
+ *   sigmoid                 d[idx[k]] += g[k] * s * (1 - s)
+ *   sigmoid, renormalised   d[idx[k]] += p[k] * (1 - s) * (g[k] - sum_j g[j] p[j])
+ * and 0 for every other expert.
+ *   d_topk_w  fp32 [T][K]       topk_idx  int64 [T][K]
+ *   d_logits  [T][E] of the logits' type, every element written
+ * Entries of -1 and experts whose logit is -infinity have no part. An index
+ * outside [0, E) that is not -1 is skipped and reported as
+ * EP_ERR_BAD_EXPERT. */
+EP_API ep_status_t ep_route_grad(const float* d_topk_w, const void* logits, int logits_type,
+                                 const int64_t* topk_idx, int64_t T, int E, int K, int score,
+                                 int renormalize, float scale, void* d_logits, int32_t* status,
+                                 void* stream);
+
+/* ---- dense products ------------------------------------------------------------
+ * In bf16 with fp32 sums: the router's logits (fp32 out), and experts that every
+ * token goes through, whose last product adds to combine's result. As for the
+ * experts' products the SM budget does not apply, a call into an SM partition's
+ * stream uses the partition's SMs, and the order of the fp32 sums depends on
+ * the sizes, whether the stream is a partition's, and the device: equal calls on
+ * one device give equal bits. */
+
+typedef enum {
+    EP_ACT_NONE = 0,
+    EP_ACT_RELU = 1,
+    EP_ACT_GELU = 2,   /* z * P(z), P the normal distribution's cumulative function */
+    EP_ACT_SILU = 3,   /* z / (1 + exp(-z)) */
+    EP_ACT_SWIGLU = 4  /* silu(g) * u, z's columns a gate half g and an up half u */
+} ep_activation_t;
+
+/* y = act(z) + residual, z = x w^T + bias.
+ *   x  bf16 [M][K]   w  bf16 [N][K], for EP_ACT_SWIGLU [2N][K], the gate half first
+ *   bias      fp32, a value for each row of w, nullable
+ *   residual  [M][N] of y's type, nullable; may be y itself
+ *   y         bf16 or fp32 [M][N]
+ *   z         bf16 [M][rows of w], nullable: z as the activation's gradient
+ *             wants it (y is made from z before that rounding)
+ * K a multiple of 8, M and N any. x, w, residual, y and z 16-byte aligned; M, K
+ * and w's rows below 2^31 - 256, and ceil(M / 128) * ceil(N / 64) at most 2^30.
+ * silu's error is that of ep_expert_gate_up_fp8. */
+EP_API ep_status_t ep_linear(const uint16_t* x, int64_t M, int64_t K, const uint16_t* w, int64_t N,
+                             const float* bias, int activation, const void* residual, int y_type,
+                             void* y, uint16_t* z, int32_t* status, void* stream);
+
+/* Through the activation, given the gradient dy of y (which is residual's too):
+ *   dz     = bf16_rne( dy * act'(z) ), for EP_ACT_SWIGLU [dy * u * silu'(g),
+ *            dy * silu(g)]
+ *   d_bias = sum over rows of dz before its rounding (fp32)
+ *   dy      bf16 or fp32 [M][N]
+ *   z       bf16 [M][N] ([M][2N]) from ep_linear; not read for EP_ACT_NONE
+ *   dz      bf16 [M][pitch], nullable; pitch a multiple of 8 of at least w's
+ *           rows (values past those are left as they are)
+ *   d_bias  fp32 [N] ([2N]), nullable; M == 0 is valid and gives zeros
+ * Without an activation and a d_bias there is nothing to do for a bf16 dy
+ * whose rows start on 16 bytes: it is dz. */
+EP_API ep_status_t ep_linear_act_grad(const void* dy, int dy_type, const uint16_t* z, int64_t M,
+                                      int64_t N, int activation, uint16_t* dz, int64_t pitch,
+                                      float* d_bias, void* stream);
+
+/* dx = bf16_rne( dz w ):
+ *   dz  bf16 [M][pitch], N values of each row used; pitch a multiple of 8
+ *   w   bf16 [N][K] (for EP_ACT_SWIGLU N counts both halves)   dx  bf16 [M][K] */
+EP_API ep_status_t ep_linear_grad_input(const uint16_t* dz, int64_t pitch, int64_t M, int64_t N,
+                                        const uint16_t* w, int64_t K, uint16_t* dx, int32_t* status,
+                                        void* stream);
+
+/* d_w = dz^T x, or with accumulate d_w += dz^T x:
+ *   dz  bf16 [M][pitch], N values of each row used   x  bf16 [M][K]
+ *   d_w bf16 or fp32 [N][K]
+ * M == 0 is valid: zeros, with accumulate nothing changes. */
+EP_API ep_status_t ep_linear_grad_weight(const uint16_t* dz, int64_t pitch, int64_t M, int64_t N,
+                                         const uint16_t* x, int64_t K, int d_w_type, void* d_w,
+                                         int accumulate, int32_t* status, void* stream);
 
 /* Layout without a workspace argument, for callers that cannot allocate
  * device memory. The pages have no counterpart; this is a library addition.
