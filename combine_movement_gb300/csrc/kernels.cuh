@@ -334,8 +334,9 @@ struct LinearArgs {
 // `partition`: num_sms are those of an SM partition, not the device's.
 cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_t stream);
 
-// Tiles of an m x n output (gated: n columns of each half); up to kMaxTiles.
-int64_t linear_tiles(int64_t m, int64_t n, bool gated);
+// The same for at most kFewRows rows, both operands along k (linear_few.cu).
+constexpr int kFewRows = 4;
+cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t stream);
 
 // dz = dy act'(z) and its column sums (linear_grad.cu).
 struct ActGradArgs {

@@ -16,42 +16,53 @@
 // products run. They read 32 columns of 32 rows at a time and turn them around in
 // shared memory, so that eight lanes write 128 bytes of a row.
 #include <cuda.h>
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/ep.h"
-#include "combine_math.cuh"
 #include "kernels.cuh"
-#include "linear_math.cuh"
+#include "linear_out.cuh"
 #include "per_device.cuh"
 #include "product.cuh"
 
 namespace ep {
 namespace {
 
-constexpr int kTileRows = 128;
-constexpr int kBlock = 128;                  // columns of one of the tile's two blocks
-constexpr int kTileCols = 2 * kBlock;
+// Who works on a tile: a CTA alone or the CTAs of a cluster that share its blocks
+// along k, on 128 x 64 (gated: 32 columns of each half), or a pair of CTAs on
+// 256 x 256 (gated: 128 of each half), 128 rows and half of b each.
+enum Mode { kAlone, kShared, kPair };
+
+constexpr int kRows = 128;                   // of the output, in one CTA
 constexpr int kTileK = 64;                   // values of one stage along k
 constexpr uint32_t kRowBytes = kTileK * 2;
 constexpr uint32_t kGroupBytes = 64 * 128;   // 64 along k x 64 along m or n
-constexpr uint32_t kStageA = kTileRows * kRowBytes;
-constexpr uint32_t kStageB = kTileCols * kRowBytes;
-constexpr uint32_t kStageBytes = kStageA + kStageB;
-constexpr int kStages = 4;
+constexpr uint32_t kStageA = kRows * kRowBytes;
+constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr int kSlots = 2;
 constexpr int kOutWarps = 8;
 constexpr int kProductWarp = kOutWarps, kCopyWarp = kOutWarps + 1;
 constexpr int kThreads = (kOutWarps + 2) * 32;
-constexpr uint32_t kTmemCols = kSlots * kTileCols;
 constexpr int kChunk = 32;                   // columns turned around at a time
 constexpr uint32_t kTurnBytes = 32 * kChunk * 4;
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + kOutWarps * kTurnBytes;
-// A shared tile's sums, [row][column] in fp32, in the stages' place.
-constexpr uint32_t kSharedPitch = kTileCols * 4 + 16;
-static_assert(kTileRows * kSharedPitch <= kStages * kStageBytes, "shared sums");
+constexpr size_t kSmem = 1024 + kRingBytes + kOutWarps * kTurnBytes;
+constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;
 constexpr int kRowGroup = 8;                 // row tiles that share a column tile's turn
+// Blocks along k after which fp32 results take a tile's sums out of tensor memory.
+constexpr int kExactBlocks = 16;
+
+template <Mode kMode>
+struct Shape {
+    static constexpr int kCols = kMode == kPair ? 256 : 64;       // of the tile
+    static constexpr int kTileRows = kMode == kPair ? 2 * kRows : kRows;
+    static constexpr int kOwnB = kMode == kPair ? kCols / 2 : kCols;  // rows of b in one CTA
+    static constexpr uint32_t kStageBytes = kStageA + kOwnB * kRowBytes;
+    static constexpr int kStages = kRingBytes / kStageBytes;
+    static constexpr int kMine = kCols / 2;  // columns of sums that a warp takes
+    // a shared tile's sums, [row][column] in fp32, in the stages' place
+    static constexpr uint32_t kPitch = kCols * 4 + 16;
+    static_assert(kStages <= kMaxStages && kRows * kPitch <= kRingBytes, "shared memory");
+};
 
 struct Maps {
     CUtensorMap a, b;
@@ -59,107 +70,28 @@ struct Maps {
 };
 
 struct Control {
-    uint64_t full[kStages];       // the copies have landed
-    uint64_t done[kStages];       // the stage's product is done
+    uint64_t full[kMaxStages];    // the copies have landed (a pair's: rank 0's)
+    uint64_t done[kMaxStages];    // the stage's product is done
     uint64_t sums[kSlots];        // a tile's sums are complete
-    uint64_t sums_read[kSlots];   // and have been read: the writing warps
+    uint64_t sums_read[kSlots];   // and have been read: the writing warps (rank 0's)
     uint64_t drained;             // after an abort: products still in flight
     uint32_t tmem;
     int32_t abort;
 };
 
 struct Tile {
-    int64_t row0, col0;
+    int64_t row0;
+    int64_t col_tile;
 };
 // Groups of kRowGroup row tiles, column tiles outside of row tiles in each: the
 // tiles that run at a time share their rows of both operands.
+template <Mode kMode>
 __device__ __forceinline__ Tile tile_at(int64_t t, const LinearArgs& a) {
     const int64_t per = kRowGroup * a.col_tiles;
     const int64_t group = t / per, r0 = group * kRowGroup;
     const int64_t rows = min(static_cast<int64_t>(kRowGroup), a.row_tiles - r0);
     const int64_t i = t - group * per;
-    return {(r0 + i % rows) * kTileRows, i / rows};
-}
-
-__device__ __forceinline__ float bf16_low(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_high(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-
-// N (4 or 1) neighbouring values of a row.
-template <int N>
-struct Values {
-    float v[N];
-};
-template <int N>
-__device__ __forceinline__ Values<N> load_f32(const float* p) {
-    Values<N> r;
-    if constexpr (N == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(p);
-        r.v[0] = f.x, r.v[1] = f.y, r.v[2] = f.z, r.v[3] = f.w;
-    } else {
-        r.v[0] = *p;
-    }
-    return r;
-}
-template <int N>
-__device__ __forceinline__ Values<N> load_bf16(const uint16_t* p) {
-    Values<N> r;
-    if constexpr (N == 4) {
-        const uint2 f = *reinterpret_cast<const uint2*>(p);
-        r.v[0] = bf16_low(f.x), r.v[1] = bf16_high(f.x), r.v[2] = bf16_low(f.y), r.v[3] = bf16_high(f.y);
-    } else {
-        r.v[0] = bf16_low(*p);
-    }
-    return r;
-}
-template <int N>
-__device__ __forceinline__ void store_bf16(uint16_t* p, const Values<N>& r) {
-    if constexpr (N == 4)
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(r.v[0], r.v[1]), pack_bf16x2(r.v[2], r.v[3]));
-    else
-        *p = __bfloat16_as_ushort(__float2bfloat16_rn(r.v[0]));
-}
-template <int N>
-__device__ __forceinline__ void store_f32(float* p, const Values<N>& r) {
-    if constexpr (N == 4)
-        *reinterpret_cast<float4*>(p) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-    else
-        *p = r.v[0];
-}
-
-template <int N>
-__device__ __forceinline__ Values<N> load_residual(const LinearArgs& a, int64_t at) {
-    return a.out_f32 ? load_f32<N>(static_cast<const float*>(a.residual) + at)
-                     : load_bf16<N>(static_cast<const uint16_t*>(a.residual) + at);
-}
-
-// The end of N values of out's row `row` from column `col` on: sums in `v`
-// (gated: the up half's in `up`), `res` what is added.
-template <int N, bool kGated>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int64_t col, Values<N> v,
-                                       Values<N> up, const Values<N>& res) {
-    if (a.bias != nullptr) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v.v[i] += __ldg(a.bias + col + i);
-        if (kGated) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) up.v[i] += __ldg(a.bias + a.n + col + i);
-        }
-    }
-    if (a.z != nullptr) {
-        uint16_t* z = a.z + row * (kGated ? 2 * a.n : a.n) + col;
-        store_bf16<N>(z, v);
-        if (kGated) store_bf16<N>(z + a.n, up);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v.v[i] = kGated ? silu(v.v[i]) * up.v[i] : activate(v.v[i], a.act);
-        v.v[i] += res.v[i];
-    }
-    const int64_t at = row * a.n + col;
-    if (a.out_f32)
-        store_f32<N>(static_cast<float*>(a.out) + at, v);
-    else
-        store_bf16<N>(static_cast<uint16_t*>(a.out) + at, v);
+    return {(r0 + i % rows) * Shape<kMode>::kTileRows, i / rows};
 }
 
 // 16-byte piece p of row r of a warp's turning place.
@@ -167,89 +99,167 @@ __device__ __forceinline__ uint32_t turn_at(uint32_t turn, int r, int p) {
     return turn + r * (kChunk * 4) + ((p ^ (r & 7)) << 4);
 }
 
-// 32 x 32 sums from the turning place: `col` the column of the first (gated:
-// of 16 of each half), `rows` how many rows are the tile's.
-template <bool kGated>
-__device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, int64_t row0,
-                                            int rows, int64_t col) {
+// A warp's part of out: 32 rows from row0 on, of which `rows` are there.
+struct Part {
+    int64_t row0;
+    int rows;
+};
+
+// What a lane adds to its values of a chunk, or of a quarter of one, read ahead
+// of them.
+template <int kQuarters>
+struct Ahead {
+    uint32_t bits[8 * kQuarters];
+};
+template <bool kGated, int kQuarters>
+__device__ __forceinline__ void read_ahead(const LinearArgs& a, const Part& part, int64_t col,
+                                           int quarter, Ahead<kQuarters>& ahead) {
+    constexpr int kCols = kGated ? kChunk / 2 : kChunk;
+    const int lane = threadIdx.x & 31;
+    if (a.residual == nullptr) return;
+    if (a.n % 4 == 0) {
+        constexpr int kPieces = kCols / 4, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
+        const int64_t c = col + lane % kPieces * 4;
+#pragma unroll
+        for (int i = 0; i < kRounds * kQuarters / 4; ++i) {
+            const int r = lane / kPieces + (quarter * (kRounds / 4) + i) * kAtOnce;
+            if (r >= part.rows || c >= a.n) continue;
+            const Residual<4> v = load_residual<4>(a, (part.row0 + r) * a.n + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ahead.bits[4 * i + j] = v.bits[j];
+        }
+    } else {
+        constexpr int kAtOnce = 32 / kCols, kRounds = 32 / kAtOnce;
+        const int64_t c = col + lane % kCols;
+#pragma unroll
+        for (int i = 0; i < kRounds * kQuarters / 4; ++i) {
+            const int r = lane / kCols + (quarter * (kRounds / 4) + i) * kAtOnce;
+            if (r < part.rows && c < a.n)
+                ahead.bits[i] = load_residual<1>(a, (part.row0 + r) * a.n + c).bits[0];
+        }
+    }
+}
+
+// 32 x 32 sums from the turning place, or with a quarter's Ahead 8 rows of them:
+// `col` the column of the first (gated: of 16 of each half).
+template <bool kGated, int kQuarters>
+__device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
+                                            int64_t col, int quarter, const Ahead<kQuarters>& ahead) {
     constexpr int kCols = kGated ? kChunk / 2 : kChunk;  // of out
     const int lane = threadIdx.x & 31;
     if (a.n % 4 == 0) {
         constexpr int kPieces = kCols / 4, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
-        const int p = lane % kPieces, r0 = lane / kPieces;
+        const int p = lane % kPieces;
         const int64_t c = col + 4 * p;
-        Values<4> res[kRounds] = {};
-        if (a.residual != nullptr) {
+        if (c >= a.n) return;
+        const Values<4> b0 = load_bias<4>(a, c), b1 = load_bias<4>(a, kGated ? a.n + c : c);
 #pragma unroll
-            for (int i = 0; i < kRounds; ++i)
-                if (r0 + i * kAtOnce < rows && c < a.n)
-                    res[i] = load_residual<4>(a, (row0 + r0 + i * kAtOnce) * a.n + c);
-        }
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-            const int r = r0 + i * kAtOnce;
-            if (r >= rows || c >= a.n) continue;
+        for (int i = 0; i < kRounds * kQuarters / 4; ++i) {
+            const int r = lane / kPieces + (quarter * (kRounds / 4) + i) * kAtOnce;
+            if (r >= part.rows) break;
             const float4 f = load_shared_v4(turn_at(turn, r, p));
             const float4 u = kGated ? load_shared_v4(turn_at(turn, r, p + kPieces)) : f;
-            finish<4, kGated>(a, row0 + r, c, {{f.x, f.y, f.z, f.w}}, {{u.x, u.y, u.z, u.w}}, res[i]);
+            const Residual<4> res = {{ahead.bits[4 * i], ahead.bits[4 * i + 1], ahead.bits[4 * i + 2],
+                                      ahead.bits[4 * i + 3]}};
+            finish<4, kGated>(a, part.row0 + r, c, sum<4>({{f.x, f.y, f.z, f.w}}, b0),
+                              sum<4>({{u.x, u.y, u.z, u.w}}, b1), res);
         }
     } else {  // rows that do not start on 16 bytes: value by value
-        constexpr int kAtOnce = 32 / kCols;
+        constexpr int kAtOnce = 32 / kCols, kRounds = 32 / kAtOnce;
         const int cl = lane % kCols;
         const int64_t c = col + cl;
-        for (int r = lane / kCols; r < rows; r += kAtOnce) {
-            if (c >= a.n) break;
-            Values<1> res = {};
-            if (a.residual != nullptr) res = load_residual<1>(a, (row0 + r) * a.n + c);
+        if (c >= a.n) return;
+        const Values<1> b0 = load_bias<1>(a, c), b1 = load_bias<1>(a, kGated ? a.n + c : c);
+#pragma unroll
+        for (int i = 0; i < kRounds * kQuarters / 4; ++i) {
+            const int r = lane / kCols + (quarter * (kRounds / 4) + i) * kAtOnce;
+            if (r >= part.rows) break;
             const float f = load_shared_f32(turn_at(turn, r, cl / 4) + cl % 4 * 4);
             const float u =
                 kGated ? load_shared_f32(turn_at(turn, r, (cl + kCols) / 4) + cl % 4 * 4) : f;
-            finish<1, kGated>(a, row0 + r, c, {{f}}, {{u}}, res);
+            finish<1, kGated>(a, part.row0 + r, c, {{f + b0.v[0]}}, {{u + b1.v[0]}}, {{ahead.bits[i]}});
         }
     }
 }
 
 // The sums of a tile that the cluster's CTAs took parts of k of: each has laid
 // its own out in shared memory; CTA `rank` adds, in the parts' order, and writes
-// those of the rows r = rank mod split.
-template <int N, bool kGated>
+// those of the rows r = rank mod kParts.
+template <int N, bool kGated, int kParts>
 __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
                                                   int rank) {
-    constexpr int kCols = kGated ? kBlock : kTileCols, kPieces = kCols / N;
+    using S = Shape<kShared>;
+    constexpr int kCols = kGated ? S::kCols / 2 : S::kCols, kPieces = kCols / N;
     const int64_t left = a.m - tile.row0;
-    const int rows = static_cast<int>(left < kTileRows ? left : kTileRows);
-    const int pieces = (rows + a.split - 1 - rank) / a.split * kPieces;
-    const int64_t col0 = tile.col0 * kCols;
+    const int rows = static_cast<int>(left < kRows ? left : kRows);
+    const int pieces = (rows + kParts - 1 - rank) / kParts * kPieces;
+    const int64_t col0 = tile.col_tile * kCols;
     for (int i = threadIdx.x; i < pieces; i += kOutWarps * 32) {
-        const int r = i / kPieces * a.split + rank, c = i % kPieces * N;
+        const int r = i / kPieces * kParts + rank, c = i % kPieces * N;
         if (col0 + c >= a.n) continue;
         const int64_t row = tile.row0 + r, col = col0 + c;
-        Values<N> res = {}, v = {}, up = {};
+        Residual<N> res = {};
         if (a.residual != nullptr) res = load_residual<N>(a, row * a.n + col);
-        const uint32_t at = sums + r * kSharedPitch + c * 4;
-        for (int p = 0; p < a.split; ++p) {
+        const uint32_t at = sums + r * S::kPitch + c * 4;
+        Values<N> v[kParts], up[kParts];
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
             const uint32_t from = cluster_map(at, p);
             if constexpr (N == 4) {
                 const float4 f = load_cluster_v4(from);
-                v.v[0] += f.x, v.v[1] += f.y, v.v[2] += f.z, v.v[3] += f.w;
+                v[p] = {{f.x, f.y, f.z, f.w}};
                 if (kGated) {
-                    const float4 u = load_cluster_v4(from + kBlock * 4);
-                    up.v[0] += u.x, up.v[1] += u.y, up.v[2] += u.z, up.v[3] += u.w;
+                    const float4 u = load_cluster_v4(from + kCols * 4);
+                    up[p] = {{u.x, u.y, u.z, u.w}};
                 }
             } else {
-                v.v[0] += load_cluster_f32(from);
-                if (kGated) up.v[0] += load_cluster_f32(from + kBlock * 4);
+                v[p] = {{load_cluster_f32(from)}};
+                if (kGated) up[p] = {{load_cluster_f32(from + kCols * 4)}};
             }
         }
-        finish<N, kGated>(a, row, col, v, up, res);
+#pragma unroll
+        for (int p = 1; p < kParts; ++p) {
+            v[0] = sum<N>(v[0], v[p]);
+            if (kGated) up[0] = sum<N>(up[0], up[p]);
+        }
+        v[0] = sum<N>(v[0], load_bias<N>(a, col));
+        if (kGated) up[0] = sum<N>(up[0], load_bias<N>(a, a.n + col));
+        finish<N, kGated>(a, row, col, v[0], kGated ? up[0] : v[0], res);
     }
 }
+template <int N, bool kGated>
+__device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
+                                                  int rank) {
+    if (a.split == 2)
+        write_shared_tile<N, kGated, 2>(a, sums, tile, rank);
+    else if (a.split == 4)
+        write_shared_tile<N, kGated, 4>(a, sums, tile, rank);
+    else
+        write_shared_tile<N, kGated, 8>(a, sums, tile, rank);
+}
 
-// kSplit: a tile's blocks along k go to the CTAs of a cluster, a tile to a
-// cluster; else a CTA takes whole tiles, one after the other.
-template <bool kGated, bool kSplit>
+// 32 x 32 sums of a warp into its turning place.
+__device__ __forceinline__ void turn_chunk(uint32_t turn, const float* v0, const float* v1) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();  // the chunk before has been read
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        store_shared_v4(turn_at(turn, lane, i),
+                        make_float4(v0[4 * i], v0[4 * i + 1], v0[4 * i + 2], v0[4 * i + 3]));
+        store_shared_v4(turn_at(turn, lane, 4 + i),
+                        make_float4(v1[4 * i], v1[4 * i + 1], v1[4 * i + 2], v1[4 * i + 3]));
+    }
+    __syncwarp();
+}
+
+// kExact: sums leave tensor memory every kExactBlocks blocks along k and are added
+// in registers (not kShared, whose parts are added as they are joined).
+template <Mode kMode, bool kGated, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const LinearArgs a, const __grid_constant__ Maps maps) {
+    using S = Shape<kMode>;
+    constexpr bool kClusters = kMode != kAlone;
+    constexpr uint32_t kTmemCols = kSlots * S::kCols;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Control ctl;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // the swizzle's period
@@ -257,128 +267,235 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t full = smem_u32(ctl.full), done = smem_u32(ctl.done);
     const uint32_t sums = smem_u32(ctl.sums), sums_read = smem_u32(ctl.sums_read);
     const uint32_t abort = smem_u32(&ctl.abort);
+    const int rank = kClusters ? static_cast<int>(cluster_rank()) : 0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < S::kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(done + 8 * i, 1);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(sums + 8 * i, 1);
-            mbar_init(sums_read + 8 * i, kOutWarps);
+            mbar_init(sums_read + 8 * i, kMode == kPair ? 2 * kOutWarps : kOutWarps);
         }
         mbar_init(smem_u32(&ctl.drained), 1);
         ctl.abort = 0;
         fence_mbar_init();
     }
-    if (warp == kProductWarp) tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
+    if (warp == kProductWarp) {
+        if constexpr (kMode == kPair)
+            tmem_alloc_pair(smem_u32(&ctl.tmem), kTmemCols);
+        else
+            tmem_alloc(smem_u32(&ctl.tmem), kTmemCols);
+    }
     if (warp == kCopyWarp && lane == 0) {
         prefetch_tensor_map(&maps.a);
         prefetch_tensor_map(&maps.b);
     }
     tcgen05_fence_before();
     __syncthreads();
+    if (kMode == kPair) {  // both CTAs' barriers and tensor memory are there
+        cluster_arrive();
+        cluster_wait();
+    }
     tcgen05_fence_after();
     griddep_wait();
     griddep_launch_dependents();
     const uint32_t tmem = ctl.tmem;
     const int64_t tiles = a.row_tiles * a.col_tiles;
-    const int split = kSplit ? a.split : 1;
-    const int rank = kSplit ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t t0 = kSplit ? blockIdx.x / split : blockIdx.x;
-    const int64_t step = kSplit ? tiles : gridDim.x;
-    const int kb_first = static_cast<int>(static_cast<int64_t>(a.k_blocks) * rank / split);
-    const int kb_end = static_cast<int>(static_cast<int64_t>(a.k_blocks) * (rank + 1) / split);
+    const int size = kMode == kPair ? 2 : kMode == kShared ? a.split : 1;
+    const int64_t t0 = blockIdx.x / size;
+    const int64_t step = kMode == kShared ? tiles : gridDim.x / size;
+    const int kb_first =
+        kMode == kShared ? static_cast<int>(static_cast<int64_t>(a.k_blocks) * rank / size) : 0;
+    const int kb_end = kMode == kShared
+                           ? static_cast<int>(static_cast<int64_t>(a.k_blocks) * (rank + 1) / size)
+                           : a.k_blocks;
+    const int per_sum = kExact ? kExactBlocks : kb_end - kb_first;  // blocks
     int64_t fills = 0;  // stages filled so far (the copying warp's)
 
     if (warp == kCopyWarp) {
         // ---- copies: one lane fills the stages in order ----
-        const int a_groups = a.m > 64 ? 2 : 1;
+        const int a_groups = kMode == kPair || a.m > 64 ? 2 : 1;
         const uint32_t bytes =
-            kStageB + (a.a_by_k ? a_groups * kGroupBytes : static_cast<uint32_t>(maps.a_rows) * kRowBytes);
-        Ring<kStages> st;
+            S::kOwnB * kRowBytes +
+            (a.a_by_k ? a_groups * kGroupBytes : static_cast<uint32_t>(maps.a_rows) * kRowBytes);
+        auto load = [](uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+            if constexpr (kMode == kPair)
+                tensor_load_2d_pair(dst, map, x, y, bar);
+            else
+                tensor_load_2d(dst, map, x, y, bar);
+        };
+        Ring<S::kStages> st;
         bool ok = true;
         for (int64_t t = t0; ok && t < tiles; t += step) {
-            const Tile tile = tile_at(t, a);
-            const int row0 = static_cast<int>(tile.row0);
-            const int col0 = static_cast<int>(tile.col0) * (kGated ? kBlock : kTileCols);
-            const int col1 = kGated ? static_cast<int>(a.n) + col0 : col0 + kBlock;
+            const Tile tile = tile_at<kMode>(t, a);
+            const int row0 = static_cast<int>(tile.row0) + (kMode == kPair ? rank * kRows : 0);
+            const int col0 = static_cast<int>(tile.col_tile) * (kGated ? S::kCols / 2 : S::kCols);
+            const int col1 = kGated ? static_cast<int>(a.n) + col0 : col0 + S::kCols / 2;
             for (int kb = kb_first; kb < kb_end; ++kb, st.next(), ++fills) {
-                ok = warp_wait(done + 8 * st.i, st.round ^ 1u, abort, a.status);
+                ok = warp_wait<kMode == kPair>(done + 8 * st.i, st.round ^ 1u, abort, a.status);
                 if (!ok) break;
                 if (elect_one()) {
-                    const uint32_t dst_a = base + st.i * kStageBytes, dst_b = dst_a + kStageA;
-                    const uint32_t bar = full + 8 * st.i;
+                    const uint32_t dst_a = base + st.i * S::kStageBytes, dst_b = dst_a + kStageA;
                     const int k = kb * kTileK;
-                    mbar_arrive_expect_tx(bar, bytes);
+                    uint32_t bar = full + 8 * st.i;
+                    if (kMode == kPair) {
+                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
+                        bar = cluster_map(bar, 0);
+                    } else {
+                        mbar_arrive_expect_tx(bar, bytes);
+                    }
                     if (a.a_by_k) {
                         for (int g = 0; g < a_groups; ++g)
-                            tensor_load_2d(dst_a + g * kGroupBytes, &maps.a, row0 + 64 * g, k, bar);
+                            load(dst_a + g * kGroupBytes, &maps.a, row0 + 64 * g, k, bar);
                     } else {
-                        tensor_load_2d(dst_a, &maps.a, k, row0, bar);
+                        load(dst_a, &maps.a, k, row0, bar);
                     }
                     if (a.b_by_k) {
-                        for (int g = 0; g < kTileCols / 64; ++g)
-                            tensor_load_2d(dst_b + g * kGroupBytes, &maps.b, col0 + 64 * g, k, bar);
+                        const int c = kMode == kPair && rank == 1 ? col1 : col0;
+#pragma unroll
+                        for (int g = 0; g < S::kOwnB / 64; ++g)
+                            load(dst_b + g * kGroupBytes, &maps.b, c + 64 * g, k, bar);
+                    } else if (kMode == kPair) {
+                        load(dst_b, &maps.b, k, rank == 1 ? col1 : col0, bar);
                     } else {
-                        tensor_load_2d(dst_b, &maps.b, k, col0, bar);
-                        tensor_load_2d(dst_b + kBlock * kRowBytes, &maps.b, k, col1, bar);
+                        load(dst_b, &maps.b, k, col0, bar);
+                        load(dst_b + S::kCols / 2 * kRowBytes, &maps.b, k, col1, bar);
                     }
                 }
                 __syncwarp();
             }
         }
+        // the last products' arrivals, too, come before the CTA's end
+        for (int i = 0; ok && i < S::kStages; ++i, st.next())
+            ok = warp_wait<kMode == kPair>(done + 8 * st.i, st.round ^ 1u, abort, a.status);
     } else if (warp == kProductWarp) {
-        // ---- products: one lane ----
-        const uint32_t desc = mma_desc_bf16(kTileRows, kTileCols, a.a_by_k, a.b_by_k);
+        // ---- products: one lane (of a pair, rank 0's) ----
+        const uint32_t desc = mma_desc_bf16(S::kTileRows, S::kCols, a.a_by_k, a.b_by_k);
         const uint64_t desc_a = a.a_by_k ? operand_desc_by_k(base) : operand_desc(base);
         const uint64_t desc_b =
             a.b_by_k ? operand_desc_by_k(base + kStageA) : operand_desc(base + kStageA);
         const uint32_t step_a = (a.a_by_k ? 2048 : 32) >> 4, step_b = (a.b_by_k ? 2048 : 32) >> 4;
-        Ring<kStages> st;
+        Ring<S::kStages> st;
         Ring<kSlots> slot;
-        bool ok = true;
-        for (int64_t t = t0; ok && t < tiles; t += step, slot.next()) {
-            ok = warp_wait(sums_read + 8 * slot.i, slot.round ^ 1u, abort, a.status);
-            if (!ok) break;
-            tcgen05_fence_after();
-            for (int kb = kb_first; kb < kb_end; ++kb, st.next()) {
-                ok = warp_wait(full + 8 * st.i, st.round, abort, a.status);
+        bool ok = kMode != kPair || rank == 0;
+        for (int64_t t = t0; ok && t < tiles; t += step) {
+            for (int kb0 = kb_first; ok && kb0 < kb_end; kb0 += per_sum, slot.next()) {
+                ok = warp_wait<kMode == kPair>(sums_read + 8 * slot.i, slot.round ^ 1u, abort, a.status);
                 if (!ok) break;
                 tcgen05_fence_after();
-                if (elect_one()) {
-                    const uint32_t at = st.i * (kStageBytes >> 4);
+                const int kb1 = min(kb0 + per_sum, kb_end);
+                for (int kb = kb0; kb < kb1; ++kb, st.next()) {
+                    ok = warp_wait<kMode == kPair>(full + 8 * st.i, st.round, abort, a.status);
+                    if (!ok) break;
+                    tcgen05_fence_after();
+                    if (elect_one()) {
+                        const uint32_t at = st.i * (S::kStageBytes >> 4);
+                        const uint32_t d = tmem + slot.i * S::kCols;
 #pragma unroll
-                    for (int k = 0; k < kTileK / 16; ++k)
-                        mma_bf16(tmem + slot.i * kTileCols, desc_a + at + k * step_a,
-                                 desc_b + at + k * step_b, desc, kb > kb_first || k > 0);
-                    mma_commit(done + 8 * st.i);
+                        for (int k = 0; k < kTileK / 16; ++k) {
+                            const uint64_t da = desc_a + at + k * step_a, db = desc_b + at + k * step_b;
+                            const bool add = kb > kb0 || k > 0;
+                            if constexpr (kMode == kPair)
+                                mma_bf16_pair(d, da, db, desc, add);
+                            else
+                                mma_bf16(d, da, db, desc, add);
+                        }
+                        if constexpr (kMode == kPair)
+                            mma_commit_pair(done + 8 * st.i);
+                        else
+                            mma_commit(done + 8 * st.i);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    if constexpr (kMode == kPair)
+                        mma_commit_pair(sums + 8 * slot.i);
+                    else
+                        mma_commit(sums + 8 * slot.i);
                 }
                 __syncwarp();
             }
-            if (!ok) break;
-            if (elect_one()) mma_commit(sums + 8 * slot.i);
-            __syncwarp();
         }
     } else {
         // ---- results: warp = 32 rows (its quarter) and half of the columns ----
         const int quarter = warp & 3, half = warp >> 2;
-        const uint32_t turn = base + kStages * kStageBytes + warp * kTurnBytes;
+        const uint32_t turn = base + kRingBytes + warp * kTurnBytes;
         const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t read = kMode == kPair ? cluster_map(sums_read, 0) : sums_read;
+        // of out, in a chunk, and the warp's
+        constexpr int kCols = kGated ? kChunk / 2 : kChunk, kMine = kGated ? S::kMine / 2 : S::kMine;
+        // the second half of a chunk's sums: gated, the up half's
+        constexpr int kSecond = kGated ? S::kCols / 2 : 16;
+        auto release = [&](int i) {
+            __syncwarp();
+            tcgen05_fence_before();
+            if (kMode == kPair) {
+                if (lane == 0) mbar_arrive_cluster(read + 8 * i);
+            } else {
+                mbar_arrive_if(read + 8 * i, lane == 0);
+            }
+        };
         Ring<kSlots> slot;
         bool ok = true;
-        for (int64_t t = t0; ok && t < tiles; t += step, slot.next()) {
-            const Tile tile = tile_at(t, a);
-            ok = warp_wait(sums + 8 * slot.i, slot.round, abort, a.status);
+        for (int64_t t = t0; ok && t < tiles; t += step) {
+            const Tile tile = tile_at<kMode>(t, a);
+            Part part;
+            part.row0 = tile.row0 + (kMode == kPair ? rank * kRows : 0) + quarter * 32;
+            part.rows = static_cast<int>(min(static_cast<int64_t>(32), a.m - part.row0));
+            const int64_t col0 = tile.col_tile * (2 * kMine) + half * kMine;
+            if constexpr (kExact) {
+                float acc[S::kMine / kChunk][2][16] = {};
+                for (int kb = kb_first; kb < kb_end; kb += per_sum, slot.next()) {
+                    ok = warp_wait<kMode == kPair>(sums + 8 * slot.i, slot.round, abort, a.status);
+                    if (!ok) break;
+                    tcgen05_fence_after();
+                    const uint32_t at = from + slot.i * S::kCols + half * kMine;
+#pragma unroll
+                    for (int c = 0; c < S::kMine / kChunk; ++c) {
+                        uint32_t v[2][16];
+                        tmem_load16(at + c * kCols, v[0]);
+                        tmem_load16(at + c * kCols + kSecond, v[1]);
+                        tmem_load_wait16(v[0]);
+                        tmem_load_wait16(v[1]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            acc[c][0][i] += __uint_as_float(v[0][i]);
+                            acc[c][1][i] += __uint_as_float(v[1][i]);
+                        }
+                    }
+                    release(slot.i);
+                }
+                if (!ok) break;
+                if (part.rows <= 0) continue;
+#pragma unroll
+                for (int c = 0; c < S::kMine / kChunk; ++c) {
+                    if (col0 + c * kCols >= a.n) break;
+                    turn_chunk(turn, acc[c][0], acc[c][1]);
+                    // (registers for no more than a quarter's)
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        Ahead<1> ahead = {};
+                        read_ahead<kGated>(a, part, col0 + c * kCols, q, ahead);
+                        write_chunk<kGated>(a, turn, part, col0 + c * kCols, q, ahead);
+                    }
+                }
+                continue;
+            }
+            Ahead<4> ahead = {};
+            if (kMode != kShared) read_ahead<kGated>(a, part, col0, 0, ahead);
+            ok = warp_wait<kMode == kPair>(sums + 8 * slot.i, slot.round, abort, a.status);
             if (!ok) break;
             tcgen05_fence_after();
-            const uint32_t slot_at = from + slot.i * kTileCols;
-            if (kSplit) {
-                const uint32_t own = base + (quarter * 32 + lane) * kSharedPitch + half * kBlock * 4;
-#pragma unroll 1
-                for (int c = 0; c < kBlock; c += 16) {
+            const uint32_t slot_at = from + slot.i * S::kCols;
+            if constexpr (kMode == kShared) {
+                const uint32_t own = base + (quarter * 32 + lane) * S::kPitch + half * S::kMine * 4;
+#pragma unroll
+                for (int c = 0; c < S::kMine; c += 16) {
                     uint32_t v[16];
-                    tmem_load16(slot_at + half * kBlock + c, v);
+                    tmem_load16(slot_at + half * S::kMine + c, v);
                     tmem_load_wait16(v);
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
@@ -387,52 +504,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])));
                 }
                 break;
-            }
-            const int64_t row0 = tile.row0 + quarter * 32;
-            const int rows = static_cast<int>(min(static_cast<int64_t>(32), a.m - row0));
-            constexpr int kCols = kGated ? kChunk / 2 : kChunk;     // of out, in a chunk
-            constexpr int kMine = kGated ? kBlock / 2 : kBlock;     // of out, the warp's
-            const int64_t col0 = tile.col0 * (2 * kMine) + half * kMine;
-            if (rows > 0) {
+            } else {
+                if (part.rows > 0) {
 #pragma unroll 1
-                for (int c = 0; c < kMine && col0 + c < a.n; c += kCols) {
-                    const uint32_t at = slot_at + half * kMine + c;
-                    uint32_t v[2][16];
-                    tmem_load16(at, v[0]);
-                    tmem_load16(at + (kGated ? kBlock : 16), v[1]);
-                    tmem_load_wait16(v[0]);
-                    tmem_load_wait16(v[1]);
-                    __syncwarp();  // the chunk before has been read
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            store_shared_v4(turn_at(turn, lane, h * 4 + i / 4),
-                                            make_float4(__uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1]),
-                                                        __uint_as_float(v[h][i + 2]),
-                                                        __uint_as_float(v[h][i + 3])));
-                    __syncwarp();
-                    write_chunk<kGated>(a, turn, row0, rows, col0 + c);
+                    for (int c = 0; c < kMine && col0 + c < a.n; c += kCols) {
+                        const uint32_t at = slot_at + half * kMine + c;
+                        uint32_t v[2][16];
+                        tmem_load16(at, v[0]);
+                        tmem_load16(at + kSecond, v[1]);
+                        tmem_load_wait16(v[0]);
+                        tmem_load_wait16(v[1]);
+                        turn_chunk(turn, reinterpret_cast<const float*>(v[0]),
+                                   reinterpret_cast<const float*>(v[1]));
+                        const Ahead<4> now = ahead;
+                        if (c + kCols < kMine) read_ahead<kGated>(a, part, col0 + c + kCols, 0, ahead);
+                        write_chunk<kGated>(a, turn, part, col0 + c, 0, now);
+                    }
                 }
+                release(slot.i);
+                slot.next();
             }
-            __syncwarp();
-            tcgen05_fence_before();
-            mbar_arrive_if(sums_read + 8 * slot.i, lane == 0);
         }
     }
-    if (kSplit) {
+    if (kMode == kShared) {
         // Every thread passes both barriers, whatever its CTA found to do.
         cluster_arrive();
         cluster_wait();
         if (warp < kOutWarps && t0 < tiles && load_shared(abort) == 0) {
-            const Tile tile = tile_at(t0, a);
+            const Tile tile = tile_at<kMode>(t0, a);
             if (a.n % 4 == 0)
                 write_shared_tile<4, kGated>(a, base, tile, rank);
             else
                 write_shared_tile<1, kGated>(a, base, tile, rank);
         }
-        cluster_arrive();
-        cluster_wait();  // no CTA reads this one's sums any more
     }
     __syncwarp();
     tcgen05_fence_before();
@@ -442,18 +546,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // copy and product has been waited for.)
     if (load_shared(abort) != 0) {
         if (warp == kCopyWarp && lane == 0)
-            mbar_drain_bounded<kStages>(full, fills > kStages ? fills - kStages : 0, fills - 1);
+            mbar_drain_bounded<S::kStages>(full, fills > S::kStages ? fills - S::kStages : 0, fills - 1);
         if (warp == kProductWarp) {
             const uint32_t bar = smem_u32(&ctl.drained);
-            if (elect_one()) mma_commit(bar);
+            if (elect_one()) {
+                if constexpr (kMode != kPair)
+                    mma_commit(bar);
+                else if (rank == 0)
+                    mma_commit_pair(bar);
+            }
             __syncwarp();
             mbar_wait_bounded(bar, 0);
         }
     }
+    if (kClusters) {  // no CTA reads this one's sums, or arrives at its barriers, any more
+        cluster_arrive();
+        cluster_wait();
+    }
     __syncwarp();
     if (warp == kProductWarp) {
         tcgen05_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        if constexpr (kMode == kPair)
+            tmem_dealloc_pair(tmem, kTmemCols);
+        else
+            tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -473,13 +589,13 @@ bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t width
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kGated, bool kSplit>
-cudaError_t launch(const LinearArgs& a, const Maps& maps, int grid, cudaStream_t stream) {
-    auto kern = linear_kernel<kGated, kSplit>;
+template <Mode kMode, bool kGated, bool kExact>
+cudaError_t launch(const LinearArgs& a, const Maps& maps, int grid, int cluster, cudaStream_t stream) {
+    auto kern = linear_kernel<kMode, kGated, kExact>;
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(kSmem));
     if (err != cudaSuccess) return err;
-    return launch_dependent_clusters(kern, grid, a.split, kThreads, kSmem, stream, a, maps);
+    return launch_dependent_clusters(kern, grid, cluster, kThreads, kSmem, stream, a, maps);
 }
 
 // Clusters of 2, 4, 8 CTAs that a device holds at a time: fewer than SMs / size,
@@ -491,7 +607,7 @@ struct ResidentClusters {
 cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
     static PerDevice<ResidentClusters> table;
     return table.get(device, clusters, [](ResidentClusters* found) {
-        auto kern = linear_kernel<false, true>;
+        auto kern = linear_kernel<kShared, false, false>;
         cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSmem));
         for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2) {
@@ -512,53 +628,85 @@ cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
     });
 }
 
-// CTAs to share a tile's blocks along k, where the tiles leave SMs idle. A
-// partition's SMs may not hold a cluster.
-cudaError_t split_for(const LinearArgs& a, int device, int num_sms, bool partition, int* split) {
-    *split = 1;
-    const int64_t tiles = a.row_tiles * a.col_tiles;
-    if (partition || 2 * tiles > num_sms) return cudaSuccess;
+int64_t up(int64_t v, int64_t by) { return (v + by - 1) / by; }
+
+// Who works on a tile, and how many CTAs share one. A partition's SMs may not
+// hold a cluster.
+struct Plan {
+    Mode mode;
+    int split;
+    int clusters;  // pairs at a time
+};
+cudaError_t plan_for(const LinearArgs& a, bool gated, int device, int num_sms, bool partition,
+                     Plan* plan) {
+    *plan = {kAlone, 1, 0};
+    if (partition) return cudaSuccess;
     ResidentClusters clusters{};
     const cudaError_t err = resident_clusters(device, &clusters);
     if (err != cudaSuccess) return err;
+    const int half = gated ? 2 : 1;
+    const int64_t pairs = up(a.m, Shape<kPair>::kTileRows) * up(a.n, Shape<kPair>::kCols / half);
+    const int64_t tiles = up(a.m, kRows) * up(a.n, Shape<kAlone>::kCols / half);
+    // a block along k takes a pair 512 cycles on its tile and a CTA about 300 on its own
+    const int64_t pair_time = up(pairs, clusters.n[2]) * 512, alone_time = up(tiles, num_sms) * 300;
+    if (clusters.n[2] > 0 && pair_time < alone_time) {
+        *plan = {kPair, 1, clusters.n[2]};
+        return cudaSuccess;
+    }
     int n = 1;
     while (n < kMaxSplit && tiles <= clusters.n[2 * n] && a.k_blocks >= 4 * n) n *= 2;
-    *split = n;
+    if (n > 1) *plan = {kShared, n, 0};
     return cudaSuccess;
 }
 
 }  // namespace
 
-int64_t linear_tiles(int64_t m, int64_t n, bool gated) {
-    const int cols = gated ? kBlock : kTileCols;
-    return ((m + kTileRows - 1) / kTileRows) * ((n + cols - 1) / cols);
-}
-
 cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_t stream) {
     const bool gated = a.act == EP_ACT_SWIGLU;
-    const int cols = gated ? kBlock : kTileCols;
-    a.k_blocks = static_cast<int>((a.k + kTileK - 1) / kTileK);
-    a.row_tiles = (a.m + kTileRows - 1) / kTileRows;
-    a.col_tiles = (a.n + cols - 1) / cols;
+    const int half = gated ? 2 : 1;
+    if (!a.a_by_k && !a.b_by_k && a.m <= kFewRows) return launch_linear_few(a, stream);
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    a.k_blocks = static_cast<int>(up(a.k, kTileK));
+    Plan plan{};
+    if (err == cudaSuccess) err = plan_for(a, gated, device, num_sms, partition, &plan);
+    if (err != cudaSuccess) return err;
+    const bool pair = plan.mode == kPair;
+    const int cols = pair ? Shape<kPair>::kCols : Shape<kAlone>::kCols;
+    a.split = plan.split;
+    a.row_tiles = up(a.m, pair ? Shape<kPair>::kTileRows : kRows);
+    a.col_tiles = up(a.n, cols / half);
     Maps maps;
     maps.a_rows = 16;  // no more than there are
-    while (maps.a_rows < kTileRows && maps.a_rows < a.m) maps.a_rows *= 2;
-    const int64_t b_rows = gated ? 2 * a.n : a.n;
+    while (maps.a_rows < kRows && (pair || maps.a_rows < a.m)) maps.a_rows *= 2;
+    const int64_t b_rows = half * a.n;
     const bool ok =
         (a.a_by_k ? encode_map(&maps.a, a.a, a.k, a.m, a.a_pitch, kTileK)
                   : encode_map(&maps.a, a.a, a.m, a.k, a.a_pitch, maps.a_rows)) &&
         (a.b_by_k ? encode_map(&maps.b, a.b, a.k, b_rows, a.b_pitch, kTileK)
-                  : encode_map(&maps.b, a.b, b_rows, a.k, a.b_pitch, kBlock));
+                  : encode_map(&maps.b, a.b, b_rows, a.k, a.b_pitch, cols / 2));
     if (!ok) return cudaErrorInvalidValue;
-    int device = 0;
-    cudaError_t err = cudaGetDevice(&device);
-    if (err == cudaSuccess) err = split_for(a, device, num_sms, partition, &a.split);
-    if (err != cudaSuccess) return err;
     const int64_t tiles = a.row_tiles * a.col_tiles;
-    const int grid = static_cast<int>(a.split > 1 ? tiles * a.split : tiles < num_sms ? tiles : num_sms);
-    if (a.split > 1)
-        return gated ? launch<true, true>(a, maps, grid, stream) : launch<false, true>(a, maps, grid, stream);
-    return gated ? launch<true, false>(a, maps, grid, stream) : launch<false, false>(a, maps, grid, stream);
+    const bool exact = a.out_f32 && a.k_blocks > kExactBlocks;
+    if (pair) {
+        const int grid = 2 * static_cast<int>(tiles < plan.clusters ? tiles : plan.clusters);
+        if (exact)
+            return gated ? launch<kPair, true, true>(a, maps, grid, 2, stream)
+                         : launch<kPair, false, true>(a, maps, grid, 2, stream);
+        return gated ? launch<kPair, true, false>(a, maps, grid, 2, stream)
+                     : launch<kPair, false, false>(a, maps, grid, 2, stream);
+    }
+    if (plan.mode == kShared) {
+        const int grid = static_cast<int>(tiles) * a.split;
+        return gated ? launch<kShared, true, false>(a, maps, grid, a.split, stream)
+                     : launch<kShared, false, false>(a, maps, grid, a.split, stream);
+    }
+    const int grid = static_cast<int>(tiles < num_sms ? tiles : num_sms);
+    if (exact)
+        return gated ? launch<kAlone, true, true>(a, maps, grid, 1, stream)
+                     : launch<kAlone, false, true>(a, maps, grid, 1, stream);
+    return gated ? launch<kAlone, true, false>(a, maps, grid, 1, stream)
+                 : launch<kAlone, false, false>(a, maps, grid, 1, stream);
 }
 
 }  // namespace ep

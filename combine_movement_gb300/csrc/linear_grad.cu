@@ -80,6 +80,7 @@ __device__ __forceinline__ void store_row(uint16_t* q, const float (&v)[W]) {
 template <int W, int kLanes, bool kGated>
 __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs a) {
     constexpr int kHalves = kGated ? 2 : 1, kRows = kThreads / kLanes, kCols = W * kLanes;
+    constexpr int kAtOnce = W == 8 ? 2 : 4;  // rows whose loads are in flight
     __shared__ float part[kThreads / 32][kHalves][kCols];
     __shared__ float total[kHalves][kCols];
     griddep_wait();
@@ -90,30 +91,38 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs a)
     const bool in = col < a.n;  // (W divides n)
     float sum[kHalves][W] = {};
     const int64_t wide = kHalves * a.n;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + rl; r < a.m && in;
-         r += static_cast<int64_t>(gridDim.x) * kRows) {
-        float dy[W], g[W], u[W];
-        load_row<W>(a.dy, a.dy_f32, r * a.n + col, dy);
-        if (a.act != EP_ACT_NONE) load_row<W>(a.z, false, r * wide + col, g);
-        if (kGated) {
-            load_row<W>(a.z, false, r * wide + a.n + col, u);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows + rl; r0 < a.m && in;
+         r0 += kAtOnce * step) {
+        float dy[kAtOnce][W], g[kAtOnce][W], u[kAtOnce][W];
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float du = dy[i] * silu(g[i]);
-                g[i] = dy[i] * u[i] * silu_slope(g[i]);
-                u[i] = du;
-                sum[kHalves - 1][i] += du;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i)
-                g[i] = a.act == EP_ACT_NONE ? dy[i] : dy[i] * activate_slope(g[i], a.act);
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int64_t r = r0 + j * step;
+            if (r >= a.m) break;
+            load_row<W>(a.dy, a.dy_f32, r * a.n + col, dy[j]);
+            if (a.act != EP_ACT_NONE) load_row<W>(a.z, false, r * wide + col, g[j]);
+            if (kGated) load_row<W>(a.z, false, r * wide + a.n + col, u[j]);
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i) sum[0][i] += g[i];
-        if (a.dz != nullptr) {
-            store_row<W>(a.dz + r * a.pitch + col, g);
-            if (kGated) store_row<W>(a.dz + r * a.pitch + a.n + col, u);
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int64_t r = r0 + j * step;
+            if (r >= a.m) break;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                if (kGated) {
+                    const float du = dy[j][i] * silu(g[j][i]);
+                    g[j][i] = dy[j][i] * u[j][i] * silu_slope(g[j][i]);
+                    u[j][i] = du;
+                    sum[kHalves - 1][i] += du;
+                } else {
+                    g[j][i] = a.act == EP_ACT_NONE ? dy[j][i] : dy[j][i] * activate_slope(g[j][i], a.act);
+                }
+                sum[0][i] += g[j][i];
+            }
+            if (a.dz != nullptr) {
+                store_row<W>(a.dz + r * a.pitch + col, g[j]);
+                if (kGated) store_row<W>(a.dz + r * a.pitch + a.n + col, u[j]);
+            }
         }
     }
     if (a.d_bias == nullptr) return;

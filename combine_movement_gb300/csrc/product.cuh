@@ -74,14 +74,20 @@ __device__ __forceinline__ void cluster_wait() {
 
 // Wait of a whole warp on a barrier; false, in every lane, once a lane gave up
 // after kWaitLimitNs or another warp did (the word at `abort`). The timer is
-// slow to read, so the first tries go without.
+// slow to read, so the first tries go without. kCluster: arrivals come from other
+// CTAs too.
+template <bool kCluster>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    return kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+}
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort,
                                           int32_t* status) {
     for (int i = 0; i < 256; ++i)
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(0xFFFFFFFFu, try_wait<kCluster>(bar, parity))) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(0xFFFFFFFFu, try_wait<kCluster>(bar, parity))) return true;
         const bool late = global_timer_ns() - t0 > kWaitLimitNs;
         if (late) {
             store_shared(abort, 1);
@@ -90,10 +96,11 @@ __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_
         if (__any_sync(0xFFFFFFFFu, late || load_shared(abort) != 0)) return false;
     }
 }
+template <bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort,
                                           int32_t* status) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    return wait_slow(bar, parity, abort, status);
+    if (__all_sync(0xFFFFFFFFu, try_wait<kCluster>(bar, parity))) return true;
+    return wait_slow<kCluster>(bar, parity, abort, status);
 }
 
 // Position in a ring of N: index, and the parity of its current round.

@@ -122,6 +122,37 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
+// ---- pairs of CTAs ----------------------------------------------------------------
+// The two CTAs of a cluster work on one tile of twice the rows: each holds its
+// rows of A, half of B's and its rows' sums; rank 0 issues the products. Tensor
+// memory is allocated and released by a warp of each.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+                 "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t addr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t desc,
+                                              bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(desc), "r"(static_cast<uint32_t>(accumulate))
+        : "memory");
+}
+// Arrive on `bar` of both CTAs.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
 // ---- registers ------------------------------------------------------------------
 // By all warps of a warpgroup; the kernel's warpgroups together stay within
 // the registers it was launched with.
@@ -151,6 +182,17 @@ __device__ __forceinline__ void tensor_load_2d(uint32_t dst_smem, const CUtensor
         : "memory");
 }
 
+// The same into this CTA's shared memory, completing on `bar`, a shared::cluster
+// address in either CTA of the pair.
+__device__ __forceinline__ void tensor_load_2d_pair(uint32_t dst_smem, const CUtensorMap* map,
+                                                    int32_t x, int32_t y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst_smem),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
 // ---- small asynchronous copies ------------------------------------------------------
 // Four bytes global -> shared by this lane; copy_async_arrive makes one
 // (already counted) arrival on `bar` when this lane's copies so far are done.
@@ -175,6 +217,11 @@ __device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool arrive) {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// On a barrier of either CTA of a cluster (a shared::cluster address).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 }  // namespace ep
