@@ -37,14 +37,12 @@ constexpr int kTileK = 64;                   // values of one stage along k
 constexpr uint32_t kRowBytes = kTileK * 2;
 constexpr uint32_t kGroupBytes = 64 * 128;   // 64 along k x 64 along m or n
 constexpr uint32_t kStageA = kRows * kRowBytes;
-constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr int kSlots = 2;
 constexpr int kOutWarps = 8;
 constexpr int kProductWarp = kOutWarps, kCopyWarp = kOutWarps + 1;
 constexpr int kThreads = (kOutWarps + 2) * 32;
 constexpr int kChunk = 32;                   // columns turned around at a time
 constexpr uint32_t kTurnBytes = 32 * kChunk * 4;
-constexpr size_t kSmem = 1024 + kRingBytes + kOutWarps * kTurnBytes;
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;
 constexpr int kRowGroup = 8;                 // row tiles that share a column tile's turn
@@ -57,7 +55,11 @@ struct Shape {
     static constexpr int kTileRows = kMode == kPair ? 2 * kRows : kRows;
     static constexpr int kOwnB = kMode == kPair ? kCols / 2 : kCols;  // rows of b in one CTA
     static constexpr uint32_t kStageBytes = kStageA + kOwnB * kRowBytes;
-    static constexpr int kStages = kRingBytes / kStageBytes;
+    // (shared tiles leave room for the next kernel's CTA beside theirs, so that it has
+    // begun when they end)
+    static constexpr int kStages = kMode == kShared ? 4 : 192 * 1024 / kStageBytes;
+    static constexpr uint32_t kRingBytes = kStages * kStageBytes;
+    static constexpr size_t kSmem = 1024 + kRingBytes + (kMode == kShared ? 0 : kOutWarps * kTurnBytes);
     static constexpr int kMine = kCols / 2;  // columns of sums that a warp takes
     // a shared tile's sums, [row][column] in fp32, in the stages' place
     static constexpr uint32_t kPitch = kCols * 4 + 16;
@@ -105,126 +107,158 @@ struct Part {
     int rows;
 };
 
+// How a warp goes through 32 rows of a chunk of kCols columns of out, N of them to a
+// lane: kRounds times kAtOnce rows.
+template <int N, bool kGated>
+struct Walk {
+    static constexpr int kCols = kGated ? kChunk / 2 : kChunk;
+    static constexpr int kPieces = kCols / N, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
+};
+
 // What a lane adds to its values of a chunk, or of a quarter of one, read ahead
 // of them.
 template <int kQuarters>
 struct Ahead {
     uint32_t bits[8 * kQuarters];
 };
+template <int N, bool kGated, int kQuarters>
+__device__ __forceinline__ void read_ahead_by(const LinearArgs& a, const Part& part, int64_t col,
+                                              int quarter, Ahead<kQuarters>& ahead) {
+    using W = Walk<N, kGated>;
+    constexpr int kRounds = W::kRounds * kQuarters / 4;
+    const int lane = threadIdx.x & 31;
+    const int64_t c = col + lane % W::kPieces * N;
+    if (c >= a.n) return;
+    const int r0 = lane / W::kPieces + quarter * (W::kRounds / 4) * W::kAtOnce;
+    int64_t at = (part.row0 + r0) * a.n + c;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i, at += W::kAtOnce * a.n) {
+        if (r0 + i * W::kAtOnce >= part.rows) continue;
+        const Residual<N> v = load_residual<N>(a, at);
+#pragma unroll
+        for (int j = 0; j < N; ++j) ahead.bits[N * i + j] = v.bits[j];
+    }
+}
 template <bool kGated, int kQuarters>
 __device__ __forceinline__ void read_ahead(const LinearArgs& a, const Part& part, int64_t col,
                                            int quarter, Ahead<kQuarters>& ahead) {
-    constexpr int kCols = kGated ? kChunk / 2 : kChunk;
-    const int lane = threadIdx.x & 31;
     if (a.residual == nullptr) return;
-    if (a.n % 4 == 0) {
-        constexpr int kPieces = kCols / 4, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
-        const int64_t c = col + lane % kPieces * 4;
-#pragma unroll
-        for (int i = 0; i < kRounds * kQuarters / 4; ++i) {
-            const int r = lane / kPieces + (quarter * (kRounds / 4) + i) * kAtOnce;
-            if (r >= part.rows || c >= a.n) continue;
-            const Residual<4> v = load_residual<4>(a, (part.row0 + r) * a.n + c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) ahead.bits[4 * i + j] = v.bits[j];
-        }
-    } else {
-        constexpr int kAtOnce = 32 / kCols, kRounds = 32 / kAtOnce;
-        const int64_t c = col + lane % kCols;
-#pragma unroll
-        for (int i = 0; i < kRounds * kQuarters / 4; ++i) {
-            const int r = lane / kCols + (quarter * (kRounds / 4) + i) * kAtOnce;
-            if (r < part.rows && c < a.n)
-                ahead.bits[i] = load_residual<1>(a, (part.row0 + r) * a.n + c).bits[0];
-        }
-    }
+    if (a.n % 4 == 0)
+        read_ahead_by<4, kGated>(a, part, col, quarter, ahead);
+    else
+        read_ahead_by<1, kGated>(a, part, col, quarter, ahead);
 }
 
 // 32 x 32 sums from the turning place, or with a quarter's Ahead 8 rows of them:
 // `col` the column of the first (gated: of 16 of each half).
+template <int N, bool kGated, int kQuarters>
+__device__ __forceinline__ void write_chunk_by(const LinearArgs& a, uint32_t turn, const Part& part,
+                                               int64_t col, int quarter,
+                                               const Ahead<kQuarters>& ahead) {
+    using W = Walk<N, kGated>;
+    constexpr int kRounds = W::kRounds * kQuarters / 4;
+    const int lane = threadIdx.x & 31, p = lane % W::kPieces;
+    const int64_t c = col + p * N;
+    if (c >= a.n) return;
+    const int r0 = lane / W::kPieces + quarter * (W::kRounds / 4) * W::kAtOnce;
+    Values<N> v[kRounds], up[kRounds];
+    Residual<N> res[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int r = r0 + i * W::kAtOnce;
+        if constexpr (N == 4) {
+            const float4 f = load_shared_v4(turn_at(turn, r, p));
+            v[i] = {{f.x, f.y, f.z, f.w}};
+            if (kGated) {
+                const float4 u = load_shared_v4(turn_at(turn, r, p + W::kPieces));
+                up[i] = {{u.x, u.y, u.z, u.w}};
+            }
+        } else {
+            v[i] = {{load_shared_f32(turn_at(turn, r, p / 4) + p % 4 * 4)}};
+            if (kGated) up[i] = {{load_shared_f32(turn_at(turn, r, (p + W::kCols) / 4) + p % 4 * 4)}};
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) res[i].bits[j] = ahead.bits[N * i + j];
+    }
+    if (a.bias != nullptr) {
+        const Values<N> b0 = load_bias<N>(a, c), b1 = load_bias<N>(a, kGated ? a.n + c : c);
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) {
+            v[i] = sum<N>(v[i], b0);
+            if (kGated) up[i] = sum<N>(up[i], b1);
+        }
+    }
+    const int rows = (part.rows - r0 + W::kAtOnce - 1) / W::kAtOnce;
+    finish<kRounds, N, kGated>(a, part.row0 + r0, c, W::kAtOnce, rows, v, up, res);
+}
 template <bool kGated, int kQuarters>
 __device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
                                             int64_t col, int quarter, const Ahead<kQuarters>& ahead) {
-    constexpr int kCols = kGated ? kChunk / 2 : kChunk;  // of out
-    const int lane = threadIdx.x & 31;
-    if (a.n % 4 == 0) {
-        constexpr int kPieces = kCols / 4, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
-        const int p = lane % kPieces;
-        const int64_t c = col + 4 * p;
-        if (c >= a.n) return;
-        const Values<4> b0 = load_bias<4>(a, c), b1 = load_bias<4>(a, kGated ? a.n + c : c);
-#pragma unroll
-        for (int i = 0; i < kRounds * kQuarters / 4; ++i) {
-            const int r = lane / kPieces + (quarter * (kRounds / 4) + i) * kAtOnce;
-            if (r >= part.rows) break;
-            const float4 f = load_shared_v4(turn_at(turn, r, p));
-            const float4 u = kGated ? load_shared_v4(turn_at(turn, r, p + kPieces)) : f;
-            const Residual<4> res = {{ahead.bits[4 * i], ahead.bits[4 * i + 1], ahead.bits[4 * i + 2],
-                                      ahead.bits[4 * i + 3]}};
-            finish<4, kGated>(a, part.row0 + r, c, sum<4>({{f.x, f.y, f.z, f.w}}, b0),
-                              sum<4>({{u.x, u.y, u.z, u.w}}, b1), res);
-        }
-    } else {  // rows that do not start on 16 bytes: value by value
-        constexpr int kAtOnce = 32 / kCols, kRounds = 32 / kAtOnce;
-        const int cl = lane % kCols;
-        const int64_t c = col + cl;
-        if (c >= a.n) return;
-        const Values<1> b0 = load_bias<1>(a, c), b1 = load_bias<1>(a, kGated ? a.n + c : c);
-#pragma unroll
-        for (int i = 0; i < kRounds * kQuarters / 4; ++i) {
-            const int r = lane / kCols + (quarter * (kRounds / 4) + i) * kAtOnce;
-            if (r >= part.rows) break;
-            const float f = load_shared_f32(turn_at(turn, r, cl / 4) + cl % 4 * 4);
-            const float u =
-                kGated ? load_shared_f32(turn_at(turn, r, (cl + kCols) / 4) + cl % 4 * 4) : f;
-            finish<1, kGated>(a, part.row0 + r, c, {{f + b0.v[0]}}, {{u + b1.v[0]}}, {{ahead.bits[i]}});
-        }
-    }
+    if (a.n % 4 == 0)
+        write_chunk_by<4, kGated>(a, turn, part, col, quarter, ahead);
+    else  // rows that do not start on 16 bytes: value by value
+        write_chunk_by<1, kGated>(a, turn, part, col, quarter, ahead);
 }
 
 // The sums of a tile that the cluster's CTAs took parts of k of: each has laid
 // its own out in shared memory; CTA `rank` adds, in the parts' order, and writes
-// those of the rows r = rank mod kParts.
+// those of the rows r = rank mod kParts. A thread takes N neighbouring columns of
+// kAtOnce rows at a time, so that its loads overlap.
 template <int N, bool kGated, int kParts>
 __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
                                                   int rank) {
     using S = Shape<kShared>;
     constexpr int kCols = kGated ? S::kCols / 2 : S::kCols, kPieces = kCols / N;
+    constexpr int kStep = kOutWarps * 32 / kPieces;  // of this CTA's rows, by all threads
+    constexpr int kMost = kRows / kParts / kStep;    // of them to a thread
+    constexpr int kAtOnce = kMost < 1 ? 1 : kMost < 8 / kParts ? kMost : 8 / kParts;
     const int64_t left = a.m - tile.row0;
     const int rows = static_cast<int>(left < kRows ? left : kRows);
-    const int pieces = (rows + kParts - 1 - rank) / kParts * kPieces;
-    const int64_t col0 = tile.col_tile * kCols;
-    for (int i = threadIdx.x; i < pieces; i += kOutWarps * 32) {
-        const int r = i / kPieces * kParts + rank, c = i % kPieces * N;
-        if (col0 + c >= a.n) continue;
-        const int64_t row = tile.row0 + r, col = col0 + c;
-        Residual<N> res = {};
-        if (a.residual != nullptr) res = load_residual<N>(a, row * a.n + col);
-        const uint32_t at = sums + r * S::kPitch + c * 4;
-        Values<N> v[kParts], up[kParts];
+    const int own = (rows + kParts - 1 - rank) / kParts;
+    const int c = threadIdx.x % kPieces * N;
+    const int64_t col = tile.col_tile * kCols + c;
+    if (col >= a.n) return;
+    const Values<N> b0 = load_bias<N>(a, col), b1 = load_bias<N>(a, kGated ? a.n + col : col);
+    for (int i0 = threadIdx.x / kPieces; i0 < own; i0 += kAtOnce * kStep) {
+        Values<N> v[kAtOnce][kParts], up[kAtOnce][kParts], vs[kAtOnce], us[kAtOnce];
+        Residual<N> res[kAtOnce] = {};
+        const int64_t row = tile.row0 + i0 * kParts + rank;
 #pragma unroll
-        for (int p = 0; p < kParts; ++p) {
-            const uint32_t from = cluster_map(at, p);
-            if constexpr (N == 4) {
-                const float4 f = load_cluster_v4(from);
-                v[p] = {{f.x, f.y, f.z, f.w}};
-                if (kGated) {
-                    const float4 u = load_cluster_v4(from + kCols * 4);
-                    up[p] = {{u.x, u.y, u.z, u.w}};
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int i = i0 + j * kStep;
+            if (i >= own) continue;
+            if (a.residual != nullptr)
+                res[j] = load_residual<N>(a, (row + static_cast<int64_t>(j) * kStep * kParts) * a.n + col);
+            const uint32_t at = sums + (i * kParts + rank) * S::kPitch + c * 4;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                const uint32_t from = cluster_map(at, p);
+                if constexpr (N == 4) {
+                    const float4 f = load_cluster_v4(from);
+                    v[j][p] = {{f.x, f.y, f.z, f.w}};
+                    if (kGated) {
+                        const float4 u = load_cluster_v4(from + kCols * 4);
+                        up[j][p] = {{u.x, u.y, u.z, u.w}};
+                    }
+                } else {
+                    v[j][p] = {{load_cluster_f32(from)}};
+                    if (kGated) up[j][p] = {{load_cluster_f32(from + kCols * 4)}};
                 }
-            } else {
-                v[p] = {{load_cluster_f32(from)}};
-                if (kGated) up[p] = {{load_cluster_f32(from + kCols * 4)}};
             }
         }
 #pragma unroll
-        for (int p = 1; p < kParts; ++p) {
-            v[0] = sum<N>(v[0], v[p]);
-            if (kGated) up[0] = sum<N>(up[0], up[p]);
+        for (int j = 0; j < kAtOnce; ++j) {
+            vs[j] = v[j][0];
+            if (kGated) us[j] = up[j][0];
+#pragma unroll
+            for (int p = 1; p < kParts; ++p) {
+                vs[j] = sum<N>(vs[j], v[j][p]);
+                if (kGated) us[j] = sum<N>(us[j], up[j][p]);
+            }
+            vs[j] = sum<N>(vs[j], b0);
+            if (kGated) us[j] = sum<N>(us[j], b1);
         }
-        v[0] = sum<N>(v[0], load_bias<N>(a, col));
-        if (kGated) up[0] = sum<N>(up[0], load_bias<N>(a, a.n + col));
-        finish<N, kGated>(a, row, col, v[0], kGated ? up[0] : v[0], res);
+        finish<kAtOnce, N, kGated>(a, row, col, kStep * kParts, (own - i0 + kStep - 1) / kStep, vs, us, res);
     }
 }
 template <int N, bool kGated>
@@ -422,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---- results: warp = 32 rows (its quarter) and half of the columns ----
         const int quarter = warp & 3, half = warp >> 2;
-        const uint32_t turn = base + kRingBytes + warp * kTurnBytes;
+        const uint32_t turn = base + S::kRingBytes + warp * kTurnBytes;
         const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t read = kMode == kPair ? cluster_map(sums_read, 0) : sums_read;
         // of out, in a chunk, and the warp's
@@ -592,38 +626,47 @@ bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t width
 template <Mode kMode, bool kGated, bool kExact>
 cudaError_t launch(const LinearArgs& a, const Maps& maps, int grid, int cluster, cudaStream_t stream) {
     auto kern = linear_kernel<kMode, kGated, kExact>;
+    constexpr size_t kSmem = Shape<kMode>::kSmem;
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(kSmem));
     if (err != cudaSuccess) return err;
     return launch_dependent_clusters(kern, grid, cluster, kThreads, kSmem, stream, a, maps);
 }
 
-// Clusters of 2, 4, 8 CTAs that a device holds at a time: fewer than SMs / size,
-// because a cluster's lie in one part (GPC) of it.
+// Pairs, and clusters of 2, 4, 8 CTAs that share a tile, that a device holds at a
+// time: fewer than SMs / size, because a cluster's lie in one part (GPC) of it.
 struct ResidentClusters {
+    int pairs;
     int n[kMaxSplit + 1];
 };
+
+template <Mode kMode>
+cudaError_t count_clusters(int size, int* n) {
+    auto kern = linear_kernel<kMode, false, false>;
+    constexpr size_t kSmem = Shape<kMode>::kSmem;
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(kSmem));
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(size);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+}
 
 cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
     static PerDevice<ResidentClusters> table;
     return table.get(device, clusters, [](ResidentClusters* found) {
-        auto kern = linear_kernel<kShared, false, false>;
-        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kSmem));
-        for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2) {
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(static_cast<unsigned>(split));
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = kSmem;
-            cudaLaunchAttribute attr{};
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = static_cast<unsigned>(split);
-            attr.val.clusterDim.y = 1;
-            attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            err = cudaOccupancyMaxActiveClusters(&found->n[split], kern, &cfg);
-        }
+        cudaError_t err = count_clusters<kPair>(2, &found->pairs);
+        for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2)
+            err = count_clusters<kShared>(split, &found->n[split]);
         return err;
     });
 }
@@ -648,9 +691,9 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, int device, int num_sms, b
     const int64_t pairs = up(a.m, Shape<kPair>::kTileRows) * up(a.n, Shape<kPair>::kCols / half);
     const int64_t tiles = up(a.m, kRows) * up(a.n, Shape<kAlone>::kCols / half);
     // a block along k takes a pair 512 cycles on its tile and a CTA about 300 on its own
-    const int64_t pair_time = up(pairs, clusters.n[2]) * 512, alone_time = up(tiles, num_sms) * 300;
-    if (clusters.n[2] > 0 && pair_time < alone_time) {
-        *plan = {kPair, 1, clusters.n[2]};
+    const int64_t pair_time = up(pairs, clusters.pairs > 0 ? clusters.pairs : 1) * 512, alone_time = up(tiles, num_sms) * 300;
+    if (clusters.pairs > 0 && pair_time < alone_time) {
+        *plan = {kPair, 1, clusters.pairs};
         return cudaSuccess;
     }
     int n = 1;

@@ -8,8 +8,8 @@
 // follow take bf16 operands, so dz is rounded to it, as z was when it was kept; the
 // sums are not.
 //
-// Mapping: a CTA to a strip of 64 columns (32 where rows do not start on 8 bytes)
-// and every c-th group of rows, a thread to a few columns of a row; a strip's
+// Mapping: a CTA to a strip of 64 columns (32 where rows do not start on 8 bytes;
+// a quarter of those where few columns are summed) and every c-th group of rows, a thread to a few columns of a row; a strip's
 // rows go to the c CTAs of a cluster. A thread adds its rows, the CTA its threads,
 // the cluster its CTAs, each in a fixed order, so that equal calls give equal
 // bits.
@@ -29,41 +29,44 @@ constexpr unsigned kFullMask = 0xFFFFFFFFu;
 constexpr int kThreads = 256;
 constexpr int kMaxCluster = 8;
 
+// W values of a row as they lie in memory.
 template <int W>
-__device__ __forceinline__ void load_row(const void* p, bool f32, int64_t at, float (&v)[W]) {
+struct Raw {
+    uint32_t bits[W];
+};
+template <int W>
+__device__ __forceinline__ Raw<W> load_row(const void* p, bool f32, int64_t at) {
+    Raw<W> r;
     if (f32) {
-        const float* q = static_cast<const float*>(p) + at;
+        const uint32_t* q = static_cast<const uint32_t*>(p) + at;
         if constexpr (W == 1) {
-            v[0] = __ldg(q);
+            r.bits[0] = __ldg(q);
         } else {
 #pragma unroll
             for (int i = 0; i < W; i += 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(q + i));
-                v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+                const uint4 f = __ldg(reinterpret_cast<const uint4*>(q + i));
+                r.bits[i] = f.x, r.bits[i + 1] = f.y, r.bits[i + 2] = f.z, r.bits[i + 3] = f.w;
             }
         }
-        return;
+        return r;
     }
     const uint16_t* q = static_cast<const uint16_t*>(p) + at;
     if constexpr (W == 1) {
-        v[0] = __uint_as_float(static_cast<uint32_t>(__ldg(q)) << 16);
+        r.bits[0] = static_cast<uint32_t>(__ldg(q)) << 16;
     } else if constexpr (W == 4) {
         const uint2 f = __ldg(reinterpret_cast<const uint2*>(q));
-        const uint32_t w[2] = {f.x, f.y};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        r.bits[0] = f.x, r.bits[1] = f.y;
     } else {
         const uint4 f = __ldg(reinterpret_cast<const uint4*>(q));
-        const uint32_t w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        r.bits[0] = f.x, r.bits[1] = f.y, r.bits[2] = f.z, r.bits[3] = f.w;
     }
+    return r;
+}
+// Value i of them.
+template <int W>
+__device__ __forceinline__ float value(const Raw<W>& r, bool f32, int i) {
+    if (W == 1 || f32) return __uint_as_float(r.bits[i]);
+    return __uint_as_float(i % 2 == 0 ? r.bits[i / 2] << 16 : r.bits[i / 2] & 0xFFFF0000u);
 }
 template <int W>
 __device__ __forceinline__ void store_row(uint16_t* q, const float (&v)[W]) {
@@ -77,8 +80,8 @@ __device__ __forceinline__ void store_row(uint16_t* q, const float (&v)[W]) {
 }
 
 // W columns to a thread, kLanes threads to a row's part.
-template <int W, int kLanes, bool kGated>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs a) {
+template <int W, int kLanes, bool kGated, bool kF32>
+__global__ void __launch_bounds__(kThreads, 2) act_grad_kernel(const ActGradArgs a) {
     constexpr int kHalves = kGated ? 2 : 1, kRows = kThreads / kLanes, kCols = W * kLanes;
     constexpr int kAtOnce = W == 8 ? 2 : 4;  // rows whose loads are in flight
     __shared__ float part[kThreads / 32][kHalves][kCols];
@@ -94,34 +97,35 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs a)
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
     for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows + rl; r0 < a.m && in;
          r0 += kAtOnce * step) {
-        float dy[kAtOnce][W], g[kAtOnce][W], u[kAtOnce][W];
+        Raw<W> dy[kAtOnce], z[kAtOnce], zu[kAtOnce];
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int64_t r = r0 + j * step;
-            if (r >= a.m) break;
-            load_row<W>(a.dy, a.dy_f32, r * a.n + col, dy[j]);
-            if (a.act != EP_ACT_NONE) load_row<W>(a.z, false, r * wide + col, g[j]);
-            if (kGated) load_row<W>(a.z, false, r * wide + a.n + col, u[j]);
+            if (r >= a.m) continue;
+            dy[j] = load_row<W>(a.dy, kF32, r * a.n + col);
+            if (a.act != EP_ACT_NONE) z[j] = load_row<W>(a.z, false, r * wide + col);
+            if (kGated) zu[j] = load_row<W>(a.z, false, r * wide + a.n + col);
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int64_t r = r0 + j * step;
-            if (r >= a.m) break;
+            if (r >= a.m) continue;
+            float g[W], u[W];
 #pragma unroll
             for (int i = 0; i < W; ++i) {
+                const float d = value<W>(dy[j], kF32, i), v = value<W>(z[j], false, i);
                 if (kGated) {
-                    const float du = dy[j][i] * silu(g[j][i]);
-                    g[j][i] = dy[j][i] * u[j][i] * silu_slope(g[j][i]);
-                    u[j][i] = du;
-                    sum[kHalves - 1][i] += du;
+                    u[i] = d * silu(v);
+                    g[i] = d * value<W>(zu[j], false, i) * silu_slope(v);
+                    sum[kHalves - 1][i] += u[i];
                 } else {
-                    g[j][i] = a.act == EP_ACT_NONE ? dy[j][i] : dy[j][i] * activate_slope(g[j][i], a.act);
+                    g[i] = a.act == EP_ACT_NONE ? d : d * activate_slope(v, a.act);
                 }
-                sum[0][i] += g[j][i];
+                sum[0][i] += g[i];
             }
             if (a.dz != nullptr) {
-                store_row<W>(a.dz + r * a.pitch + col, g[j]);
-                if (kGated) store_row<W>(a.dz + r * a.pitch + a.n + col, u[j]);
+                store_row<W>(a.dz + r * a.pitch + col, g);
+                if (kGated) store_row<W>(a.dz + r * a.pitch + a.n + col, u);
             }
         }
     }
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradArgs a)
     cluster_wait();  // no CTA reads this one's sums any more
 }
 
-template <int W, int kLanes, bool kGated>
+template <int W, int kLanes, bool kGated, bool kF32>
 cudaError_t launch(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
     constexpr int kRows = kThreads / kLanes, kCols = W * kLanes;
     const int64_t strips = (a.n + kCols - 1) / kCols;
@@ -187,21 +191,33 @@ cudaError_t launch(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, act_grad_kernel<W, kLanes, kGated>, a);
+    return cudaLaunchKernelEx(&cfg, act_grad_kernel<W, kLanes, kGated, kF32>, a);
 }
 
-template <bool kGated>
+// Strips of a quarter of the columns where the clusters of whole ones leave SMs
+// idle.
+template <int W, int kLanes, bool kGated, bool kF32>
+cudaError_t launch_lanes(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
+    if (a.d_bias != nullptr && (a.n + W * kLanes - 1) / (W * kLanes) * kMaxCluster < num_sms)
+        return launch<W, kLanes / 4, kGated, kF32>(a, num_sms, stream);
+    return launch<W, kLanes, kGated, kF32>(a, num_sms, stream);
+}
+
+template <bool kGated, bool kF32>
 cudaError_t launch_width(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.n % 8 == 0) return launch<8, 8, kGated>(a, num_sms, stream);
-    if (a.n % 4 == 0) return launch<4, 16, kGated>(a, num_sms, stream);
-    return launch<1, 32, kGated>(a, num_sms, stream);
+    if (a.n % 8 == 0) return launch_lanes<8, 8, kGated, kF32>(a, num_sms, stream);
+    if (a.n % 4 == 0) return launch_lanes<4, 16, kGated, kF32>(a, num_sms, stream);
+    return launch_lanes<1, 32, kGated, kF32>(a, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_act_grad(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
-    return a.act == EP_ACT_SWIGLU ? launch_width<true>(a, num_sms, stream)
-                                  : launch_width<false>(a, num_sms, stream);
+    if (a.act == EP_ACT_SWIGLU)
+        return a.dy_f32 ? launch_width<true, true>(a, num_sms, stream)
+                        : launch_width<true, false>(a, num_sms, stream);
+    return a.dy_f32 ? launch_width<false, true>(a, num_sms, stream)
+                    : launch_width<false, false>(a, num_sms, stream);
 }
 
 }  // namespace ep

@@ -81,34 +81,69 @@ __device__ __forceinline__ Values<N> load_bias(const LinearArgs& a, int64_t col)
     return r;
 }
 
-// The end of N values of out's row `row` from column `col` on: sums with their
-// bias in `v` (gated: the up half's in `up`), `residual` what is added.
-template <int N, bool kGated>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int64_t col, Values<N> v,
-                                       const Values<N>& up, const Residual<N>& residual) {
-    if (a.z != nullptr) {
-        uint16_t* z = a.z + row * (kGated ? 2 * a.n : a.n) + col;
-        store_bf16<N>(z, v);
-        if (kGated) store_bf16<N>(z + a.n, up);
-    }
-    const Values<N> res = residual_values<N>(a, residual);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v.v[i] = kGated ? silu(v.v[i]) * up.v[i] : activate(v.v[i], a.act);
-        v.v[i] += res.v[i];
-    }
-    const int64_t at = row * a.n + col;
-    if (a.out_f32)
-        store_f32<N>(static_cast<float*>(a.out) + at, v);
-    else
-        store_bf16<N>(static_cast<uint16_t*>(a.out) + at, v);
-}
 template <int N>
 __device__ __forceinline__ Values<N> sum(const Values<N>& x, const Values<N>& y) {
     Values<N> r;
 #pragma unroll
     for (int i = 0; i < N; ++i) r.v[i] = x.v[i] + y.v[i];
     return r;
+}
+
+// The activation of `v` (gated: with `up`), for the whole array at once, so that
+// what it is is asked once.
+template <int kCount, int N, bool kGated>
+__device__ __forceinline__ void activate_all(Values<N> (&v)[kCount], const Values<N> (&up)[kCount],
+                                             int act) {
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < kCount; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[i].v[j] = f(v[i].v[j], up[i].v[j]);
+    };
+    if (kGated)
+        each([](float g, float u) { return silu(g) * u; });
+    else if (act == EP_ACT_RELU)
+        each([](float z, float) { return activate(z, EP_ACT_RELU); });
+    else if (act == EP_ACT_GELU)
+        each([](float z, float) { return activate(z, EP_ACT_GELU); });
+    else if (act == EP_ACT_SILU)
+        each([](float z, float) { return activate(z, EP_ACT_SILU); });
+}
+
+// The end of kCount times N values of out, `apart` rows apart from row `row` on,
+// of which `rows` (as many as are there) are stored: sums with their bias in `v`
+// (gated: the up half's in `up`), `residual` what is added.
+template <int kCount, int N, bool kGated>
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int64_t col, int apart,
+                                       int rows, Values<N> (&v)[kCount], const Values<N> (&up)[kCount],
+                                       const Residual<N> (&residual)[kCount]) {
+    if (a.z != nullptr) {
+        const int64_t pitch = kGated ? 2 * a.n : a.n;
+        uint16_t* z = a.z + row * pitch + col;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i, z += apart * pitch) {
+            if (i >= rows) continue;
+            store_bf16<N>(z, v[i]);
+            if (kGated) store_bf16<N>(z + a.n, up[i]);
+        }
+    }
+    activate_all<kCount, N, kGated>(v, up, a.act);
+    if (a.residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) v[i] = sum<N>(v[i], residual_values<N>(a, residual[i]));
+    }
+    const int64_t at = row * a.n + col, step = apart * a.n;
+    if (a.out_f32) {
+        float* p = static_cast<float*>(a.out) + at;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i, p += step)
+            if (i < rows) store_f32<N>(p, v[i]);
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i, p += step)
+            if (i < rows) store_bf16<N>(p, v[i]);
+    }
 }
 
 }  // namespace ep
