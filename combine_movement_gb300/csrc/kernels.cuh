@@ -304,6 +304,8 @@ struct RouteArgs {
     const float* d_topk_w;     // [T][K]
     void* d_logits;            // [T][E], the logits' type
     int32_t* status;
+    // set by launch_route
+    int group_lanes;           // lanes of a warp that hold a group's experts, 0: none
 };
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);

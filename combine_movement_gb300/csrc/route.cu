@@ -21,10 +21,10 @@
 // whose order the bound leaves open (a few of ten thousand) goes through the
 // choice again in 64 bits (route_exact).
 //
-// Mapping: a warp to a token; lane i holds the V = ceil(E / 32) experts from
-// i * V on, as fp32 values and as integers of the same order, so that the K
-// rounds of the choice are one warp-wide integer maximum and one ballot each and
-// ties fall to the lower index by themselves.
+// Mapping: a warp to a token; lane i holds the V = ceil(E / 32) experts (rounded up
+// to a power of two) from i * V on, as integers of their values' order, and sorts
+// its own. A round of the choice is one warp-wide integer maximum of the lanes'
+// first ones and one ballot, and ties fall to the lower index by themselves.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -53,6 +53,9 @@ __device__ __forceinline__ unsigned long long key_of(double v) {
     return b < 0 ? ~static_cast<unsigned long long>(b)
                  : static_cast<unsigned long long>(b) | 0x8000000000000000ull;
 }
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
+}
 __device__ __forceinline__ double value_of(unsigned long long key) {
     const unsigned long long b = (key >> 63) ? key & 0x7FFFFFFFFFFFFFFFull : ~key;
     return __longlong_as_double(static_cast<long long>(b));
@@ -66,10 +69,90 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t at) {
     return __ldg(static_cast<const float*>(a.logits) + at);
 }
 
-__device__ __forceinline__ float warp_max(float v) {  // NaN only of NaN alone
+// V values from lane * V on of a row that starts at `at`; what lies past its E
+// values is `past`. kFull: there is none, and the rows are 16-byte aligned.
+template <int V, bool kFull>
+__device__ __forceinline__ void load_part(const void* p, bool bf16, int64_t at, int E, float past,
+                                          float (&v)[V]) {
+    const int e0 = (threadIdx.x & 31) * V;
+    if constexpr (kFull && V >= 2) {
+        constexpr int kAtOnce = V < 8 ? V : 8;  // 16 bytes of bf16
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, d));
-    return v;
+        for (int i = 0; i < V; i += kAtOnce) {
+            uint32_t w[kAtOnce];
+            if (bf16) {
+                const uint16_t* q = static_cast<const uint16_t*>(p) + at + e0 + i;
+                if constexpr (kAtOnce == 8) {
+                    const uint4 f = __ldg(reinterpret_cast<const uint4*>(q));
+                    w[0] = f.x, w[1] = f.y, w[2] = f.z, w[3] = f.w;
+                } else if constexpr (kAtOnce == 4) {
+                    const uint2 f = __ldg(reinterpret_cast<const uint2*>(q));
+                    w[0] = f.x, w[1] = f.y;
+                } else {
+                    w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+                }
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    v[i + j] = __uint_as_float(j % 2 == 0 ? w[j / 2] << 16 : w[j / 2] & 0xFFFF0000u);
+            } else {
+                const float* q = static_cast<const float*>(p) + at + e0 + i;
+                if constexpr (kAtOnce == 2) {
+                    const float2 f = __ldg(reinterpret_cast<const float2*>(q));
+                    v[i] = f.x, v[i + 1] = f.y;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kAtOnce; j += 4) {
+                        const float4 f = __ldg(reinterpret_cast<const float4*>(q + j));
+                        v[i + j] = f.x, v[i + j + 1] = f.y, v[i + j + 2] = f.z, v[i + j + 3] = f.w;
+                    }
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[j] = past;
+            if (e0 + j >= E) continue;
+            if (bf16)
+                v[j] = __uint_as_float(
+                    static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + at + e0 + j)) << 16);
+            else
+                v[j] = __ldg(static_cast<const float*>(p) + at + e0 + j);
+        }
+    }
+}
+
+template <int V, bool kFull>
+__device__ __forceinline__ void store_part(void* p, bool bf16, int64_t at, int E, const float (&v)[V]) {
+    const int e0 = (threadIdx.x & 31) * V;
+    if constexpr (kFull && V >= 4) {
+        if (bf16) {
+            uint16_t* q = static_cast<uint16_t*>(p) + at + e0;
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<uint2*>(q + i) =
+                    make_uint2(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]));
+        } else {
+            float* q = static_cast<float*>(p) + at + e0;
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<float4*>(q + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (e0 + j >= E) continue;
+            if (bf16)
+                static_cast<__nv_bfloat16*>(p)[at + e0 + j] = __float2bfloat16_rn(v[j]);
+            else
+                static_cast<float*>(p)[at + e0 + j] = v[j];
+        }
+    }
+}
+
+// The largest number of the warp; -inf of none (NaN alone).
+__device__ __forceinline__ float warp_max(float v) {
+    return value_of(__reduce_max_sync(kFullMask, v == v ? key_of(v) : key_of(-kInf)));
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -90,6 +173,11 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
     return v;
 }
 
+__device__ __forceinline__ float approx_reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
 
 // The groups to keep, as a bit mask, from each lane's group (`key` of its worth,
@@ -111,7 +199,8 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, unsigned 
     const int lane = threadIdx.x & 31, E = a.E;
     const int64_t row = t * E;
     double m = 0.0, z = 1.0;
-    if (a.softmax) {
+    const bool scores = a.bias != nullptr || (a.groups > 1 && a.group_top2);
+    if (a.softmax && scores) {
         float top = -kInf;
         for (int e = lane; e < E; e += 32) top = fmaxf(top, load_logit(a, row + e));
         m = warp_max(top);
@@ -126,8 +215,9 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, unsigned 
         const float l = load_logit(a, row + e);
         const float b = a.bias != nullptr ? __ldg(a.bias + e) : 0.0f;
         const double ld = l;
-        const double s = a.softmax ? exp(ld - m) / z : 1.0 / (1.0 + exp(-ld));
-        keys[e] = l == -kInf || b == -kInf ? 0ull : key_of(s + b);
+        double c = ld;
+        if (scores) c = (a.softmax ? exp(ld - m) / z : 1.0 / (1.0 + exp(-ld))) + b;
+        keys[e] = l == -kInf || b == -kInf ? 0ull : key_of(c);
     }
     __syncwarp();
     if (a.groups > 1) {
@@ -152,7 +242,7 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, unsigned 
             if (!((kept >> (e / size)) & 1)) keys[e] = 0;
         // without a bias experts go by their logits, not by what scores are left
         // of them
-        if (a.bias == nullptr)
+        if (scores && a.bias == nullptr)
             for (int e = lane; e < E; e += 32)
                 if (keys[e] != 0) keys[e] = key_of(static_cast<double>(load_logit(a, row + e)));
         __syncwarp();
@@ -176,7 +266,42 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, unsigned 
     return mine;
 }
 
+// Descending, by odd-even merging.
 template <int V>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[V]) {
+#pragma unroll
+    for (int p = 1; p < V; p <<= 1)
+#pragma unroll
+        for (int k = p; k > 0; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t x = v[i + j], y = v[i + j + k];
+                        v[i + j] = max(x, y);
+                        v[i + j + k] = min(x, y);
+                    }
+}
+
+// Scores as the choice first takes them, with approximate functions, and a bound
+// on their error. With t = e^-l off by (2^-22 + |l| 2^-23) of itself, sigmoid
+// is off by s (1 - s) of that, s (1 - s) |l| < 0.23, and by the reciprocal's
+// 2^-23: less than 2^-21. A softmax score, r = 1 / sum: its own exponential by
+// 2^-22 + |l - m| 2^-23 of itself, at most 5 2^-24 of the largest score r; the sum
+// by its V + 5 additions, 2^-22, and the exponents' part, at most ln E + 1 < 10 times
+// 2^-23 of itself; the product and the reciprocal by 2 2^-23.
+struct Scores {
+    bool softmax;
+    float m, r;
+    float bound;
+    __device__ __forceinline__ float of(float l) const {
+        return softmax ? __expf(l - m) * r : approx_reciprocal(1.0f + __expf(-l));
+    }
+};
+
+// kFull: E = 32 V in 16-byte aligned rows.
+template <int V, bool kFull>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     extern __shared__ unsigned long long smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -188,136 +313,167 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     const int64_t row = t * a.E;
     const int e0 = lane * V;
 
-    float l[V];
-    float top = -kInf;
-    bool odd = false;  // whether the choice has to be made again in 64 bits
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        l[j] = e0 + j < a.E ? load_logit(a, row + e0 + j) : -kInf;
-        top = fmaxf(top, l[j]);
-    }
+    float l[V], b[V];
+    load_part<V, kFull>(a.logits, a.bf16_logits, row, a.E, -kInf, l);
+    if (a.bias != nullptr) load_part<V, kFull>(a.bias, false, 0, a.E, 0.0f, b);
     const bool scores = a.bias != nullptr || (a.groups > 1 && a.group_top2);
     float m = 0.0f, z = 1.0f;
-    if (a.softmax) {
+    if (a.softmax && (scores || !a.renormalize)) {
+        float top = -kInf;
+#pragma unroll
+        for (int j = 0; j < V; ++j) top = fmaxf(top, l[j]);
         m = warp_max(top);
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < V; ++j) sum += l[j] == -kInf ? 0.0f : expf(l[j] - m);
         z = warp_sum(sum);
     }
+    Scores score{a.softmax, m, approx_reciprocal(z), 0.0f};
+    score.bound = a.softmax ? score.r * static_cast<float>(V + 40) * 0x1p-24f : 0x1p-21f;
+    bool odd = false;  // whether the choice has to be made again in 64 bits
     uint32_t key[V];
-    float c[V];
-    // bound on a score's error: sigmoid's exponential, sum and division are off by
-    // less than 4 units of 2^-23 together; a softmax score besides by the sum's
-    // V + 5 additions and by l - m's rounding, |l - m| 2^-24 times the score,
-    // at most 0.37 2^-24 of the largest
-    const float bound =
-        a.softmax ? __fdiv_rn(static_cast<float>(V + 20), z) * 0x1p-23f : 0x1p-20f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        float b = 0.0f;
-        if (a.bias != nullptr && e0 + j < a.E) b = __ldg(a.bias + e0 + j);
-        c[j] = l[j];
+        float c = l[j];
+        bool out = l[j] == -kInf;
         if (scores) {
-            const float s = a.softmax ? __fdiv_rn(expf(l[j] - m), z) : sigmoid(l[j]);
-            c[j] = s + b;
+            c = score.of(l[j]);
+            if (a.bias != nullptr) {
+                c += b[j];
+                out |= b[j] == -kInf;
+            }
+            odd |= !out && c != c;
         }
-        const bool out = l[j] == -kInf || b == -kInf;
-        key[j] = out ? 0u : key_of(c[j]);
-        odd |= scores && !out && c[j] != c[j];
+        key[j] = out ? 0u : key_of(c);
     }
-    const int size = a.E / a.groups;
     if (a.groups > 1) {
-        // each lane's group from shared memory
-        uint32_t* keys = reinterpret_cast<uint32_t*>(keys64);
+        uint32_t first = 0, second = 0;
+        const int lanes = kFull ? a.group_lanes : 0;
+        const int size = a.E / a.groups;
+        auto add = [&](uint32_t k) {
+            second = max(second, min(first, k));
+            first = max(first, k);
+        };
+        if (lanes > 0) {  // a group's experts are those of `lanes` neighbouring lanes
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j < a.E) keys[e0 + j] = key[j];
-        __syncwarp();
-        uint32_t worth = 0;
-        float value = 0.0f, error = 0.0f;
-        if (lane < a.groups) {
-            uint32_t first = 0, second = 0;
-            for (int e = lane * size; e < (lane + 1) * size; ++e) {
-                const uint32_t k = keys[e];
-                second = max(second, min(first, k));
-                first = max(first, k);
+            for (int j = 0; j < V; ++j) add(key[j]);
+            for (int d = 1; d < lanes; d <<= 1) {
+                const uint32_t f = __shfl_xor_sync(kFullMask, first, d);
+                const uint32_t s = __shfl_xor_sync(kFullMask, second, d);
+                second = max(min(first, f), max(second, s));
+                first = max(first, f);
             }
-            auto of = [](uint32_t k) {
-                return __uint_as_float((k >> 31) ? k & 0x7FFFFFFFu : ~k);
-            };
-            worth = first;
-            if (first != 0) {
-                value = of(first);
-                error = bound + fabsf(value) * 0x1p-23f;
-                if (a.group_top2 && second != 0) {
-                    error += bound + fabsf(of(second)) * 0x1p-23f;
-                    value += of(second);
-                    error += fabsf(value) * 0x1p-23f;
-                    worth = key_of(value);
-                }
-            }
+            // to the lane of the group's number
+            first = __shfl_sync(kFullMask, first, lane * lanes);
+            second = __shfl_sync(kFullMask, second, lane * lanes);
+        } else {
+            uint32_t* keys = reinterpret_cast<uint32_t*>(keys64);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (e0 + j < a.E) keys[e0 + j] = key[j];
+            __syncwarp();
+            if (lane < a.groups)
+                for (int e = lane * size; e < (lane + 1) * size; ++e) add(keys[e]);
+            __syncwarp();
+        }
+        uint32_t worth = lane < a.groups ? first : 0;
+        float value = value_of(first), error = score.bound + fabsf(value) * 0x1p-23f;
+        if (a.group_top2 && second != 0) {
+            const float v2 = value_of(second);
+            error += score.bound + fabsf(v2) * 0x1p-23f;
+            value += v2;
+            error += fabsf(value) * 0x1p-23f;
+            if (worth != 0) worth = key_of(value);
         }
         const uint32_t kept = best_groups(worth, a);
         if (scores) {
-            const bool has = lane < a.groups && worth != 0, mine = (kept >> lane) & 1;
-            const float low = -warp_max(has && mine ? error - value : -kInf);
-            const float high = warp_max(has && !mine ? value + error : -kInf);
-            odd |= high > -kInf && !(low > high);
+            const bool mine = (kept >> lane) & 1;
+            const uint32_t low =
+                __reduce_min_sync(kFullMask, worth != 0 && mine ? key_of(value - error) : 0xFFFFFFFFu);
+            const uint32_t high =
+                __reduce_max_sync(kFullMask, worth != 0 && !mine ? key_of(value + error) : 0u);
+            odd |= high >= low;
         }
+        if (lanes > 0) {
+            const bool stays = (kept >> (lane / max(lanes, 1))) & 1;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (e0 + j >= a.E || !((kept >> ((e0 + j) / size)) & 1)) key[j] = 0;
+            for (int j = 0; j < V; ++j)
+                if (!stays) key[j] = 0;
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (e0 + j >= a.E || !((kept >> ((e0 + j) / size)) & 1)) key[j] = 0;
+        }
         if (scores && a.bias == nullptr) {
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 if (key[j] != 0) key[j] = key_of(l[j]);
         }
-        __syncwarp();
     }
-    // K rounds, and one more where the next value decides whether the last of
-    // them is settled
-    const bool check = a.bias != nullptr;
-    int mine = -1;
-    float c_before = 0.0f, l_before = 0.0f, b_before = 0.0f;
-    for (int k = 0; k < a.K + (check ? 1 : 0); ++k) {
-        uint32_t best = 0;
+    // The lane's experts in order: the integers without their last bits, which say
+    // which expert it is (the lower the index, the larger). What is lost with them
+    // shows below, where the chosen ones' values are compared.
+    constexpr uint32_t kLast = V - 1;
+    static_assert((V & (V - 1)) == 0, "a power of two");
+    constexpr bool kSort = V <= 16;
 #pragma unroll
-        for (int j = 0; j < V; ++j) best = max(best, key[j]);
-        const uint32_t most = __reduce_max_sync(kFullMask, best);
+    for (int j = 0; j < V; ++j)
+        if (key[j] != 0) key[j] = (key[j] & ~kLast) | (kLast - j);
+    if constexpr (kSort) sort_descending<V>(key);
+    // K rounds, and one more for what the last of them has to be larger than
+    int mine = -1, next = -1;
+    for (int k = 0; k <= a.K; ++k) {
+        uint32_t head = key[0];
+        if constexpr (!kSort) {
+#pragma unroll
+            for (int j = 1; j < V; ++j) head = max(head, key[j]);
+        }
+        const uint32_t most = __reduce_max_sync(kFullMask, head & ~kLast);
         if (most == 0) break;
-        const int owner = __ffs(__ballot_sync(kFullMask, best == most)) - 1;
-        int at = 0;
-        float lv = 0.0f, cv = 0.0f;
+        const int owner = __ffs(__ballot_sync(kFullMask, (head & ~kLast) == most)) - 1;
+        const int e = owner * V + static_cast<int>(kLast - (__shfl_sync(kFullMask, head, owner) & kLast));
+        if (lane == k) mine = e;
+        if (k == a.K) next = e;
         if (lane == owner) {
+            if constexpr (kSort) {
 #pragma unroll
-            for (int j = V - 1; j >= 0; --j)
-                if (key[j] == most) {
-                    at = j;
-                    lv = l[j];
-                    cv = c[j];
-                }
+                for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1];
+                key[V - 1] = 0;
+            } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (j == at) key[j] = 0;
-        }
-        const int e = __shfl_sync(kFullMask, e0 + at, owner);
-        if (k < a.K && lane == k) mine = e;
-        if (check) {
-            lv = __shfl_sync(kFullMask, lv, owner);
-            cv = __shfl_sync(kFullMask, cv, owner);
-            const float b = __ldg(a.bias + e);
-            if (k > 0 && !(lv == l_before && b == b_before))
-                odd |= !(c_before - cv > 2.0f * bound + (fabsf(c_before) + fabsf(cv)) * 0x1p-22f);
-            c_before = cv;
-            l_before = lv;
-            b_before = b;
+                for (int j = 0; j < V; ++j)
+                    if (key[j] == head) key[j] = 0;
+            }
         }
     }
-    if (__any_sync(kFullMask, odd)) mine = route_exact(a, t, keys64);
+    if (lane >= a.K) mine = -1;
+    // Is each of them larger than the one after it, by more than both may be off?
+    float lk = mine >= 0 ? load_logit(a, row + mine) : -kInf;
+    {
+        int e2 = __shfl_down_sync(kFullMask, mine, 1);
+        float l2 = __shfl_down_sync(kFullMask, lk, 1);
+        if (lane == a.K - 1) {
+            e2 = next;
+            l2 = next >= 0 ? load_logit(a, row + next) : -kInf;
+        }
+        if (mine >= 0 && e2 >= 0) {
+            if (a.bias != nullptr) {
+                const float b1 = __ldg(a.bias + mine), b2 = __ldg(a.bias + e2);
+                const float c1 = score.of(lk) + b1, c2 = score.of(l2) + b2;
+                const float off = 2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * 0x1p-22f;
+                odd |= !(lk == l2 && b1 == b2) && !(c1 - c2 > off);
+            } else {
+                const uint32_t k1 = key_of(lk), k2 = key_of(l2);
+                odd |= k1 < k2 || (k1 == k2 && mine > e2);
+            }
+        }
+    }
+    if (__any_sync(kFullMask, odd)) {
+        mine = route_exact(a, t, keys64);
+        lk = mine >= 0 ? load_logit(a, row + mine) : -kInf;
+    }
 
     // weights: lane k's
-    const float lk = mine >= 0 ? load_logit(a, row + mine) : -kInf;
     float w = 0.0f;
     if (a.renormalize) {
         const float high = warp_max(lk);
@@ -346,11 +502,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
 //   softmax, renormalised d_k = p_k (g_k - sum_j g_j p_j)
 //   sigmoid               d_k = g_k s_k (1 - s_k)
 //   sigmoid, renormalised d_k = p_k (1 - s_k) (g_k - sum_j g_j p_j)
-// and zero where nothing is said. A warp to a token: lane k an entry, then the row
-// through shared memory. An expert that a token has twice gets the sum of both, in
-// their order.
+// and zero where nothing is said. A warp to a token: lane k an entry, then the row,
+// of which a lane holds V neighbouring experts as in the choice (V = 0: in shared
+// memory, for more than 8). An expert that a token has twice gets the sum of
+// both, in their order.
+template <int V, bool kFull>
 __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const RouteArgs a) {
     extern __shared__ unsigned long long smem[];
+    constexpr bool kHeld = V > 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float* const d_row = reinterpret_cast<float*>(smem) + static_cast<int64_t>(warp) * a.E;
     griddep_wait();
@@ -358,29 +517,44 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const RouteArgs
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= a.T) return;
     const int64_t row = t * a.E;
+    const bool dense = a.softmax && !a.renormalize;
 
     int64_t idx = lane < a.K ? __ldg(a.topk_idx + t * a.K + lane) : -1;
+    const float dw = lane < a.K ? __ldg(a.d_topk_w + t * a.K + lane) : 0.0f;
+    float l[kHeld ? V : 1];
+    if constexpr (kHeld) {
+        if (dense) load_part<V, kFull>(a.logits, a.bf16_logits, row, a.E, -kInf, l);
+    }
     if (idx < -1 || idx >= a.E) {
         set_status(a.status, EP_ERR_BAD_EXPERT);
         idx = -1;
     }
-    const bool on = idx >= 0;
-    const float lk = on ? load_logit(a, row + idx) : -kInf;
-    const float g = on ? __ldg(a.d_topk_w + t * a.K + lane) * a.scale : 0.0f;
-    const bool dense = a.softmax && !a.renormalize;
+    const int mine = static_cast<int>(idx);
+    const float lk = mine >= 0 ? load_logit(a, row + mine) : -kInf;
+    const float g = dw * a.scale;
+    const bool live = lk != -kInf;  // (an expert taken out has score 0)
     float m = 0.0f, z = 1.0f;
     if (dense) {
-        float top = -kInf;
-        for (int e = lane; e < a.E; e += 32) top = fmaxf(top, load_logit(a, row + e));
-        m = warp_max(top);
-        float sum = 0.0f;
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = load_logit(a, row + e);
-            sum += l == -kInf ? 0.0f : expf(l - m);
+        float top = -kInf, sum = 0.0f;
+        if constexpr (kHeld) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) top = fmaxf(top, l[j]);
+            m = warp_max(top);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                l[j] = l[j] == -kInf ? 0.0f : expf(l[j] - m);
+                sum += l[j];
+            }
+        } else {
+            for (int e = lane; e < a.E; e += 32) top = fmaxf(top, load_logit(a, row + e));
+            m = warp_max(top);
+            for (int e = lane; e < a.E; e += 32) {
+                const float v = load_logit(a, row + e);
+                sum += v == -kInf ? 0.0f : expf(v - m);
+            }
         }
         z = warp_sum(sum);
     }
-    const bool live = on && lk != -kInf;  // (an expert taken out has score 0)
     float d = 0.0f, dot = 0.0f;
     if (a.renormalize) {
         const float high = warp_max(lk);
@@ -404,36 +578,54 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const RouteArgs
     } else if (live) {
         d = g * sigmoid(lk) * sigmoid(-lk);
     }
-    for (int e = lane; e < a.E; e += 32) d_row[e] = 0.0f;
-    float sum = 0.0f;
-    bool first = on;
-    for (int k = 0; k < a.K; ++k) {
-        const int e = __shfl_sync(kFullMask, static_cast<int>(idx), k);
-        const float dk = __shfl_sync(kFullMask, d, k);
-        if (on && e == static_cast<int>(idx)) {
-            sum += dk;
-            if (k < lane) first = false;
+    if constexpr (kHeld) {
+        float out[V] = {};
+        const int e0 = lane * V;
+        for (int k = 0; k < a.K; ++k) {
+            const int e = __shfl_sync(kFullMask, mine, k) - e0;
+            const float dk = __shfl_sync(kFullMask, d, k);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (e == j) out[j] += dk;
         }
-    }
-    __syncwarp();
-    if (first) d_row[idx] = sum;
-    __syncwarp();
-    for (int e = lane; e < a.E; e += 32) {
-        float v = d_row[e];
         if (dense) {
-            const float l = load_logit(a, row + e);
-            v = l == -kInf ? 0.0f : __fdiv_rn(expf(l - m), z) * (v - dot);
+            const float r = __fdiv_rn(1.0f, z);
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[j] = l[j] == 0.0f ? 0.0f : l[j] * r * (out[j] - dot);
         }
-        if (a.bf16_logits)
-            static_cast<__nv_bfloat16*>(a.d_logits)[row + e] = __float2bfloat16_rn(v);
-        else
-            static_cast<float*>(a.d_logits)[row + e] = v;
+        store_part<V, kFull>(a.d_logits, a.bf16_logits, row, a.E, out);
+    } else {
+        for (int e = lane; e < a.E; e += 32) d_row[e] = 0.0f;
+        float sum = 0.0f;
+        bool first = mine >= 0;
+        for (int k = 0; k < a.K; ++k) {
+            const int e = __shfl_sync(kFullMask, mine, k);
+            const float dk = __shfl_sync(kFullMask, d, k);
+            if (mine >= 0 && e == mine) {
+                sum += dk;
+                if (k < lane) first = false;
+            }
+        }
+        __syncwarp();
+        if (first) d_row[mine] = sum;
+        __syncwarp();
+        for (int e = lane; e < a.E; e += 32) {
+            float v = d_row[e];
+            if (dense) {
+                const float le = load_logit(a, row + e);
+                v = le == -kInf ? 0.0f : __fdiv_rn(expf(le - m), z) * (v - dot);
+            }
+            if (a.bf16_logits)
+                static_cast<__nv_bfloat16*>(a.d_logits)[row + e] = __float2bfloat16_rn(v);
+            else
+                static_cast<float*>(a.d_logits)[row + e] = v;
+        }
     }
 }
 
-template <int V>
-cudaError_t launch_route_v(const RouteArgs& a, size_t smem, cudaStream_t stream) {
-    auto kern = route_kernel<V>;
+// kernel(a) with a token to a warp.
+cudaError_t launch_tokens(void (*kern)(RouteArgs), const RouteArgs& a, size_t smem,
+                          cudaStream_t stream) {
     if (smem > 48 * 1024) {
         const cudaError_t err = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -441,6 +633,24 @@ cudaError_t launch_route_v(const RouteArgs& a, size_t smem, cudaStream_t stream)
     }
     return launch_dependent(kern, static_cast<int>((a.T + kWarps - 1) / kWarps), kWarps * 32, smem,
                             stream, a);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <int V>
+cudaError_t launch_route_v(RouteArgs a, size_t smem, cudaStream_t stream) {
+    if (a.E != 32 * V || !aligned16(a.logits) || !aligned16(a.bias))
+        return launch_tokens(route_kernel<V, false>, a, smem, stream);
+    const int lanes = 32 / a.groups;
+    a.group_lanes = a.groups > 1 && lanes * a.groups == 32 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    return launch_tokens(route_kernel<V, true>, a, smem, stream);
+}
+
+template <int V>
+cudaError_t launch_route_grad_v(const RouteArgs& a, cudaStream_t stream) {
+    if (a.E != 32 * V || !aligned16(a.logits) || !aligned16(a.d_logits))
+        return launch_tokens(route_grad_kernel<V, false>, a, 0, stream);
+    return launch_tokens(route_grad_kernel<V, true>, a, 0, stream);
 }
 
 }  // namespace
@@ -458,14 +668,13 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_route_grad(const RouteArgs& a, cudaStream_t stream) {
-    const size_t smem = sizeof(float) * kWarps * static_cast<size_t>(a.E);
-    if (smem > 48 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(
-            route_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (err != cudaSuccess) return err;
-    }
-    return launch_dependent(route_grad_kernel, static_cast<int>((a.T + kWarps - 1) / kWarps),
-                            kWarps * 32, smem, stream, a);
+    const int v = (a.E + 31) / 32;
+    if (v <= 1) return launch_route_grad_v<1>(a, stream);
+    if (v <= 2) return launch_route_grad_v<2>(a, stream);
+    if (v <= 4) return launch_route_grad_v<4>(a, stream);
+    if (v <= 8) return launch_route_grad_v<8>(a, stream);
+    return launch_tokens(route_grad_kernel<0, false>, a,
+                         sizeof(float) * kWarps * static_cast<size_t>(a.E), stream);
 }
 
 }  // namespace ep
