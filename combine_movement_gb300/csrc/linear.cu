@@ -28,9 +28,9 @@ namespace ep {
 namespace {
 
 // Who works on a tile: a CTA alone or the CTAs of a cluster that share its blocks
-// along k, on 128 x 64 (gated: 32 columns of each half), or a pair of CTAs on
-// 256 x 256 (gated: 128 of each half), 128 rows and half of b each.
-enum Mode { kAlone, kShared, kPair };
+// along k, on 128 x 64 (gated: 32 columns of each half; kSharedWide 128 x 256), or a
+// pair of CTAs on 256 x 256 (gated: 128 of each half), 128 rows and half of b each.
+enum Mode { kAlone, kShared, kSharedWide, kPair };
 
 constexpr int kRows = 128;                   // of the output, in one CTA
 constexpr int kTileK = 64;                   // values of one stage along k
@@ -51,7 +51,8 @@ constexpr int kExactBlocks = 16;
 
 template <Mode kMode>
 struct Shape {
-    static constexpr int kCols = kMode == kPair ? 256 : 64;       // of the tile
+    static constexpr bool kParts = kMode == kShared || kMode == kSharedWide;
+    static constexpr int kCols = kMode == kPair || kMode == kSharedWide ? 256 : 64;  // of the tile
     static constexpr int kTileRows = kMode == kPair ? 2 * kRows : kRows;
     static constexpr int kOwnB = kMode == kPair ? kCols / 2 : kCols;  // rows of b in one CTA
     static constexpr uint32_t kStageBytes = kStageA + kOwnB * kRowBytes;
@@ -59,7 +60,7 @@ struct Shape {
     // begun when they end)
     static constexpr int kStages = kMode == kShared ? 4 : 192 * 1024 / kStageBytes;
     static constexpr uint32_t kRingBytes = kStages * kStageBytes;
-    static constexpr size_t kSmem = 1024 + kRingBytes + (kMode == kShared ? 0 : kOutWarps * kTurnBytes);
+    static constexpr size_t kSmem = 1024 + kRingBytes + (kParts ? 0 : kOutWarps * kTurnBytes);
     static constexpr int kMine = kCols / 2;  // columns of sums that a warp takes
     // a shared tile's sums, [row][column] in fp32, in the stages' place
     static constexpr uint32_t kPitch = kCols * 4 + 16;
@@ -204,10 +205,10 @@ __device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, 
 // its own out in shared memory; CTA `rank` adds, in the parts' order, and writes
 // those of the rows r = rank mod kParts. A thread takes N neighbouring columns of
 // kAtOnce rows at a time, so that its loads overlap.
-template <int N, bool kGated, int kParts>
+template <Mode kMode, int N, bool kGated, int kParts>
 __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
                                                   int rank) {
-    using S = Shape<kShared>;
+    using S = Shape<kMode>;
     constexpr int kCols = kGated ? S::kCols / 2 : S::kCols, kPieces = kCols / N;
     constexpr int kStep = kOutWarps * 32 / kPieces;  // of this CTA's rows, by all threads
     constexpr int kMost = kRows / kParts / kStep;    // of them to a thread
@@ -261,15 +262,15 @@ __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t 
         finish<kAtOnce, N, kGated>(a, row, col, kStep * kParts, (own - i0 + kStep - 1) / kStep, vs, us, res);
     }
 }
-template <int N, bool kGated>
+template <Mode kMode, int N, bool kGated>
 __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
                                                   int rank) {
     if (a.split == 2)
-        write_shared_tile<N, kGated, 2>(a, sums, tile, rank);
+        write_shared_tile<kMode, N, kGated, 2>(a, sums, tile, rank);
     else if (a.split == 4)
-        write_shared_tile<N, kGated, 4>(a, sums, tile, rank);
-    else
-        write_shared_tile<N, kGated, 8>(a, sums, tile, rank);
+        write_shared_tile<kMode, N, kGated, 4>(a, sums, tile, rank);
+    else if (a.split == 8)
+        write_shared_tile<kMode, N, kGated, 8>(a, sums, tile, rank);
 }
 
 // 32 x 32 sums of a warp into its turning place.
@@ -287,7 +288,7 @@ __device__ __forceinline__ void turn_chunk(uint32_t turn, const float* v0, const
 }
 
 // kExact: sums leave tensor memory every kExactBlocks blocks along k and are added
-// in registers (not kShared, whose parts are added as they are joined).
+// in registers (not of shared tiles, whose parts are added as they are joined).
 template <Mode kMode, bool kGated, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const LinearArgs a, const __grid_constant__ Maps maps) {
@@ -337,12 +338,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     const uint32_t tmem = ctl.tmem;
     const int64_t tiles = a.row_tiles * a.col_tiles;
-    const int size = kMode == kPair ? 2 : kMode == kShared ? a.split : 1;
+    const int size = kMode == kPair ? 2 : S::kParts ? a.split : 1;
     const int64_t t0 = blockIdx.x / size;
-    const int64_t step = kMode == kShared ? tiles : gridDim.x / size;
+    const int64_t step = S::kParts ? tiles : gridDim.x / size;
     const int kb_first =
-        kMode == kShared ? static_cast<int>(static_cast<int64_t>(a.k_blocks) * rank / size) : 0;
-    const int kb_end = kMode == kShared
+        S::kParts ? static_cast<int>(static_cast<int64_t>(a.k_blocks) * rank / size) : 0;
+    const int kb_end = S::kParts
                            ? static_cast<int>(static_cast<int64_t>(a.k_blocks) * (rank + 1) / size)
                            : a.k_blocks;
     const int per_sum = kExact ? kExactBlocks : kb_end - kb_first;  // blocks
@@ -508,6 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < S::kMine / kChunk; ++c) {
                     if (col0 + c * kCols >= a.n) break;
                     turn_chunk(turn, acc[c][0], acc[c][1]);
+                    if (a.residual == nullptr) {
+                        write_chunk<kGated>(a, turn, part, col0 + c * kCols, 0, Ahead<4>{});
+                        continue;
+                    }
                     // (registers for no more than a quarter's)
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
@@ -519,12 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             Ahead<4> ahead = {};
-            if (kMode != kShared) read_ahead<kGated>(a, part, col0, 0, ahead);
+            if (!S::kParts) read_ahead<kGated>(a, part, col0, 0, ahead);
             ok = warp_wait<kMode == kPair>(sums + 8 * slot.i, slot.round, abort, a.status);
             if (!ok) break;
             tcgen05_fence_after();
             const uint32_t slot_at = from + slot.i * S::kCols;
-            if constexpr (kMode == kShared) {
+            if constexpr (S::kParts) {
                 const uint32_t own = base + (quarter * 32 + lane) * S::kPitch + half * S::kMine * 4;
 #pragma unroll
                 for (int c = 0; c < S::kMine; c += 16) {
@@ -560,16 +565,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    if (kMode == kShared) {
+    if (S::kParts) {
         // Every thread passes both barriers, whatever its CTA found to do.
         cluster_arrive();
         cluster_wait();
         if (warp < kOutWarps && t0 < tiles && load_shared(abort) == 0) {
             const Tile tile = tile_at<kMode>(t0, a);
             if (a.n % 4 == 0)
-                write_shared_tile<4, kGated>(a, base, tile, rank);
+                write_shared_tile<kMode, 4, kGated>(a, base, tile, rank);
             else
-                write_shared_tile<1, kGated>(a, base, tile, rank);
+                write_shared_tile<kMode, 1, kGated>(a, base, tile, rank);
         }
     }
     __syncwarp();
@@ -638,6 +643,7 @@ cudaError_t launch(const LinearArgs& a, const Maps& maps, int grid, int cluster,
 struct ResidentClusters {
     int pairs;
     int n[kMaxSplit + 1];
+    int wide[kMaxSplit + 1];
 };
 
 template <Mode kMode>
@@ -667,14 +673,18 @@ cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
         cudaError_t err = count_clusters<kPair>(2, &found->pairs);
         for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2)
             err = count_clusters<kShared>(split, &found->n[split]);
+        for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2)
+            err = count_clusters<kSharedWide>(split, &found->wide[split]);
         return err;
     });
 }
 
 int64_t up(int64_t v, int64_t by) { return (v + by - 1) / by; }
 
-// Who works on a tile, and how many CTAs share one. A partition's SMs may not
-// hold a cluster.
+// Who works on a tile, and how many CTAs share one: what takes least by the
+// times measured for a block along k (an SM takes in about 120 GB/s from L2: 24 KB of
+// a narrow tile, 48 KB of a wide one; a pair's products fill its time) and
+// for the joining of shared tiles' parts. A partition's SMs may not hold a cluster.
 struct Plan {
     Mode mode;
     int split;
@@ -689,16 +699,19 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, int device, int num_sms, b
     if (err != cudaSuccess) return err;
     const int half = gated ? 2 : 1;
     const int64_t pairs = up(a.m, Shape<kPair>::kTileRows) * up(a.n, Shape<kPair>::kCols / half);
-    const int64_t tiles = up(a.m, kRows) * up(a.n, Shape<kAlone>::kCols / half);
-    // a block along k takes a pair 512 cycles on its tile and a CTA about 300 on its own
-    const int64_t pair_time = up(pairs, clusters.pairs > 0 ? clusters.pairs : 1) * 512, alone_time = up(tiles, num_sms) * 300;
-    if (clusters.pairs > 0 && pair_time < alone_time) {
-        *plan = {kPair, 1, clusters.pairs};
-        return cudaSuccess;
+    const int64_t narrow = up(a.m, kRows) * up(a.n, Shape<kAlone>::kCols / half);
+    const int64_t wide = up(a.m, kRows) * up(a.n, Shape<kSharedWide>::kCols / half);
+    constexpr float kNarrow = 0.19f, kWide = 0.38f, kPairs = 0.27f;  // us a block
+    float best = up(narrow, num_sms) * (a.k_blocks * kNarrow + 0.5f);
+    auto take = [&](float time, Plan p) {
+        if (time < best) best = time, *plan = p;
+    };
+    if (clusters.pairs > 0)
+        take(up(pairs, clusters.pairs) * a.k_blocks * kPairs + 3.0f, {kPair, 1, clusters.pairs});
+    for (int n = 2; n <= kMaxSplit && n <= a.k_blocks; n *= 2) {
+        if (narrow <= clusters.n[n]) take(up(a.k_blocks, n) * kNarrow + 2.5f, {kShared, n, 0});
+        if (wide <= clusters.wide[n]) take(up(a.k_blocks, n) * kWide + 5.0f, {kSharedWide, n, 0});
     }
-    int n = 1;
-    while (n < kMaxSplit && tiles <= clusters.n[2 * n] && a.k_blocks >= 4 * n) n *= 2;
-    if (n > 1) *plan = {kShared, n, 0};
     return cudaSuccess;
 }
 
@@ -715,7 +728,7 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
     if (err == cudaSuccess) err = plan_for(a, gated, device, num_sms, partition, &plan);
     if (err != cudaSuccess) return err;
     const bool pair = plan.mode == kPair;
-    const int cols = pair ? Shape<kPair>::kCols : Shape<kAlone>::kCols;
+    const int cols = pair || plan.mode == kSharedWide ? Shape<kPair>::kCols : Shape<kAlone>::kCols;
     a.split = plan.split;
     a.row_tiles = up(a.m, pair ? Shape<kPair>::kTileRows : kRows);
     a.col_tiles = up(a.n, cols / half);
@@ -738,6 +751,11 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
                          : launch<kPair, false, true>(a, maps, grid, 2, stream);
         return gated ? launch<kPair, true, false>(a, maps, grid, 2, stream)
                      : launch<kPair, false, false>(a, maps, grid, 2, stream);
+    }
+    if (plan.mode == kSharedWide) {
+        const int grid = static_cast<int>(tiles) * a.split;
+        return gated ? launch<kSharedWide, true, false>(a, maps, grid, a.split, stream)
+                     : launch<kSharedWide, false, false>(a, maps, grid, a.split, stream);
     }
     if (plan.mode == kShared) {
         const int grid = static_cast<int>(tiles) * a.split;

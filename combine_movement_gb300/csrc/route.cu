@@ -43,9 +43,9 @@ constexpr int kWarps = 4;
 // Integers ordered like the values: 0 for "out" (no value has it), NaN the
 // largest, both zeros alike.
 __device__ __forceinline__ uint32_t key_of(float v) {
-    if (v != v) return 0xFFFFFFFFu;
-    const uint32_t b = __float_as_uint(v + 0.0f);  // (-0 + 0 = +0)
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    // -0 + 0 = +0, and a sum's NaN is 0x7FFFFFFF
+    const int32_t b = __float_as_int(__fadd_rn(v, 0.0f));
+    return static_cast<uint32_t>(b ^ (b >> 31 | static_cast<int32_t>(0x80000000u)));
 }
 __device__ __forceinline__ unsigned long long key_of(double v) {
     if (v != v) return ~0ull;
@@ -178,6 +178,11 @@ __device__ __forceinline__ float approx_reciprocal(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float approx_exp(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.44269504088896341f));
+    return r;
+}
 __device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
 
 // The groups to keep, as a bit mask, from each lane's group (`key` of its worth,
@@ -193,59 +198,82 @@ __device__ __forceinline__ uint32_t best_groups(Key key, const RouteArgs& a) {
     return __ballot_sync(kFullMask, lane < a.groups && rank < a.topk_groups && key != 0);
 }
 
-// The choice in 64 bits, by the whole warp; `keys` is the warp's [E]. Returns
-// the entry of each lane k < K, or -1.
-__device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, unsigned long long* keys) {
-    const int lane = threadIdx.x & 31, E = a.E;
-    const int64_t row = t * E;
-    double m = 0.0, z = 1.0;
-    const bool scores = a.bias != nullptr || (a.groups > 1 && a.group_top2);
-    if (a.softmax && scores) {
-        float top = -kInf;
-        for (int e = lane; e < E; e += 32) top = fmaxf(top, load_logit(a, row + e));
-        m = warp_max(top);
-        z = 0.0;
-        for (int e = lane; e < E; e += 32) {
-            const double l = load_logit(a, row + e);
-            z += l == -kInf ? 0.0 : exp(l - m);
-        }
-        z = warp_sum(z);
+// c in 64 bits: of every expert into the warp's `keys` [E] (0: out). Not inlined:
+// a few tokens of ten thousand come here.
+struct Exact {
+    double m, z;
+};
+__device__ __noinline__ Exact exact_softmax(const RouteArgs& a, int64_t row) {
+    const int lane = threadIdx.x & 31;
+    float top = -kInf;
+    for (int e = lane; e < a.E; e += 32) top = fmaxf(top, load_logit(a, row + e));
+    const double m = warp_max(top);
+    double z = 0.0;
+    for (int e = lane; e < a.E; e += 32) {
+        const double l = load_logit(a, row + e);
+        z += l == -kInf ? 0.0 : exp(l - m);
     }
-    for (int e = lane; e < E; e += 32) {
+    return {m, warp_sum(z)};
+}
+__device__ __noinline__ double exact_score(const RouteArgs& a, const Exact& x, float l) {
+    const double ld = l;
+    return a.softmax ? exp(ld - x.m) / x.z : 1.0 / (1.0 + exp(-ld));
+}
+__device__ __noinline__ void exact_keys(const RouteArgs& a, int64_t row, unsigned long long* keys) {
+    const int lane = threadIdx.x & 31;
+    const bool scores = a.bias != nullptr || (a.groups > 1 && a.group_top2);
+    Exact x{};
+    if (a.softmax && scores) x = exact_softmax(a, row);
+    for (int e = lane; e < a.E; e += 32) {
         const float l = load_logit(a, row + e);
         const float b = a.bias != nullptr ? __ldg(a.bias + e) : 0.0f;
-        const double ld = l;
-        double c = ld;
-        if (scores) c = (a.softmax ? exp(ld - m) / z : 1.0 / (1.0 + exp(-ld))) + b;
+        double c = l;
+        if (scores) c = exact_score(a, x, l) + b;
         keys[e] = l == -kInf || b == -kInf ? 0ull : key_of(c);
     }
     __syncwarp();
+}
+
+// The groups that stay, by values in 64 bits; leaves exact_keys.
+__device__ __noinline__ uint32_t exact_groups(const RouteArgs& a, int64_t row, unsigned long long* keys) {
+    const int lane = threadIdx.x & 31, size = a.E / a.groups;
+    exact_keys(a, row, keys);
+    unsigned long long worth = 0;
+    if (lane < a.groups) {
+        unsigned long long first = 0, second = 0;
+        for (int i = 0; i < size; ++i) {
+            // (the lanes start at different places, so that they meet in few banks)
+            const unsigned long long k = keys[lane * size + (i + lane) % size];
+            if (k > first) {
+                second = first;
+                first = k;
+            } else if (k > second) {
+                second = k;
+            }
+        }
+        worth = first;
+        if (a.group_top2 && second != 0) worth = key_of(value_of(first) + value_of(second));
+    }
+    return best_groups(worth, a);
+}
+
+// The choice in 64 bits by the whole warp. Returns the entry of each lane k < K,
+// or -1.
+__device__ __noinline__ int exact_choice(const RouteArgs& a, int64_t row, unsigned long long* keys) {
+    const int lane = threadIdx.x & 31, E = a.E;
     if (a.groups > 1) {
         const int size = E / a.groups;
-        unsigned long long worth = 0;
-        if (lane < a.groups) {
-            unsigned long long first = 0, second = 0;
-            for (int e = lane * size; e < (lane + 1) * size; ++e) {
-                const unsigned long long k = keys[e];
-                if (k > first) {
-                    second = first;
-                    first = k;
-                } else if (k > second) {
-                    second = k;
-                }
-            }
-            worth = first;
-            if (a.group_top2 && second != 0) worth = key_of(value_of(first) + value_of(second));
-        }
-        const uint32_t kept = best_groups(worth, a);
+        const uint32_t kept = exact_groups(a, row, keys);
         for (int e = lane; e < E; e += 32)
             if (!((kept >> (e / size)) & 1)) keys[e] = 0;
         // without a bias experts go by their logits, not by what scores are left
         // of them
-        if (scores && a.bias == nullptr)
+        if (a.bias == nullptr)
             for (int e = lane; e < E; e += 32)
                 if (keys[e] != 0) keys[e] = key_of(static_cast<double>(load_logit(a, row + e)));
         __syncwarp();
+    } else {
+        exact_keys(a, row, keys);
     }
     int mine = -1;
     for (int k = 0; k < a.K; ++k) {
@@ -264,6 +292,34 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, unsigned 
         __syncwarp();
     }
     return mine;
+}
+
+// The order of the warp's candidates (lane i's `e`, -1: none) in 64 bits, among
+// which the chosen ones are: returns lane k's.
+__device__ __noinline__ int exact_order(const RouteArgs& a, int64_t row, int e) {
+    const int lane = threadIdx.x & 31;
+    const float l = e >= 0 ? load_logit(a, row + e) : 0.0f;
+    unsigned long long key = 0;
+    if (a.bias != nullptr) {
+        Exact x{};
+        if (a.softmax) x = exact_softmax(a, row);
+        const double c = exact_score(a, x, l) + (e >= 0 ? __ldg(a.bias + e) : 0.0f);
+        if (e >= 0) key = key_of(c);
+    } else if (e >= 0) {
+        key = key_of(static_cast<double>(l));
+    }
+    int rank = 0;
+    for (int i = 0; i < 32; ++i) {
+        const unsigned long long o = __shfl_sync(kFullMask, key, i);
+        const int oe = __shfl_sync(kFullMask, e, i);
+        rank += (o > key || (o == key && oe < e && oe >= 0)) ? 1 : 0;
+    }
+    int mine = -1;
+    for (int i = 0; i < 32; ++i) {
+        const int oe = __shfl_sync(kFullMask, e, i), to = __shfl_sync(kFullMask, rank, i);
+        if (oe >= 0 && to == lane) mine = oe;
+    }
+    return lane < a.K ? mine : -1;
 }
 
 // Descending, by odd-even merging.
@@ -296,7 +352,7 @@ struct Scores {
     float m, r;
     float bound;
     __device__ __forceinline__ float of(float l) const {
-        return softmax ? __expf(l - m) * r : approx_reciprocal(1.0f + __expf(-l));
+        return softmax ? approx_exp(l - m) * r : approx_reciprocal(1.0f + approx_exp(-l));
     }
 };
 
@@ -330,7 +386,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     }
     Scores score{a.softmax, m, approx_reciprocal(z), 0.0f};
     score.bound = a.softmax ? score.r * static_cast<float>(V + 40) * 0x1p-24f : 0x1p-21f;
-    bool odd = false;  // whether the choice has to be made again in 64 bits
     uint32_t key[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -342,7 +397,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
                 c += b[j];
                 out |= b[j] == -kInf;
             }
-            odd |= !out && c != c;
         }
         key[j] = out ? 0u : key_of(c);
     }
@@ -385,14 +439,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
             error += fabsf(value) * 0x1p-23f;
             if (worth != 0) worth = key_of(value);
         }
-        const uint32_t kept = best_groups(worth, a);
+        uint32_t kept = best_groups(worth, a);
         if (scores) {
             const bool mine = (kept >> lane) & 1;
             const uint32_t low =
                 __reduce_min_sync(kFullMask, worth != 0 && mine ? key_of(value - error) : 0xFFFFFFFFu);
             const uint32_t high =
                 __reduce_max_sync(kFullMask, worth != 0 && !mine ? key_of(value + error) : 0u);
-            odd |= high >= low;
+            if (high >= low) kept = exact_groups(a, row, keys64);
         }
         if (lanes > 0) {
             const bool stays = (kept >> (lane / max(lanes, 1))) & 1;
@@ -420,58 +474,86 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     for (int j = 0; j < V; ++j)
         if (key[j] != 0) key[j] = (key[j] & ~kLast) | (kLast - j);
     if constexpr (kSort) sort_descending<V>(key);
-    // K rounds, and one more for what the last of them has to be larger than
-    int mine = -1, next = -1;
-    for (int k = 0; k <= a.K; ++k) {
+    // A round: the largest that is left becomes lane k's (and the last one's).
+    int mine = -1, last = -1;
+    uint32_t mine_key = 0, last_key = 0;
+    auto take = [&](int k) {
         uint32_t head = key[0];
         if constexpr (!kSort) {
 #pragma unroll
             for (int j = 1; j < V; ++j) head = max(head, key[j]);
         }
         const uint32_t most = __reduce_max_sync(kFullMask, head & ~kLast);
-        if (most == 0) break;
+        if (most == 0) return false;
         const int owner = __ffs(__ballot_sync(kFullMask, (head & ~kLast) == most)) - 1;
-        const int e = owner * V + static_cast<int>(kLast - (__shfl_sync(kFullMask, head, owner) & kLast));
-        if (lane == k) mine = e;
-        if (k == a.K) next = e;
-        if (lane == owner) {
-            if constexpr (kSort) {
+        last = owner * V + static_cast<int>(kLast - (__shfl_sync(kFullMask, head, owner) & kLast));
+        last_key = most;
+        const bool won = lane == owner, here = lane == k;
+        mine = here ? last : mine;
+        mine_key = here ? most : mine_key;
+        if constexpr (kSort) {
 #pragma unroll
-                for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1];
-                key[V - 1] = 0;
-            } else {
+            for (int j = 0; j + 1 < V; ++j) key[j] = won ? key[j + 1] : key[j];
+            key[V - 1] = won ? 0u : key[V - 1];
+        } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (key[j] == head) key[j] = 0;
+            for (int j = 0; j < V; ++j) key[j] = won && key[j] == head ? 0u : key[j];
+        }
+        return true;
+    };
+    // Whether one is larger than the next by more than both may be off: their own
+    // error, c's rounding and the lost bits, up to V units of 2^-23 of the value. (By
+    // logits only the lost bits matter. NaN goes before all.)
+    auto clear = [&](uint32_t k1, uint32_t k2) {
+        if (a.bias == nullptr) return k1 > k2;
+        const float c1 = value_of(k1), c2 = value_of(k2);
+        const float off = 2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * (static_cast<float>(V + 1) * 0x1p-23f);
+        return c1 - c2 > off || k1 > (0xFF800000u | kLast);
+    };
+    int n = 0;  // K, and the one that the last of them has to be larger than
+    while (n <= a.K && take(n)) ++n;
+    {
+        uint32_t next_key = __shfl_down_sync(kFullMask, mine_key, 1);
+        if (lane == 31) next_key = last_key;  // (K = 32)
+        bool doubt = lane < min(n - 1, a.K) && !clear(mine_key, next_key);
+        if (__any_sync(kFullMask, doubt)) {
+            // the lost bits back, and equal ones
+            int next = __shfl_down_sync(kFullMask, mine, 1);
+            if (lane == 31) next = last;
+            if (doubt) {
+                const float l1 = load_logit(a, row + mine), l2 = load_logit(a, row + next);
+                if (a.bias != nullptr) {
+                    const float b1 = __ldg(a.bias + mine), b2 = __ldg(a.bias + next);
+                    const float c1 = score.of(l1) + b1, c2 = score.of(l2) + b2;
+                    const float off = 2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * 0x1p-22f;
+                    doubt = !(l1 == l2 && b1 == b2 && mine < next) && !(c1 - c2 > off);
+                } else {
+                    const uint32_t k1 = key_of(l1), k2 = key_of(l2);
+                    doubt = k1 < k2 || (k1 == k2 && mine > next);
+                }
+            }
+            const uint32_t doubts = __ballot_sync(kFullMask, doubt);
+            if (doubts != 0) {
+                // the candidates for the K places, down to a clear step
+                int count = a.K;
+                bool found = true;
+                if ((doubts >> (a.K - 1)) & 1) {
+                    found = false;
+                    for (count = n; !found && count < 32;) {
+                        const uint32_t before = last_key;
+                        if (!take(count) || clear(before, last_key))
+                            found = true;
+                        else
+                            ++count;
+                    }
+                }
+                mine = found ? exact_order(a, row, lane < count ? mine : -1)
+                             : exact_choice(a, row, keys64);
             }
         }
     }
     if (lane >= a.K) mine = -1;
-    // Is each of them larger than the one after it, by more than both may be off?
-    float lk = mine >= 0 ? load_logit(a, row + mine) : -kInf;
-    {
-        int e2 = __shfl_down_sync(kFullMask, mine, 1);
-        float l2 = __shfl_down_sync(kFullMask, lk, 1);
-        if (lane == a.K - 1) {
-            e2 = next;
-            l2 = next >= 0 ? load_logit(a, row + next) : -kInf;
-        }
-        if (mine >= 0 && e2 >= 0) {
-            if (a.bias != nullptr) {
-                const float b1 = __ldg(a.bias + mine), b2 = __ldg(a.bias + e2);
-                const float c1 = score.of(lk) + b1, c2 = score.of(l2) + b2;
-                const float off = 2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * 0x1p-22f;
-                odd |= !(lk == l2 && b1 == b2) && !(c1 - c2 > off);
-            } else {
-                const uint32_t k1 = key_of(lk), k2 = key_of(l2);
-                odd |= k1 < k2 || (k1 == k2 && mine > e2);
-            }
-        }
-    }
-    if (__any_sync(kFullMask, odd)) {
-        mine = route_exact(a, t, keys64);
-        lk = mine >= 0 ? load_logit(a, row + mine) : -kInf;
-    }
+    const float lk = mine >= 0 ? load_logit(a, row + mine) : -kInf;
 
     // weights: lane k's
     float w = 0.0f;
