@@ -108,169 +108,141 @@ struct Part {
     int rows;
 };
 
-// How a warp goes through 32 rows of a chunk of kCols columns of out, N of them to a
+// How a warp goes through the 32 rows of a chunk's columns of out, four of them to a
 // lane: kRounds times kAtOnce rows.
-template <int N, bool kGated>
+template <bool kGated>
 struct Walk {
     static constexpr int kCols = kGated ? kChunk / 2 : kChunk;
-    static constexpr int kPieces = kCols / N, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
+    static constexpr int kPieces = kCols / 4, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
 };
 
-// What a lane adds to its values of a chunk, or of a quarter of one, read ahead
-// of them.
-template <int kQuarters>
+// What a lane adds to its values of a chunk, read ahead of them.
+template <bool kGated>
 struct Ahead {
-    uint32_t bits[8 * kQuarters];
+    Residual r[Walk<kGated>::kRounds];
 };
-template <int N, bool kGated, int kQuarters>
-__device__ __forceinline__ void read_ahead_by(const LinearArgs& a, const Part& part, int64_t col,
-                                              int quarter, Ahead<kQuarters>& ahead) {
-    using W = Walk<N, kGated>;
-    constexpr int kRounds = W::kRounds * kQuarters / 4;
-    const int lane = threadIdx.x & 31;
-    const int64_t c = col + lane % W::kPieces * N;
+template <bool kGated>
+__device__ __forceinline__ void read_ahead(const LinearArgs& a, const Part& part, int64_t col, bool vec,
+                                           Ahead<kGated>& ahead) {
+    using W = Walk<kGated>;
+    if (a.residual == nullptr) return;
+    const int lane = threadIdx.x & 31, r0 = lane / W::kPieces;
+    const int64_t c = col + lane % W::kPieces * 4;
     if (c >= a.n) return;
-    const int r0 = lane / W::kPieces + quarter * (W::kRounds / 4) * W::kAtOnce;
     int64_t at = (part.row0 + r0) * a.n + c;
 #pragma unroll
-    for (int i = 0; i < kRounds; ++i, at += W::kAtOnce * a.n) {
-        if (r0 + i * W::kAtOnce >= part.rows) continue;
-        const Residual<N> v = load_residual<N>(a, at);
-#pragma unroll
-        for (int j = 0; j < N; ++j) ahead.bits[N * i + j] = v.bits[j];
-    }
-}
-template <bool kGated, int kQuarters>
-__device__ __forceinline__ void read_ahead(const LinearArgs& a, const Part& part, int64_t col,
-                                           int quarter, Ahead<kQuarters>& ahead) {
-    if (a.residual == nullptr) return;
-    if (a.n % 4 == 0)
-        read_ahead_by<4, kGated>(a, part, col, quarter, ahead);
-    else
-        read_ahead_by<1, kGated>(a, part, col, quarter, ahead);
+    for (int i = 0; i < W::kRounds; ++i, at += W::kAtOnce * a.n)
+        if (r0 + i * W::kAtOnce < part.rows) ahead.r[i] = load_residual(a, at, a.n - c, vec);
 }
 
-// 32 x 32 sums from the turning place, or with a quarter's Ahead 8 rows of them:
-// `col` the column of the first (gated: of 16 of each half).
-template <int N, bool kGated, int kQuarters>
-__device__ __forceinline__ void write_chunk_by(const LinearArgs& a, uint32_t turn, const Part& part,
-                                               int64_t col, int quarter,
-                                               const Ahead<kQuarters>& ahead) {
-    using W = Walk<N, kGated>;
-    constexpr int kRounds = W::kRounds * kQuarters / 4;
-    const int lane = threadIdx.x & 31, p = lane % W::kPieces;
-    const int64_t c = col + p * N;
-    if (c >= a.n) return;
-    const int r0 = lane / W::kPieces + quarter * (W::kRounds / 4) * W::kAtOnce;
-    Values<N> v[kRounds], up[kRounds];
-    Residual<N> res[kRounds];
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const int r = r0 + i * W::kAtOnce;
-        if constexpr (N == 4) {
-            const float4 f = load_shared_v4(turn_at(turn, r, p));
-            v[i] = {{f.x, f.y, f.z, f.w}};
-            if (kGated) {
-                const float4 u = load_shared_v4(turn_at(turn, r, p + W::kPieces));
-                up[i] = {{u.x, u.y, u.z, u.w}};
-            }
-        } else {
-            v[i] = {{load_shared_f32(turn_at(turn, r, p / 4) + p % 4 * 4)}};
-            if (kGated) up[i] = {{load_shared_f32(turn_at(turn, r, (p + W::kCols) / 4) + p % 4 * 4)}};
-        }
-#pragma unroll
-        for (int j = 0; j < N; ++j) res[i].bits[j] = ahead.bits[N * i + j];
-    }
-    if (a.bias != nullptr) {
-        const Values<N> b0 = load_bias<N>(a, c), b1 = load_bias<N>(a, kGated ? a.n + c : c);
-#pragma unroll
-        for (int i = 0; i < kRounds; ++i) {
-            v[i] = sum<N>(v[i], b0);
-            if (kGated) up[i] = sum<N>(up[i], b1);
+// Bias, z and the activation, on a chunk in its turning place: `col` the column of
+// its first sums (gated: of 16 of each half, whose results take the gate's place).
+// Not unrolled: all warps of the SM go through the same few instructions.
+template <bool kGated>
+__device__ __forceinline__ void activate_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
+                                               int64_t col, bool vec) {
+    using W = Walk<kGated>;
+    const int lane = threadIdx.x & 31, p = lane % W::kPieces, r0 = lane / W::kPieces;
+    const int64_t c = col + p * 4, left = a.n - c;
+    if (left > 0) {
+        const Four b0 = load_bias(a.bias, c, left), b1 = load_bias(a.bias, kGated ? a.n + c : c, left);
+#pragma unroll 2
+        for (int i = 0; i < W::kRounds; ++i) {
+            const int r = r0 + i * W::kAtOnce;
+            if (r >= part.rows) break;
+            const uint32_t at = turn_at(turn, r, p);
+            Four v = four(load_shared_v4(at)) + b0, up = {};
+            if (kGated) up = four(load_shared_v4(turn_at(turn, r, p + W::kPieces))) + b1;
+            keep_z<kGated>(a, part.row0 + r, c, v, up, left, vec);
+            v = activate<kGated>(a, v, up);
+            store_shared_v4(at, make_float4(v.v[0], v.v[1], v.v[2], v.v[3]));
         }
     }
-    const int rows = (part.rows - r0 + W::kAtOnce - 1) / W::kAtOnce;
-    finish<kRounds, N, kGated>(a, part.row0 + r0, c, W::kAtOnce, rows, v, up, res);
+    __syncwarp();
 }
-template <bool kGated, int kQuarters>
+
+// A chunk from its turning place to out.
+template <bool kGated>
 __device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
-                                            int64_t col, int quarter, const Ahead<kQuarters>& ahead) {
-    if (a.n % 4 == 0)
-        write_chunk_by<4, kGated>(a, turn, part, col, quarter, ahead);
-    else  // rows that do not start on 16 bytes: value by value
-        write_chunk_by<1, kGated>(a, turn, part, col, quarter, ahead);
+                                            int64_t col, bool vec, const Ahead<kGated>& ahead) {
+    using W = Walk<kGated>;
+    const int lane = threadIdx.x & 31, p = lane % W::kPieces, r0 = lane / W::kPieces;
+    const int64_t c = col + p * 4, left = a.n - c;
+    if (left <= 0) return;
+    Four v[W::kRounds];
+#pragma unroll
+    for (int i = 0; i < W::kRounds; ++i)
+        v[i] = four(load_shared_v4(turn_at(turn, r0 + i * W::kAtOnce, p)));
+    if (a.residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < W::kRounds; ++i) v[i] = v[i] + residual_values(a, ahead.r[i], vec);
+    }
+    int64_t at = (part.row0 + r0) * a.n + c;
+#pragma unroll
+    for (int i = 0; i < W::kRounds; ++i, at += W::kAtOnce * a.n)
+        if (r0 + i * W::kAtOnce < part.rows) store_out(a, at, v[i], left, vec);
 }
 
 // The sums of a tile that the cluster's CTAs took parts of k of: each has laid
 // its own out in shared memory; CTA `rank` adds, in the parts' order, and writes
-// those of the rows r = rank mod kParts. A thread takes N neighbouring columns of
-// kAtOnce rows at a time, so that its loads overlap.
-template <Mode kMode, int N, bool kGated, int kParts>
+// those of the rows r = rank mod kParts. A thread takes four neighbouring columns
+// of a few rows at a time, so that its loads overlap.
+template <Mode kMode, bool kGated, int kParts>
 __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
                                                   int rank) {
     using S = Shape<kMode>;
-    constexpr int kCols = kGated ? S::kCols / 2 : S::kCols, kPieces = kCols / N;
+    constexpr int kCols = kGated ? S::kCols / 2 : S::kCols, kPieces = kCols / 4;
     constexpr int kStep = kOutWarps * 32 / kPieces;  // of this CTA's rows, by all threads
     constexpr int kMost = kRows / kParts / kStep;    // of them to a thread
     constexpr int kAtOnce = kMost < 1 ? 1 : kMost < 8 / kParts ? kMost : 8 / kParts;
-    const int64_t left = a.m - tile.row0;
-    const int rows = static_cast<int>(left < kRows ? left : kRows);
+    const int64_t rows_left = a.m - tile.row0;
+    const int rows = static_cast<int>(rows_left < kRows ? rows_left : kRows);
     const int own = (rows + kParts - 1 - rank) / kParts;
-    const int c = threadIdx.x % kPieces * N;
-    const int64_t col = tile.col_tile * kCols + c;
-    if (col >= a.n) return;
-    const Values<N> b0 = load_bias<N>(a, col), b1 = load_bias<N>(a, kGated ? a.n + col : col);
+    const int c = threadIdx.x % kPieces * 4;
+    const int64_t col = tile.col_tile * kCols + c, left = a.n - col;
+    const bool vec = a.n % 4 == 0;
+    if (left <= 0) return;
+#pragma unroll 1
     for (int i0 = threadIdx.x / kPieces; i0 < own; i0 += kAtOnce * kStep) {
-        Values<N> v[kAtOnce][kParts], up[kAtOnce][kParts], vs[kAtOnce], us[kAtOnce];
-        Residual<N> res[kAtOnce] = {};
+        Four v[kAtOnce][kParts], up[kAtOnce][kParts];
+        Residual res[kAtOnce] = {};
         const int64_t row = tile.row0 + i0 * kParts + rank;
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
             const int i = i0 + j * kStep;
             if (i >= own) continue;
             if (a.residual != nullptr)
-                res[j] = load_residual<N>(a, (row + static_cast<int64_t>(j) * kStep * kParts) * a.n + col);
+                res[j] = load_residual(a, (row + j * kStep * kParts) * a.n + col, left, vec);
             const uint32_t at = sums + (i * kParts + rank) * S::kPitch + c * 4;
 #pragma unroll
             for (int p = 0; p < kParts; ++p) {
                 const uint32_t from = cluster_map(at, p);
-                if constexpr (N == 4) {
-                    const float4 f = load_cluster_v4(from);
-                    v[j][p] = {{f.x, f.y, f.z, f.w}};
-                    if (kGated) {
-                        const float4 u = load_cluster_v4(from + kCols * 4);
-                        up[j][p] = {{u.x, u.y, u.z, u.w}};
-                    }
-                } else {
-                    v[j][p] = {{load_cluster_f32(from)}};
-                    if (kGated) up[j][p] = {{load_cluster_f32(from + kCols * 4)}};
-                }
+                v[j][p] = four(load_cluster_v4(from));
+                if (kGated) up[j][p] = four(load_cluster_v4(from + kCols * 4));
             }
         }
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
-            vs[j] = v[j][0];
-            if (kGated) us[j] = up[j][0];
+            if (i0 + j * kStep >= own) continue;
 #pragma unroll
             for (int p = 1; p < kParts; ++p) {
-                vs[j] = sum<N>(vs[j], v[j][p]);
-                if (kGated) us[j] = sum<N>(us[j], up[j][p]);
+                v[j][0] = v[j][0] + v[j][p];
+                if (kGated) up[j][0] = up[j][0] + up[j][p];
             }
-            vs[j] = sum<N>(vs[j], b0);
-            if (kGated) us[j] = sum<N>(us[j], b1);
+            finish<kGated>(a, row + j * kStep * kParts, col, v[j][0], kGated ? up[j][0] : v[j][0], res[j],
+                           left, vec);
         }
-        finish<kAtOnce, N, kGated>(a, row, col, kStep * kParts, (own - i0 + kStep - 1) / kStep, vs, us, res);
     }
 }
-template <Mode kMode, int N, bool kGated>
+template <Mode kMode, bool kGated>
 __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
                                                   int rank) {
     if (a.split == 2)
-        write_shared_tile<kMode, N, kGated, 2>(a, sums, tile, rank);
+        write_shared_tile<kMode, kGated, 2>(a, sums, tile, rank);
     else if (a.split == 4)
-        write_shared_tile<kMode, N, kGated, 4>(a, sums, tile, rank);
+        write_shared_tile<kMode, kGated, 4>(a, sums, tile, rank);
     else if (a.split == 8)
-        write_shared_tile<kMode, N, kGated, 8>(a, sums, tile, rank);
+        write_shared_tile<kMode, kGated, 8>(a, sums, tile, rank);
 }
 
 // 32 x 32 sums of a warp into its turning place.
@@ -464,6 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kCols = kGated ? kChunk / 2 : kChunk, kMine = kGated ? S::kMine / 2 : S::kMine;
         // the second half of a chunk's sums: gated, the up half's
         constexpr int kSecond = kGated ? S::kCols / 2 : 16;
+        const bool vec = a.n % 4 == 0;
+        const bool plain = !kGated && a.act == EP_ACT_NONE && a.bias == nullptr && a.z == nullptr;
         auto release = [&](int i) {
             __syncwarp();
             tcgen05_fence_before();
@@ -481,57 +455,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             part.row0 = tile.row0 + (kMode == kPair ? rank * kRows : 0) + quarter * 32;
             part.rows = static_cast<int>(min(static_cast<int64_t>(32), a.m - part.row0));
             const int64_t col0 = tile.col_tile * (2 * kMine) + half * kMine;
+            Ahead<kGated> ahead = {};
+            if (!kExact && !S::kParts) read_ahead<kGated>(a, part, col0, vec, ahead);
             if constexpr (kExact) {
-                float acc[S::kMine / kChunk][2][16] = {};
-                for (int kb = kb_first; kb < kb_end; kb += per_sum, slot.next()) {
+                // all but the last of the tile's sums into registers, which the last ones
+                // are then added to, in their place
+                float acc[S::kMine / 16][16] = {};
+                for (int kb = kb_first; kb < kb_end; kb += per_sum) {
                     ok = warp_wait<kMode == kPair>(sums + 8 * slot.i, slot.round, abort, a.status);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t at = from + slot.i * S::kCols + half * kMine;
+                    const bool last = kb + per_sum >= kb_end;
 #pragma unroll
-                    for (int c = 0; c < S::kMine / kChunk; ++c) {
-                        uint32_t v[2][16];
-                        tmem_load16(at + c * kCols, v[0]);
-                        tmem_load16(at + c * kCols + kSecond, v[1]);
-                        tmem_load_wait16(v[0]);
-                        tmem_load_wait16(v[1]);
+                    for (int c = 0; c < S::kMine / 16; ++c) {
+                        // gated, 64 of each half: the columns that it writes
+                        const uint32_t at = from + slot.i * S::kCols + half * kMine + 16 * c +
+                                            (16 * c >= kMine ? S::kCols / 2 - kMine : 0);
+                        uint32_t v[16];
+                        tmem_load16(at, v);
+                        tmem_load_wait16(v);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            acc[c][0][i] += __uint_as_float(v[0][i]);
-                            acc[c][1][i] += __uint_as_float(v[1][i]);
+                            acc[c][i] += __uint_as_float(v[i]);
+                            v[i] = __float_as_uint(acc[c][i]);
                         }
+                        if (last) tmem_store16(at, v);
                     }
+                    if (last) break;
                     release(slot.i);
+                    slot.next();
                 }
                 if (!ok) break;
-                if (part.rows <= 0) continue;
-#pragma unroll
-                for (int c = 0; c < S::kMine / kChunk; ++c) {
-                    if (col0 + c * kCols >= a.n) break;
-                    turn_chunk(turn, acc[c][0], acc[c][1]);
-                    if (a.residual == nullptr) {
-                        write_chunk<kGated>(a, turn, part, col0 + c * kCols, 0, Ahead<4>{});
-                        continue;
-                    }
-                    // (registers for no more than a quarter's)
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        Ahead<1> ahead = {};
-                        read_ahead<kGated>(a, part, col0 + c * kCols, q, ahead);
-                        write_chunk<kGated>(a, turn, part, col0 + c * kCols, q, ahead);
-                    }
-                }
-                continue;
+                tmem_store_wait();
+                read_ahead<kGated>(a, part, col0, vec, ahead);
+            } else {
+                ok = warp_wait<kMode == kPair>(sums + 8 * slot.i, slot.round, abort, a.status);
+                if (!ok) break;
+                tcgen05_fence_after();
             }
-            Ahead<4> ahead = {};
-            if (!S::kParts) read_ahead<kGated>(a, part, col0, 0, ahead);
-            ok = warp_wait<kMode == kPair>(sums + 8 * slot.i, slot.round, abort, a.status);
-            if (!ok) break;
-            tcgen05_fence_after();
             const uint32_t slot_at = from + slot.i * S::kCols;
             if constexpr (S::kParts) {
                 const uint32_t own = base + (quarter * 32 + lane) * S::kPitch + half * S::kMine * 4;
-#pragma unroll
+#pragma unroll 2
                 for (int c = 0; c < S::kMine; c += 16) {
                     uint32_t v[16];
                     tmem_load16(slot_at + half * S::kMine + c, v);
@@ -555,9 +520,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_load_wait16(v[1]);
                         turn_chunk(turn, reinterpret_cast<const float*>(v[0]),
                                    reinterpret_cast<const float*>(v[1]));
-                        const Ahead<4> now = ahead;
-                        if (c + kCols < kMine) read_ahead<kGated>(a, part, col0 + c + kCols, 0, ahead);
-                        write_chunk<kGated>(a, turn, part, col0 + c, 0, now);
+                        if (!plain) activate_chunk<kGated>(a, turn, part, col0 + c, vec);
+                        const Ahead<kGated> now = ahead;
+                        if (c + kCols < kMine) read_ahead<kGated>(a, part, col0 + c + kCols, vec, ahead);
+                        write_chunk<kGated>(a, turn, part, col0 + c, vec, now);
                     }
                 }
                 release(slot.i);
@@ -571,10 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_wait();
         if (warp < kOutWarps && t0 < tiles && load_shared(abort) == 0) {
             const Tile tile = tile_at<kMode>(t0, a);
-            if (a.n % 4 == 0)
-                write_shared_tile<kMode, 4, kGated>(a, base, tile, rank);
-            else
-                write_shared_tile<kMode, 1, kGated>(a, base, tile, rank);
+            write_shared_tile<kMode, kGated>(a, base, tile, rank);
         }
     }
     __syncwarp();

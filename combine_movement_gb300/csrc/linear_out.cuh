@@ -1,5 +1,5 @@
-// linear_out.cuh -- the end of a dense product: from the sums of a few
-// neighbouring values of a row to what is stored of them.
+// linear_out.cuh -- the end of a dense product: from the sums of four neighbouring
+// values of a row to what is stored of them.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -14,136 +14,131 @@ namespace ep {
 __device__ __forceinline__ float bf16_low(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
-// N (4 or 1) neighbouring values of a row.
-template <int N>
-struct Values {
-    float v[N];
+// Four neighbouring values of a row. In memory `left` of them (at most four) are
+// there; rows of a multiple of four values hold them all, 16-byte (in bf16 8-byte)
+// aligned (`vec`).
+struct Four {
+    float v[4];
 };
-template <int N>
-__device__ __forceinline__ void store_bf16(uint16_t* p, const Values<N>& r) {
-    if constexpr (N == 4)
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(r.v[0], r.v[1]), pack_bf16x2(r.v[2], r.v[3]));
-    else
-        *p = __bfloat16_as_ushort(__float2bfloat16_rn(r.v[0]));
+__device__ __forceinline__ Four operator+(const Four& x, const Four& y) {
+    return {{x.v[0] + y.v[0], x.v[1] + y.v[1], x.v[2] + y.v[2], x.v[3] + y.v[3]}};
 }
-template <int N>
-__device__ __forceinline__ void store_f32(float* p, const Values<N>& r) {
-    if constexpr (N == 4)
-        *reinterpret_cast<float4*>(p) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-    else
-        *p = r.v[0];
+__device__ __forceinline__ Four four(float4 f) { return {{f.x, f.y, f.z, f.w}}; }
+
+__device__ __forceinline__ Four load_bias(const float* bias, int64_t col, int64_t left) {
+    Four r = {};
+    if (bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) r.v[i] = __ldg(bias + col + i);
+    }
+    return r;
 }
 
-// What is added to N values of out, as it lies in memory until it is added.
-template <int N>
+// What is added to four values, as it lies in memory until it is added.
 struct Residual {
-    uint32_t bits[N];
+    uint32_t bits[4];
 };
-template <int N>
-__device__ __forceinline__ Residual<N> load_residual(const LinearArgs& a, int64_t at) {
-    Residual<N> r = {};
-    if constexpr (N == 4) {
-        if (a.out_f32) {
-            const uint4 f = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.residual) + at);
+__device__ __forceinline__ Residual load_residual(const LinearArgs& a, int64_t at, int64_t left,
+                                                  bool vec) {
+    Residual r = {};
+    if (a.out_f32) {
+        const uint32_t* p = static_cast<const uint32_t*>(a.residual) + at;
+        if (vec) {
+            const uint4 f = *reinterpret_cast<const uint4*>(p);
             r.bits[0] = f.x, r.bits[1] = f.y, r.bits[2] = f.z, r.bits[3] = f.w;
         } else {
-            const uint2 f = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + at);
-            r.bits[0] = f.x, r.bits[1] = f.y;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left) r.bits[i] = p[i];
         }
     } else {
-        if (a.out_f32)
-            r.bits[0] = static_cast<const uint32_t*>(a.residual)[at];
-        else
-            r.bits[0] = static_cast<uint32_t>(static_cast<const uint16_t*>(a.residual)[at]) << 16;
-    }
-    return r;
-}
-template <int N>
-__device__ __forceinline__ Values<N> residual_values(const LinearArgs& a, const Residual<N>& r) {
-    if constexpr (N == 4) {
-        if (!a.out_f32)
-            return {{bf16_low(r.bits[0]), bf16_high(r.bits[0]), bf16_low(r.bits[1]), bf16_high(r.bits[1])}};
-        return {{__uint_as_float(r.bits[0]), __uint_as_float(r.bits[1]), __uint_as_float(r.bits[2]),
-                 __uint_as_float(r.bits[3])}};
-    } else {
-        return {{__uint_as_float(r.bits[0])}};
-    }
-}
-
-// What is added to N columns from `col` on of b's sums.
-template <int N>
-__device__ __forceinline__ Values<N> load_bias(const LinearArgs& a, int64_t col) {
-    Values<N> r = {};
-    if (a.bias != nullptr) {
+        const uint16_t* p = static_cast<const uint16_t*>(a.residual) + at;
+        if (vec) {
+            const uint2 f = *reinterpret_cast<const uint2*>(p);
+            r.bits[0] = f.x, r.bits[1] = f.y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) r.v[i] = __ldg(a.bias + col + i);
+            for (int i = 0; i < 4; ++i)
+                if (i < left) r.bits[i] = p[i];
+        }
     }
     return r;
 }
-
-template <int N>
-__device__ __forceinline__ Values<N> sum(const Values<N>& x, const Values<N>& y) {
-    Values<N> r;
-#pragma unroll
-    for (int i = 0; i < N; ++i) r.v[i] = x.v[i] + y.v[i];
-    return r;
+__device__ __forceinline__ Four residual_values(const LinearArgs& a, const Residual& r, bool vec) {
+    const uint32_t* b = r.bits;
+    if (a.out_f32)
+        return {{__uint_as_float(b[0]), __uint_as_float(b[1]), __uint_as_float(b[2]), __uint_as_float(b[3])}};
+    if (vec) return {{bf16_low(b[0]), bf16_high(b[0]), bf16_low(b[1]), bf16_high(b[1])}};
+    return {{bf16_low(b[0]), bf16_low(b[1]), bf16_low(b[2]), bf16_low(b[3])}};
 }
 
-// The activation of `v` (gated: with `up`), for the whole array at once, so that
-// what it is is asked once.
-template <int kCount, int N, bool kGated>
-__device__ __forceinline__ void activate_all(Values<N> (&v)[kCount], const Values<N> (&up)[kCount],
-                                             int act) {
+__device__ __forceinline__ void store_bf16(uint16_t* p, const Four& r, int64_t left, bool vec) {
+    const uint32_t lo = pack_bf16x2(r.v[0], r.v[1]), hi = pack_bf16x2(r.v[2], r.v[3]);
+    if (vec) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+        return;
+    }
+    if (0 < left) p[0] = static_cast<uint16_t>(lo);
+    if (1 < left) p[1] = static_cast<uint16_t>(lo >> 16);
+    if (2 < left) p[2] = static_cast<uint16_t>(hi);
+    if (3 < left) p[3] = static_cast<uint16_t>(hi >> 16);
+}
+__device__ __forceinline__ void store_out(const LinearArgs& a, int64_t at, const Four& r, int64_t left,
+                                          bool vec) {
+    if (!a.out_f32) {
+        store_bf16(static_cast<uint16_t*>(a.out) + at, r, left, vec);
+        return;
+    }
+    float* p = static_cast<float*>(a.out) + at;
+    if (vec) {
+        *reinterpret_cast<float4*>(p) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < left) p[i] = r.v[i];
+}
+
+// act(v), gated silu(v) * up.
+template <bool kGated>
+__device__ __forceinline__ Four activate(const LinearArgs& a, Four v, const Four& up) {
     auto each = [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < kCount; ++i)
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[i].v[j] = f(v[i].v[j], up[i].v[j]);
+        for (int i = 0; i < 4; ++i) v.v[i] = f(v.v[i], up.v[i]);
     };
     if (kGated)
         each([](float g, float u) { return silu(g) * u; });
-    else if (act == EP_ACT_RELU)
+    else if (a.act == EP_ACT_RELU)
         each([](float z, float) { return activate(z, EP_ACT_RELU); });
-    else if (act == EP_ACT_GELU)
+    else if (a.act == EP_ACT_GELU)
         each([](float z, float) { return activate(z, EP_ACT_GELU); });
-    else if (act == EP_ACT_SILU)
+    else if (a.act == EP_ACT_SILU)
         each([](float z, float) { return activate(z, EP_ACT_SILU); });
+    return v;
 }
 
-// The end of kCount times N values of out, `apart` rows apart from row `row` on,
-// of which `rows` (as many as are there) are stored: sums with their bias in `v`
-// (gated: the up half's in `up`), `residual` what is added.
-template <int kCount, int N, bool kGated>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int64_t col, int apart,
-                                       int rows, Values<N> (&v)[kCount], const Values<N> (&up)[kCount],
-                                       const Residual<N> (&residual)[kCount]) {
-    if (a.z != nullptr) {
-        const int64_t pitch = kGated ? 2 * a.n : a.n;
-        uint16_t* z = a.z + row * pitch + col;
-#pragma unroll
-        for (int i = 0; i < kCount; ++i, z += apart * pitch) {
-            if (i >= rows) continue;
-            store_bf16<N>(z, v[i]);
-            if (kGated) store_bf16<N>(z + a.n, up[i]);
-        }
-    }
-    activate_all<kCount, N, kGated>(v, up, a.act);
-    if (a.residual != nullptr) {
-#pragma unroll
-        for (int i = 0; i < kCount; ++i) v[i] = sum<N>(v[i], residual_values<N>(a, residual[i]));
-    }
-    const int64_t at = row * a.n + col, step = apart * a.n;
-    if (a.out_f32) {
-        float* p = static_cast<float*>(a.out) + at;
-#pragma unroll
-        for (int i = 0; i < kCount; ++i, p += step)
-            if (i < rows) store_f32<N>(p, v[i]);
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(a.out) + at;
-#pragma unroll
-        for (int i = 0; i < kCount; ++i, p += step)
-            if (i < rows) store_bf16<N>(p, v[i]);
-    }
+// z, where it is kept: row `row`'s values from column `col` on, sums with their
+// bias in `v` (gated: the up half's in `up`).
+template <bool kGated>
+__device__ __forceinline__ void keep_z(const LinearArgs& a, int64_t row, int64_t col, const Four& v,
+                                       const Four& up, int64_t left, bool vec) {
+    if (a.z == nullptr) return;
+    uint16_t* z = a.z + row * (kGated ? 2 * a.n : a.n) + col;
+    store_bf16(z, v, left, vec);
+    if (kGated) store_bf16(z + a.n, up, left, vec);
+}
+
+// All of it, for sums without their bias.
+template <bool kGated>
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int64_t col, Four v, Four up,
+                                       const Residual& residual, int64_t left, bool vec) {
+    v = v + load_bias(a.bias, col, left);
+    if (kGated) up = up + load_bias(a.bias, a.n + col, left);
+    keep_z<kGated>(a, row, col, v, up, left, vec);
+    v = activate<kGated>(a, v, up);
+    if (a.residual != nullptr) v = v + residual_values(a, residual, vec);
+    store_out(a, row * a.n + col, v, left, vec);
 }
 
 }  // namespace ep

@@ -358,7 +358,7 @@ struct Scores {
 
 // kFull: E = 32 V in 16-byte aligned rows.
 template <int V, bool kFull>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(const RouteArgs a) {
     extern __shared__ unsigned long long smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned long long* const keys64 = smem + static_cast<int64_t>(warp) * a.E;
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const RouteArgs
             const float dk = __shfl_sync(kFullMask, d, k);
 #pragma unroll
             for (int j = 0; j < V; ++j)
-                if (e == j) out[j] += dk;
+                out[j] += e == j ? dk : 0.0f;
         }
         if (dense) {
             const float r = __fdiv_rn(1.0f, z);
