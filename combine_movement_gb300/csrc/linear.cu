@@ -69,6 +69,8 @@ struct Shape {
 
 struct Maps {
     CUtensorMap a, b;
+    CUtensorMap out;                         // where `plain`
+    bool plain;                              // out is the rounded sums, in aligned rows
     int a_rows;                              // of a's box along m (not by_k)
 };
 
@@ -183,6 +185,54 @@ __device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, 
         if (r0 + i * W::kAtOnce < part.rows) store_out(a, at, v[i], left, vec);
 }
 
+// 32 x 32 sums of a warp into its turning place.
+__device__ __forceinline__ void turn_chunk(uint32_t turn, const float* v0, const float* v1) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();  // the chunk before has been read
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        store_shared_v4(turn_at(turn, lane, i),
+                        make_float4(v0[4 * i], v0[4 * i + 1], v0[4 * i + 2], v0[4 * i + 3]));
+        store_shared_v4(turn_at(turn, lane, 4 + i),
+                        make_float4(v1[4 * i], v1[4 * i + 1], v1[4 * i + 2], v1[4 * i + 3]));
+    }
+    __syncwarp();
+}
+
+// A chunk that is out as it is: each lane lays its row's 32 sums out as the copy
+// engine's swizzle has them (fp32 rows of 128 bytes: the turning place's own; bf16 rows
+// of 64), which takes them out together. `second`: of two places that take turns.
+__device__ __forceinline__ void send_chunk(const LinearArgs& a, const Maps& maps, uint32_t turn,
+                                           const Part& part, int64_t col, bool second,
+                                           const uint32_t (&v)[2][16]) {
+    const int lane = threadIdx.x & 31;
+    if (a.out_f32) {
+        if (elect_one()) bulk_wait_read<0>();  // the chunk before has left
+        turn_chunk(turn, reinterpret_cast<const float*>(v[0]), reinterpret_cast<const float*>(v[1]));
+    } else {
+        if (elect_one()) bulk_wait_read<1>();  // the one before that
+        __syncwarp();
+        turn += second ? kTurnBytes / 2 : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t* w = &v[i / 2][i % 2 * 8];
+            auto pack = [&](int j) {
+                return pack_bf16x2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
+            };
+            const uint32_t at = turn + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4);
+            store_shared_v4(at, make_float4(__uint_as_float(pack(0)), __uint_as_float(pack(2)),
+                                            __uint_as_float(pack(4)), __uint_as_float(pack(6))));
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (elect_one()) {
+        tensor_store_2d(&maps.out, static_cast<int>(col), static_cast<int>(part.row0), turn);
+        bulk_commit();
+    }
+    __syncwarp();
+}
+
 // The sums of a tile that the cluster's CTAs took parts of k of: each has laid
 // its own out in shared memory; CTA `rank` adds, in the parts' order, and writes
 // those of the rows r = rank mod kParts. A thread takes four neighbouring columns
@@ -245,20 +295,6 @@ __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t 
         write_shared_tile<kMode, kGated, 8>(a, sums, tile, rank);
 }
 
-// 32 x 32 sums of a warp into its turning place.
-__device__ __forceinline__ void turn_chunk(uint32_t turn, const float* v0, const float* v1) {
-    const int lane = threadIdx.x & 31;
-    __syncwarp();  // the chunk before has been read
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        store_shared_v4(turn_at(turn, lane, i),
-                        make_float4(v0[4 * i], v0[4 * i + 1], v0[4 * i + 2], v0[4 * i + 3]));
-        store_shared_v4(turn_at(turn, lane, 4 + i),
-                        make_float4(v1[4 * i], v1[4 * i + 1], v1[4 * i + 2], v1[4 * i + 3]));
-    }
-    __syncwarp();
-}
-
 // kExact: sums leave tensor memory every kExactBlocks blocks along k and are added
 // in registers (not of shared tiles, whose parts are added as they are joined).
 template <Mode kMode, bool kGated, bool kExact>
@@ -298,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp && lane == 0) {
         prefetch_tensor_map(&maps.a);
         prefetch_tensor_map(&maps.b);
+        if (maps.plain) prefetch_tensor_map(&maps.out);
     }
     tcgen05_fence_before();
     __syncthreads();
@@ -437,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the second half of a chunk's sums: gated, the up half's
         constexpr int kSecond = kGated ? S::kCols / 2 : 16;
         const bool vec = a.n % 4 == 0;
-        const bool plain = !kGated && a.act == EP_ACT_NONE && a.bias == nullptr && a.z == nullptr;
+        const bool plain = !kGated && maps.plain;
+        const bool as_is = !kGated && a.act == EP_ACT_NONE && a.bias == nullptr && a.z == nullptr;
         auto release = [&](int i) {
             __syncwarp();
             tcgen05_fence_before();
@@ -448,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         Ring<kSlots> slot;
-        bool ok = true;
+        bool ok = true, second = false;
         for (int64_t t = t0; ok && t < tiles; t += step) {
             const Tile tile = tile_at<kMode>(t, a);
             Part part;
@@ -518,9 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_load16(at + kSecond, v[1]);
                         tmem_load_wait16(v[0]);
                         tmem_load_wait16(v[1]);
+                        if (plain) {
+                            send_chunk(a, maps, turn, part, col0 + c, second, v);
+                            second = !second;
+                            continue;
+                        }
                         turn_chunk(turn, reinterpret_cast<const float*>(v[0]),
                                    reinterpret_cast<const float*>(v[1]));
-                        if (!plain) activate_chunk<kGated>(a, turn, part, col0 + c, vec);
+                        if (!as_is) activate_chunk<kGated>(a, turn, part, col0 + c, vec);
                         const Ahead<kGated> now = ahead;
                         if (c + kCols < kMine) read_ahead<kGated>(a, part, col0 + c + kCols, vec, ahead);
                         write_chunk<kGated>(a, turn, part, col0 + c, vec, now);
@@ -530,6 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 slot.next();
             }
         }
+        if (elect_one()) bulk_wait<0>();  // what was sent has been written
+        __syncwarp();
     }
     if (S::kParts) {
         // Every thread passes both barriers, whatever its CTA found to do.
@@ -589,6 +634,21 @@ bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t width
               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// out, written in boxes of 32 x 32.
+bool encode_out(CUtensorMap* map, const LinearArgs& a) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t size = a.out_f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.n), static_cast<cuuint64_t>(a.m)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.n) * size};
+    const cuuint32_t box[2] = {kChunk, 32};
+    const cuuint32_t step[2] = {1, 1};
+    return fn(map, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              a.out, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              a.out_f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <Mode kMode, bool kGated, bool kExact>
@@ -704,7 +764,9 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
                   : encode_map(&maps.a, a.a, a.m, a.k, a.a_pitch, maps.a_rows)) &&
         (a.b_by_k ? encode_map(&maps.b, a.b, a.k, b_rows, a.b_pitch, kTileK)
                   : encode_map(&maps.b, a.b, b_rows, a.k, a.b_pitch, cols / 2));
-    if (!ok) return cudaErrorInvalidValue;
+    maps.plain = a.act == EP_ACT_NONE && a.bias == nullptr && a.z == nullptr && a.residual == nullptr &&
+                 a.n % (a.out_f32 ? 4 : 8) == 0 && (pair || plan.mode == kAlone);
+    if (!ok || (maps.plain && !encode_out(&maps.out, a))) return cudaErrorInvalidValue;
     const int64_t tiles = a.row_tiles * a.col_tiles;
     const bool exact = a.out_f32 && a.k_blocks > kExactBlocks;
     if (pair) {

@@ -195,6 +195,17 @@ __device__ __forceinline__ void tensor_load_2d(uint32_t dst_smem, const CUtensor
         : "memory");
 }
 
+// Shared memory -> box of `map` at (x, y), both 0 or more, tracked by this thread's
+// bulk async-group; what lies out of range is not written.
+__device__ __forceinline__ void tensor_store_2d(const CUtensorMap* map, int32_t x, int32_t y,
+                                                uint32_t src_smem) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y), "r"(src_smem)
+        : "memory");
+}
+
 // The same into this CTA's shared memory, completing on `bar`, a shared::cluster
 // address in either CTA of the pair.
 __device__ __forceinline__ void tensor_load_2d_pair(uint32_t dst_smem, const CUtensorMap* map,
