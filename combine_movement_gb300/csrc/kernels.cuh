@@ -305,10 +305,13 @@ struct RouteArgs {
     void* d_logits;            // [T][E], the logits' type
     int32_t* status;
     // set by launch_route
+    int group_size;            // E / groups
+    float group_part;          // 1 / group_size
     int group_lanes;           // lanes of a warp that hold a group's experts, 0: none
+    int log_group_lanes;
 };
 
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream);
+cudaError_t launch_route(RouteArgs a, cudaStream_t stream);
 cudaError_t launch_route_grad(const RouteArgs& a, cudaStream_t stream);
 
 // ---- dense products ----------------------------------------------------------

@@ -137,33 +137,51 @@ __device__ __forceinline__ void read_ahead(const LinearArgs& a, const Part& part
         if (r0 + i * W::kAtOnce < part.rows) ahead.r[i] = load_residual(a, at, a.n - c, vec);
 }
 
-// Bias, z and the activation, on a chunk in its turning place: `col` the column of
-// its first sums (gated: of 16 of each half, whose results take the gate's place).
-// Not unrolled: all warps of the SM go through the same few instructions.
+// A chunk from its turning place to out, with all that may be asked for: `col` the
+// column of its first sums (gated: of 16 of each half). Two rounds at a time, not
+// unrolled further: a small call goes through these instructions once, and its time
+// is that of bringing them in. (Unrolled, 333 x 1075 with all of it took 4.7 us in
+// here, so 3.) The next rounds' residual is read ahead.
 template <bool kGated>
-__device__ __forceinline__ void activate_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
-                                               int64_t col, bool vec) {
+__device__ __forceinline__ void finish_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
+                                             int64_t col, bool vec) {
     using W = Walk<kGated>;
     const int lane = threadIdx.x & 31, p = lane % W::kPieces, r0 = lane / W::kPieces;
     const int64_t c = col + p * 4, left = a.n - c;
-    if (left > 0) {
-        const Four b0 = load_bias(a.bias, c, left), b1 = load_bias(a.bias, kGated ? a.n + c : c, left);
-#pragma unroll 2
-        for (int i = 0; i < W::kRounds; ++i) {
-            const int r = r0 + i * W::kAtOnce;
-            if (r >= part.rows) break;
-            const uint32_t at = turn_at(turn, r, p);
-            Four v = four(load_shared_v4(at)) + b0, up = {};
-            if (kGated) up = four(load_shared_v4(turn_at(turn, r, p + W::kPieces))) + b1;
-            keep_z<kGated>(a, part.row0 + r, c, v, up, left, vec);
-            v = activate<kGated>(a, v, up);
-            store_shared_v4(at, make_float4(v.v[0], v.v[1], v.v[2], v.v[3]));
+    if (left <= 0) return;
+    const Four b0 = load_bias(a.bias, c, left), b1 = load_bias(a.bias, kGated ? a.n + c : c, left);
+    auto residual = [&](int i) {
+        const int r = r0 + i * W::kAtOnce;
+        if (a.residual == nullptr || r >= part.rows) return Residual{};
+        return load_residual(a, (part.row0 + r) * a.n + c, left, vec);
+    };
+    Residual next[2] = {residual(0), residual(1)};
+#pragma unroll 1
+    for (int i = 0; i < W::kRounds; i += 2) {
+        const Residual now[2] = {next[0], next[1]};
+        next[0] = residual(i + 2);
+        next[1] = residual(i + 3);
+        Four v[2], up[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = r0 + (i + j) * W::kAtOnce;
+            v[j] = four(load_shared_v4(turn_at(turn, r, p))) + b0;
+            up[j] = v[j];
+            if (kGated) up[j] = four(load_shared_v4(turn_at(turn, r, p + W::kPieces))) + b1;
+            if (r < part.rows) keep_z<kGated>(a, part.row0 + r, c, v[j], up[j], left, vec);
+        }
+        activate<kGated>(a, v, up);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = r0 + (i + j) * W::kAtOnce;
+            if (r >= part.rows) continue;
+            if (a.residual != nullptr) v[j] = v[j] + residual_values(a, now[j], vec);
+            store_out(a, (part.row0 + r) * a.n + c, v[j], left, vec);
         }
     }
-    __syncwarp();
 }
 
-// A chunk from its turning place to out.
+// A chunk whose sums have at most a residual to be added, all of it read ahead.
 template <bool kGated>
 __device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
                                             int64_t col, bool vec, const Ahead<kGated>& ahead) {
@@ -494,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             part.rows = static_cast<int>(min(static_cast<int64_t>(32), a.m - part.row0));
             const int64_t col0 = tile.col_tile * (2 * kMine) + half * kMine;
             Ahead<kGated> ahead = {};
-            if (!kExact && !S::kParts) read_ahead<kGated>(a, part, col0, vec, ahead);
+            if (!kExact && !S::kParts && as_is) read_ahead<kGated>(a, part, col0, vec, ahead);
             if constexpr (kExact) {
                 // all but the last of the tile's sums into registers, which the last ones
                 // are then added to, in their place
@@ -525,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 tmem_store_wait();
-                read_ahead<kGated>(a, part, col0, vec, ahead);
+                if (as_is) read_ahead<kGated>(a, part, col0, vec, ahead);
             } else {
                 ok = warp_wait<kMode == kPair>(sums + 8 * slot.i, slot.round, abort, a.status);
                 if (!ok) break;
@@ -563,7 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         turn_chunk(turn, reinterpret_cast<const float*>(v[0]),
                                    reinterpret_cast<const float*>(v[1]));
-                        if (!as_is) activate_chunk<kGated>(a, turn, part, col0 + c, vec);
+                        if (!as_is) {
+                            finish_chunk<kGated>(a, turn, part, col0 + c, vec);
+                            continue;
+                        }
                         const Ahead<kGated> now = ahead;
                         if (c + kCols < kMine) read_ahead<kGated>(a, part, col0 + c + kCols, vec, ahead);
                         write_chunk<kGated>(a, turn, part, col0 + c, vec, now);

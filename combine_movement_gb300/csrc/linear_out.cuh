@@ -100,12 +100,15 @@ __device__ __forceinline__ void store_out(const LinearArgs& a, int64_t at, const
         if (i < left) p[i] = r.v[i];
 }
 
-// act(v), gated silu(v) * up.
-template <bool kGated>
-__device__ __forceinline__ Four activate(const LinearArgs& a, Four v, const Four& up) {
+// act(v), gated silu(v) * up, of all at once, so that what it is is asked once.
+template <bool kGated, int kCount>
+__device__ __forceinline__ void activate(const LinearArgs& a, Four (&v)[kCount],
+                                         const Four (&up)[kCount]) {
     auto each = [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v.v[i] = f(v.v[i], up.v[i]);
+        for (int j = 0; j < kCount; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j].v[i] = f(v[j].v[i], up[j].v[i]);
     };
     if (kGated)
         each([](float g, float u) { return silu(g) * u; });
@@ -115,7 +118,6 @@ __device__ __forceinline__ Four activate(const LinearArgs& a, Four v, const Four
         each([](float z, float) { return activate(z, EP_ACT_GELU); });
     else if (a.act == EP_ACT_SILU)
         each([](float z, float) { return activate(z, EP_ACT_SILU); });
-    return v;
 }
 
 // z, where it is kept: row `row`'s values from column `col` on, sums with their
@@ -131,14 +133,15 @@ __device__ __forceinline__ void keep_z(const LinearArgs& a, int64_t row, int64_t
 
 // All of it, for sums without their bias.
 template <bool kGated>
-__device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int64_t col, Four v, Four up,
-                                       const Residual& residual, int64_t left, bool vec) {
-    v = v + load_bias(a.bias, col, left);
-    if (kGated) up = up + load_bias(a.bias, a.n + col, left);
-    keep_z<kGated>(a, row, col, v, up, left, vec);
-    v = activate<kGated>(a, v, up);
-    if (a.residual != nullptr) v = v + residual_values(a, residual, vec);
-    store_out(a, row * a.n + col, v, left, vec);
+__device__ __forceinline__ void finish(const LinearArgs& a, int64_t row, int64_t col, const Four& sums,
+                                       const Four& up_sums, const Residual& residual, int64_t left,
+                                       bool vec) {
+    Four v[1] = {sums + load_bias(a.bias, col, left)}, up[1] = {up_sums};
+    if (kGated) up[0] = up[0] + load_bias(a.bias, a.n + col, left);
+    keep_z<kGated>(a, row, col, v[0], up[0], left, vec);
+    activate<kGated>(a, v, up);
+    if (a.residual != nullptr) v[0] = v[0] + residual_values(a, residual, vec);
+    store_out(a, row * a.n + col, v[0], left, vec);
 }
 
 }  // namespace ep

@@ -183,7 +183,7 @@ __device__ __forceinline__ float approx_exp(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.44269504088896341f));
     return r;
 }
-__device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.0f, 1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid(float l) { return approx_reciprocal(1.0f + expf(-l)); }
 
 // The groups to keep, as a bit mask, from each lane's group (`key` of its worth,
 // 0 where it has no expert left).
@@ -191,9 +191,10 @@ template <typename Key>
 __device__ __forceinline__ uint32_t best_groups(Key key, const RouteArgs& a) {
     const int lane = threadIdx.x & 31;
     int rank = 0;
+#pragma unroll 4
     for (int g = 0; g < a.groups; ++g) {
         const Key o = __shfl_sync(kFullMask, key, g);
-        rank += (o > key || (o == key && g < lane)) ? 1 : 0;
+        rank += g < lane ? (o >= key ? 1 : 0) : (o > key ? 1 : 0);
     }
     return __ballot_sync(kFullMask, lane < a.groups && rank < a.topk_groups && key != 0);
 }
@@ -236,14 +237,13 @@ __device__ __noinline__ void exact_keys(const RouteArgs& a, int64_t row, unsigne
 
 // The groups that stay, by values in 64 bits; leaves exact_keys.
 __device__ __noinline__ uint32_t exact_groups(const RouteArgs& a, int64_t row, unsigned long long* keys) {
-    const int lane = threadIdx.x & 31, size = a.E / a.groups;
+    const int lane = threadIdx.x & 31, size = a.group_size;
     exact_keys(a, row, keys);
     unsigned long long worth = 0;
     if (lane < a.groups) {
         unsigned long long first = 0, second = 0;
         for (int i = 0; i < size; ++i) {
-            // (the lanes start at different places, so that they meet in few banks)
-            const unsigned long long k = keys[lane * size + (i + lane) % size];
+            const unsigned long long k = keys[lane * size + i];
             if (k > first) {
                 second = first;
                 first = k;
@@ -356,9 +356,80 @@ struct Scores {
     }
 };
 
+// The groups that stay, where what the choice's integers have lost leaves it open: by
+// scores as they are in 32 bits, and where that leaves it open too in 64. The groups'
+// experts are those of neighbouring lanes, else 64 bits decide at once.
+template <int V, bool kFull>
+__device__ __noinline__ uint32_t settle_groups(const RouteArgs& a, int64_t row, const Scores& score,
+                                               unsigned long long* keys) {
+    if (!kFull || a.group_lanes == 0) return exact_groups(a, row, keys);
+    const int lane = threadIdx.x & 31;
+    const bool scores = a.bias != nullptr || a.group_top2;
+    float l[V], b[V] = {};
+    load_part<V, kFull>(a.logits, a.bf16_logits, row, a.E, -kInf, l);
+    if (a.bias != nullptr) load_part<V, kFull>(a.bias, false, 0, a.E, -kInf, b);
+    // the two largest of a group, over its lanes, to the lane of its number
+    auto join = [&](auto& first, auto& second) {
+        for (int d = 1; d < a.group_lanes; d <<= 1) {
+            const auto f = __shfl_xor_sync(kFullMask, first, d), s = __shfl_xor_sync(kFullMask, second, d);
+            second = max(min(first, f), max(second, s));
+            first = max(first, f);
+        }
+        first = __shfl_sync(kFullMask, first, lane * a.group_lanes);
+        second = __shfl_sync(kFullMask, second, lane * a.group_lanes);
+    };
+    if (scores) {
+        uint32_t first = 0, second = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const bool out = l[j] == -kInf || b[j] == -kInf;
+            const uint32_t k = out ? 0u : key_of(score.of(l[j]) + b[j]);
+            second = max(second, min(first, k));
+            first = max(first, k);
+        }
+        join(first, second);
+        float value = value_of(first), error = score.bound + fabsf(value) * 0x1p-23f;
+        uint32_t worth = lane < a.groups ? first : 0;
+        if (a.group_top2 && second != 0) {
+            const float v2 = value_of(second);
+            error += score.bound + fabsf(v2) * 0x1p-23f;
+            value += v2;
+            error += fabsf(value) * 0x1p-23f;
+            if (worth != 0) worth = key_of(value);
+        }
+        const uint32_t kept = best_groups(worth, a);
+        const bool stays = (kept >> lane) & 1;
+        const uint32_t low =
+            __reduce_min_sync(kFullMask, worth != 0 && stays ? key_of(value - error) : 0xFFFFFFFFu);
+        const uint32_t high =
+            __reduce_max_sync(kFullMask, worth != 0 && !stays ? key_of(value + error) : 0u);
+        if (high < low) return kept;
+    }
+    Exact x{};
+    if (a.softmax && scores) x = exact_softmax(a, row);
+    unsigned long long first = 0, second = 0;
+#pragma unroll 1
+    for (int j = 0; j < V; ++j) {
+        const int e = lane * V + j;
+        const float le = load_logit(a, row + e), be = a.bias != nullptr ? __ldg(a.bias + e) : 0.0f;
+        double c = le;
+        if (scores) c = exact_score(a, x, le) + be;
+        const unsigned long long k = le == -kInf || be == -kInf ? 0ull : key_of(c);
+        second = max(second, min(first, k));
+        first = max(first, k);
+    }
+    join(first, second);
+    unsigned long long worth = lane < a.groups ? first : 0;
+    if (a.group_top2 && worth != 0 && second != 0) worth = key_of(value_of(first) + value_of(second));
+    return best_groups(worth, a);
+}
+
+// Integers of out experts: at most that of -inf, whatever their last bits.
+constexpr uint32_t kOutKey = 0x007FFFFFu;
+
 // kFull: E = 32 V in 16-byte aligned rows.
 template <int V, bool kFull>
-__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ unsigned long long smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned long long* const keys64 = smem + static_cast<int64_t>(warp) * a.E;
@@ -367,12 +438,21 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
     if (t >= a.T) return;
     const int64_t row = t * a.E;
-    const int e0 = lane * V;
-
+    const bool scores = a.bias != nullptr || (a.groups > 1 && a.group_top2);
+    const bool by_logit = a.bias == nullptr;  // what the experts go by, if not the groups
     float l[V], b[V];
     load_part<V, kFull>(a.logits, a.bf16_logits, row, a.E, -kInf, l);
-    if (a.bias != nullptr) load_part<V, kFull>(a.bias, false, 0, a.E, 0.0f, b);
-    const bool scores = a.bias != nullptr || (a.groups > 1 && a.group_top2);
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = 0.0f;
+    if (a.bias != nullptr) load_part<V, kFull>(a.bias, false, 0, a.E, -kInf, b);
+    constexpr uint32_t kLast = V - 1;
+    static_assert((V & (V - 1)) == 0, "a power of two");
+    constexpr bool kSort = V <= 16;
+    // An integer without its last bits, which say which of the lane's experts it is (the
+    // lower the index, the larger). What is lost with them shows where the chosen
+    // ones' values are compared.
+    auto pack = [&](float c, int j) { return (key_of(c) & ~kLast) | (kLast - j); };
+
     float m = 0.0f, z = 1.0f;
     if (a.softmax && (scores || !a.renormalize)) {
         float top = -kInf;
@@ -384,33 +464,25 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
         for (int j = 0; j < V; ++j) sum += l[j] == -kInf ? 0.0f : expf(l[j] - m);
         z = warp_sum(sum);
     }
-    Scores score{a.softmax, m, approx_reciprocal(z), 0.0f};
-    score.bound = a.softmax ? score.r * static_cast<float>(V + 40) * 0x1p-24f : 0x1p-21f;
+    Scores score{a.softmax, m, approx_reciprocal(z), 0x1p-21f};
+    if (a.softmax) score.bound = score.r * static_cast<float>(V + 40) * 0x1p-24f;
     uint32_t key[V];
+    if (scores) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float c = l[j];
-        bool out = l[j] == -kInf;
-        if (scores) {
-            c = score.of(l[j]);
-            if (a.bias != nullptr) {
-                c += b[j];
-                out |= b[j] == -kInf;
-            }
-        }
-        key[j] = out ? 0u : key_of(c);
+        for (int j = 0; j < V; ++j)
+            key[j] = pack(l[j] == -kInf || b[j] == -kInf ? -kInf : score.of(l[j]) + b[j], j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) key[j] = pack(l[j], j);
     }
+    if constexpr (kSort) sort_descending<V>(key);
     if (a.groups > 1) {
         uint32_t first = 0, second = 0;
-        const int lanes = kFull ? a.group_lanes : 0;
-        const int size = a.E / a.groups;
-        auto add = [&](uint32_t k) {
-            second = max(second, min(first, k));
-            first = max(first, k);
-        };
+        const int lanes = kFull && kSort ? a.group_lanes : 0;
+        const int size = a.group_size;
         if (lanes > 0) {  // a group's experts are those of `lanes` neighbouring lanes
-#pragma unroll
-            for (int j = 0; j < V; ++j) add(key[j]);
+            first = key[0];
+            second = V > 1 ? key[V > 1 ? 1 : 0] : 0;
             for (int d = 1; d < lanes; d <<= 1) {
                 const uint32_t f = __shfl_xor_sync(kFullMask, first, d);
                 const uint32_t s = __shfl_xor_sync(kFullMask, second, d);
@@ -423,60 +495,66 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
         } else {
             uint32_t* keys = reinterpret_cast<uint32_t*>(keys64);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (e0 + j < a.E) keys[e0 + j] = key[j];
+            for (int j = 0; j < V; ++j) {
+                const int e = lane * V + static_cast<int>(kLast - (key[j] & kLast));
+                if (e < a.E) keys[e] = key[j];
+            }
             __syncwarp();
             if (lane < a.groups)
-                for (int e = lane * size; e < (lane + 1) * size; ++e) add(keys[e]);
+                for (int e = lane * size; e < (lane + 1) * size; ++e) {
+                    const uint32_t k = keys[e];
+                    second = max(second, min(first, k));
+                    first = max(first, k);
+                }
             __syncwarp();
         }
-        uint32_t worth = lane < a.groups ? first : 0;
-        float value = value_of(first), error = score.bound + fabsf(value) * 0x1p-23f;
-        if (a.group_top2 && second != 0) {
-            const float v2 = value_of(second);
-            error += score.bound + fabsf(v2) * 0x1p-23f;
-            value += v2;
-            error += fabsf(value) * 0x1p-23f;
-            if (worth != 0) worth = key_of(value);
-        }
+        first &= ~kLast;
+        second &= ~kLast;
+        uint32_t worth = lane < a.groups && first > kOutKey ? first : 0;
+        if (a.group_top2 && worth != 0 && second > kOutKey)
+            worth = key_of(value_of(first) + value_of(second));
         uint32_t kept = best_groups(worth, a);
-        if (scores) {
-            const bool mine = (kept >> lane) & 1;
-            const uint32_t low =
-                __reduce_min_sync(kFullMask, worth != 0 && mine ? key_of(value - error) : 0xFFFFFFFFu);
-            const uint32_t high =
-                __reduce_max_sync(kFullMask, worth != 0 && !mine ? key_of(value + error) : 0u);
-            if (high >= low) kept = exact_groups(a, row, keys64);
+        // Are the worst that stays and the best that does not clearly apart? Each is
+        // off by two scores' errors, three roundings and twice the lost bits, up to
+        // V units of 2^-23 of what was added, of which no part is larger than 1 + the
+        // sum's magnitude (by logits: the lost bits alone).
+        const bool stays = (kept >> lane) & 1;
+        const uint32_t low = __reduce_min_sync(kFullMask, worth != 0 && stays ? worth : 0xFFFFFFFFu);
+        const uint32_t high = __reduce_max_sync(kFullMask, stays ? 0u : worth);
+        if (high != 0) {
+            bool clear = low > (0xFF800000u | kLast) && high < (0xFF800000u | kLast);  // NaN first
+            if (!scores) {
+                clear |= low > high;
+            } else {
+                const float v1 = value_of(low), v2 = value_of(high);
+                float parts = fabsf(v1) + fabsf(v2);
+                if (a.group_top2) parts += 2.0f * warp_max(fabsf(value_of(first)) < kInf ? fabsf(value_of(first)) : 0.0f);
+                clear |= v1 - v2 > 4.0f * score.bound + parts * (static_cast<float>(2 * V + 4) * 0x1p-23f);
+            }
+            if (!clear) kept = settle_groups<V, kFull>(a, row, score, keys64);
         }
-        if (lanes > 0) {
-            const bool stays = (kept >> (lane / max(lanes, 1))) & 1;
+        if (scores && by_logit) {  // from here on by logits
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (!stays) key[j] = 0;
+            for (int j = 0; j < V; ++j) key[j] = pack(l[j], j);
+            if constexpr (kSort) sort_descending<V>(key);
+        }
+        if (lanes > 0) {  // (a lane whose largest is out takes no part)
+            key[0] = (kept >> (lane >> a.log_group_lanes)) & 1 ? key[0] : 0;
         } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (e0 + j >= a.E || !((kept >> ((e0 + j) / size)) & 1)) key[j] = 0;
-        }
-        if (scores && a.bias == nullptr) {
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (key[j] != 0) key[j] = key_of(l[j]);
+            for (int j = 0; j < V; ++j) {
+                const int e = lane * V + static_cast<int>(kLast - (key[j] & kLast));
+                // (e / size: a float's error is far below half of 1 / size)
+                const int g = static_cast<int>((static_cast<float>(e) + 0.5f) * a.group_part);
+                if (e >= a.E || !((kept >> g) & 1)) key[j] = key[j] & kLast;
+            }
+            if constexpr (kSort) sort_descending<V>(key);
         }
     }
-    // The lane's experts in order: the integers without their last bits, which say
-    // which expert it is (the lower the index, the larger). What is lost with them
-    // shows below, where the chosen ones' values are compared.
-    constexpr uint32_t kLast = V - 1;
-    static_assert((V & (V - 1)) == 0, "a power of two");
-    constexpr bool kSort = V <= 16;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (key[j] != 0) key[j] = (key[j] & ~kLast) | (kLast - j);
-    if constexpr (kSort) sort_descending<V>(key);
     // A round: the largest that is left becomes lane k's (and the last one's).
-    int mine = -1, last = -1;
-    uint32_t mine_key = 0, last_key = 0;
+    // (its index: the lane it was found in, and the last bits)
+    int mine_owner = -1, last_owner = -1;
+    uint32_t mine_head = 0, last_head = 0;
     auto take = [&](int k) {
         uint32_t head = key[0];
         if constexpr (!kSort) {
@@ -484,13 +562,13 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
             for (int j = 1; j < V; ++j) head = max(head, key[j]);
         }
         const uint32_t most = __reduce_max_sync(kFullMask, head & ~kLast);
-        if (most == 0) return false;
+        if (most <= kOutKey) return false;
         const int owner = __ffs(__ballot_sync(kFullMask, (head & ~kLast) == most)) - 1;
-        last = owner * V + static_cast<int>(kLast - (__shfl_sync(kFullMask, head, owner) & kLast));
-        last_key = most;
+        last_owner = owner;
+        last_head = __shfl_sync(kFullMask, head, owner);
         const bool won = lane == owner, here = lane == k;
-        mine = here ? last : mine;
-        mine_key = here ? most : mine_key;
+        mine_owner = here ? last_owner : mine_owner;
+        mine_head = here ? last_head : mine_head;
         if constexpr (kSort) {
 #pragma unroll
             for (int j = 0; j + 1 < V; ++j) key[j] = won ? key[j + 1] : key[j];
@@ -505,28 +583,36 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
     // error, c's rounding and the lost bits, up to V units of 2^-23 of the value. (By
     // logits only the lost bits matter. NaN goes before all.)
     auto clear = [&](uint32_t k1, uint32_t k2) {
-        if (a.bias == nullptr) return k1 > k2;
+        k1 &= ~kLast;
+        k2 &= ~kLast;
+        if (by_logit) return k1 > k2;
         const float c1 = value_of(k1), c2 = value_of(k2);
-        const float off = 2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * (static_cast<float>(V + 1) * 0x1p-23f);
-        return c1 - c2 > off || k1 > (0xFF800000u | kLast);
+        const float off =
+            2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * (static_cast<float>(V + 1) * 0x1p-23f);
+        return c1 - c2 > off || (k1 > 0xFF800000u && k2 <= 0xFF800000u);
     };
     int n = 0;  // K, and the one that the last of them has to be larger than
     while (n <= a.K && take(n)) ++n;
+    auto index = [&](int owner, uint32_t head) {
+        return owner < 0 ? -1 : owner * V + static_cast<int>(kLast - (head & kLast));
+    };
+    int mine = index(mine_owner, mine_head);
     {
-        uint32_t next_key = __shfl_down_sync(kFullMask, mine_key, 1);
-        if (lane == 31) next_key = last_key;  // (K = 32)
-        bool doubt = lane < min(n - 1, a.K) && !clear(mine_key, next_key);
+        uint32_t next_head = __shfl_down_sync(kFullMask, mine_head, 1);
+        if (lane == 31) next_head = last_head;  // (K = 32)
+        bool doubt = lane < min(n - 1, a.K) && !clear(mine_head, next_head);
         if (__any_sync(kFullMask, doubt)) {
             // the lost bits back, and equal ones
             int next = __shfl_down_sync(kFullMask, mine, 1);
-            if (lane == 31) next = last;
+            if (lane == 31) next = index(last_owner, last_head);
             if (doubt) {
                 const float l1 = load_logit(a, row + mine), l2 = load_logit(a, row + next);
-                if (a.bias != nullptr) {
+                if (!by_logit) {
                     const float b1 = __ldg(a.bias + mine), b2 = __ldg(a.bias + next);
                     const float c1 = score.of(l1) + b1, c2 = score.of(l2) + b2;
                     const float off = 2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * 0x1p-22f;
-                    doubt = !(l1 == l2 && b1 == b2 && mine < next) && !(c1 - c2 > off);
+                    doubt = !(l1 == l2 && b1 == b2 && mine < next) && !(c1 - c2 > off) &&
+                        !(c1 != c1 && (c2 == c2 || mine < next));
                 } else {
                     const uint32_t k1 = key_of(l1), k2 = key_of(l2);
                     doubt = k1 < k2 || (k1 == k2 && mine > next);
@@ -540,12 +626,13 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
                 if ((doubts >> (a.K - 1)) & 1) {
                     found = false;
                     for (count = n; !found && count < 32;) {
-                        const uint32_t before = last_key;
-                        if (!take(count) || clear(before, last_key))
+                        const uint32_t before = last_head;
+                        if (!take(count) || clear(before, last_head))
                             found = true;
                         else
                             ++count;
                     }
+                    mine = index(mine_owner, mine_head);
                 }
                 mine = found ? exact_order(a, row, lane < count ? mine : -1)
                              : exact_choice(a, row, keys64);
@@ -558,19 +645,18 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
     // weights: lane k's
     float w = 0.0f;
     if (a.renormalize) {
-        const float high = warp_max(lk);
-        if (a.softmax) {
-            w = mine >= 0 ? expf(lk - high) : 0.0f;
-        } else if (high >= 0.0f) {
+        if (!a.softmax && __any_sync(kFullMask, lk >= 0.0f)) {
             w = mine >= 0 ? sigmoid(lk) : 0.0f;
+        } else if (const float high = warp_max(lk); a.softmax) {
+            w = mine >= 0 ? expf(lk - high) : 0.0f;
         } else {
             // by e^high, so that scores below fp32's range keep their ratios
             w = mine >= 0 ? __fdiv_rn(expf(lk - high) * (1.0f + expf(high)), 1.0f + expf(lk)) : 0.0f;
         }
         const float sum = warp_sum(w);
-        w = mine >= 0 ? __fdiv_rn(w, sum) : 0.0f;
+        w = mine >= 0 ? w * approx_reciprocal(sum) : 0.0f;
     } else if (mine >= 0) {
-        w = a.softmax ? __fdiv_rn(expf(lk - m), z) : sigmoid(lk);
+        w = a.softmax ? expf(lk - m) * score.r : sigmoid(lk);
     }
     if (lane < a.K) {
         a.topk_idx[t * a.K + lane] = mine;
@@ -589,7 +675,7 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
 // memory, for more than 8). An expert that a token has twice gets the sum of
 // both, in their order.
 template <int V, bool kFull>
-__global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_constant__ RouteArgs a) {
     extern __shared__ unsigned long long smem[];
     constexpr bool kHeld = V > 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -724,7 +810,10 @@ cudaError_t launch_route_v(RouteArgs a, size_t smem, cudaStream_t stream) {
     if (a.E != 32 * V || !aligned16(a.logits) || !aligned16(a.bias))
         return launch_tokens(route_kernel<V, false>, a, smem, stream);
     const int lanes = 32 / a.groups;
-    a.group_lanes = a.groups > 1 && lanes * a.groups == 32 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    if (a.groups > 1 && lanes * a.groups == 32 && (lanes & (lanes - 1)) == 0) {
+        a.group_lanes = lanes;
+        while ((1 << a.log_group_lanes) < lanes) ++a.log_group_lanes;
+    }
     return launch_tokens(route_kernel<V, true>, a, smem, stream);
 }
 
@@ -737,7 +826,9 @@ cudaError_t launch_route_grad_v(const RouteArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t stream) {
+cudaError_t launch_route(RouteArgs a, cudaStream_t stream) {
+    a.group_size = a.E / a.groups;
+    a.group_part = 1.0f / static_cast<float>(a.group_size);
     const size_t smem = sizeof(unsigned long long) * kWarps * static_cast<size_t>(a.E);
     const int v = (a.E + 31) / 32;
     if (v <= 1) return launch_route_v<1>(a, smem, stream);

@@ -601,7 +601,13 @@ def ep_linear(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor,
             and x.dtype is _BF16 and w.dtype is _BF16 and x.is_contiguous() and w.is_contiguous()
             and y.is_contiguous() and x.is_cuda
             and x.get_device() == w.get_device() == y.get_device() == _cur_device()
-            and bias is None and residual is None and z is None):
+            and (bias is None or bias.dtype is _F32 and bias.dim() == 1 and bias.shape[0] == ws[0]
+                 and bias.is_contiguous() and bias.get_device() == x.get_device())
+            and (residual is None or residual.dtype is y.dtype and residual.shape == ys
+                 and residual.is_contiguous() and residual.get_device() == x.get_device())
+            and (z is None or z.dtype is _BF16 and z.dim() == 2 and z.shape[0] == xs[0]
+                 and z.shape[1] == ws[0] and z.is_contiguous()
+                 and z.get_device() == x.get_device())):
         (M, K), (wide, _) = _rows(x, "x"), _rows(w, "w")
         _choice(ACTIVATIONS, activation, "activation")
         N = wide
