@@ -1,6 +1,7 @@
 """Build libep_gb300.so in-tree for sm_103a (nvcc, one -gencode, TUs compiled
-in parallel, no cmake). ``python -m combine_movement_gb300.build`` or
-``build()``; skipped when the library is newer than every source."""
+in parallel, no cmake), and the binding's extension _calls.so (the C compiler).
+``python -m combine_movement_gb300.build`` or ``build()``; skipped when they are
+newer than every source."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -9,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_objs")
 LIB_PATH = os.path.join(PKG, "libep_gb300.so")
+CALLS_PATH = os.path.join(PKG, "_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "calls.c")
 
 GENCODE = "arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [
@@ -47,6 +51,25 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+def build_calls(force: bool = False) -> str:
+    """Build the binding's extension; returns its path."""
+    inputs = [CALLS_SOURCE, os.path.join(INCLUDE, "ep.h")]
+    if not force and os.path.exists(CALLS_PATH) and all(
+            os.path.getmtime(p) <= os.path.getmtime(CALLS_PATH) for p in inputs):
+        return CALLS_PATH
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        raise RuntimeError("no C compiler found for the binding's extension")
+    tmp = CALLS_PATH + ".tmp"
+    cmd = [cc, "-O2", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], CALLS_SOURCE, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
           out_dir: str | None = None) -> str:
     """Build the library; returns its path. With ``out_dir`` the objects and
@@ -55,6 +78,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     default library)."""
     lib_path = os.path.join(out_dir, "libep_gb300.so") if out_dir else LIB_PATH
     obj_dir = os.path.join(out_dir, "_objs") if out_dir else OBJ_DIR
+    if out_dir is None:
+        build_calls(force)
     if out_dir is None and not force and not is_stale():
         return LIB_PATH
     nvcc = _nvcc()

@@ -44,7 +44,7 @@ constexpr int kThreads = (kOutWarps + 2) * 32;
 constexpr int kChunk = 32;                   // columns turned around at a time
 constexpr uint32_t kTurnBytes = 32 * kChunk * 4;
 constexpr int kMaxStages = 8;
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 16;
 constexpr int kRowGroup = 8;                 // row tiles that share a column tile's turn
 // Blocks along k after which fp32 results take a tile's sums out of tensor memory.
 constexpr int kExactBlocks = 16;
@@ -262,7 +262,7 @@ __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t 
     constexpr int kCols = kGated ? S::kCols / 2 : S::kCols, kPieces = kCols / 4;
     constexpr int kStep = kOutWarps * 32 / kPieces;  // of this CTA's rows, by all threads
     constexpr int kMost = kRows / kParts / kStep;    // of them to a thread
-    constexpr int kAtOnce = kMost < 1 ? 1 : kMost < 8 / kParts ? kMost : 8 / kParts;
+    constexpr int kAtOnce = kMost < 1 || kParts >= 8 ? 1 : kMost < 8 / kParts ? kMost : 8 / kParts;
     const int64_t rows_left = a.m - tile.row0;
     const int rows = static_cast<int>(rows_left < kRows ? rows_left : kRows);
     const int own = (rows + kParts - 1 - rank) / kParts;
@@ -311,12 +311,14 @@ __device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t 
         write_shared_tile<kMode, kGated, 4>(a, sums, tile, rank);
     else if (a.split == 8)
         write_shared_tile<kMode, kGated, 8>(a, sums, tile, rank);
+    else if (kMode == kShared && a.split == 16)
+        write_shared_tile<kMode, kGated, 16>(a, sums, tile, rank);
 }
 
 // kExact: sums leave tensor memory every kExactBlocks blocks along k and are added
 // in registers (not of shared tiles, whose parts are added as they are joined).
 template <Mode kMode, bool kGated, bool kExact>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
     linear_kernel(const LinearArgs a, const __grid_constant__ Maps maps) {
     using S = Shape<kMode>;
     constexpr bool kClusters = kMode != kAlone;
@@ -672,17 +674,26 @@ bool encode_out(CUtensorMap* map, const LinearArgs& a) {
               CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// What a kernel's launches need beyond the defaults: its shared memory, and for narrow
+// shared tiles clusters of up to 16 CTAs.
+template <Mode kMode>
+cudaError_t allow(void (*kern)(LinearArgs, Maps)) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(Shape<kMode>::kSmem));
+    if (err != cudaSuccess || kMode != kShared) return err;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+
 template <Mode kMode, bool kGated, bool kExact>
 cudaError_t launch(const LinearArgs& a, const Maps& maps, int grid, int cluster, cudaStream_t stream) {
     auto kern = linear_kernel<kMode, kGated, kExact>;
     constexpr size_t kSmem = Shape<kMode>::kSmem;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(kSmem));
+    const cudaError_t err = allow<kMode>(kern);
     if (err != cudaSuccess) return err;
     return launch_dependent_clusters(kern, grid, cluster, kThreads, kSmem, stream, a, maps);
 }
 
-// Pairs, and clusters of 2, 4, 8 CTAs that share a tile, that a device holds at a
+// Pairs, and clusters of 2, 4, 8, 16 CTAs that share a tile (wide ones at most 8), that a device holds at a
 // time: fewer than SMs / size, because a cluster's lie in one part (GPC) of it.
 struct ResidentClusters {
     int pairs;
@@ -694,8 +705,7 @@ template <Mode kMode>
 cudaError_t count_clusters(int size, int* n) {
     auto kern = linear_kernel<kMode, false, false>;
     constexpr size_t kSmem = Shape<kMode>::kSmem;
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(kSmem));
+    const cudaError_t err = allow<kMode>(kern);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(size));
@@ -717,7 +727,7 @@ cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
         cudaError_t err = count_clusters<kPair>(2, &found->pairs);
         for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2)
             err = count_clusters<kShared>(split, &found->n[split]);
-        for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2)
+        for (int split = 2; err == cudaSuccess && split <= 8; split *= 2)
             err = count_clusters<kSharedWide>(split, &found->wide[split]);
         return err;
     });
@@ -754,7 +764,7 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, int device, int num_sms, b
         take(up(pairs, clusters.pairs) * a.k_blocks * kPairs + 3.0f, {kPair, 1, clusters.pairs});
     for (int n = 2; n <= kMaxSplit && n <= a.k_blocks; n *= 2) {
         if (narrow <= clusters.n[n]) take(up(a.k_blocks, n) * kNarrow + 2.5f, {kShared, n, 0});
-        if (wide <= clusters.wide[n]) take(up(a.k_blocks, n) * kWide + 5.0f, {kSharedWide, n, 0});
+        if (n <= 8 && wide <= clusters.wide[n]) take(up(a.k_blocks, n) * kWide + 5.0f, {kSharedWide, n, 0});
     }
     return cudaSuccess;
 }

@@ -156,6 +156,12 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+try:
+    from . import _calls
+except ImportError as e:
+    raise ImportError(f"the binding's extension _calls.so is not built ({e}); run "
+                      "`python -m combine_movement_gb300.build`") from e
+
 
 # --------------------------------------------------------------------------
 # marshalling helpers
@@ -177,6 +183,17 @@ def _ptr(t: Optional[torch.Tensor], dtype=None, what: str = "") -> Optional[int]
 # tensor first, so CUDA is initialised by the time this runs.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _cur_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _current_stream(device: int) -> int:
+    """The device's current stream, for the extension."""
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+    lib.ep_route, lib.ep_route_grad, lib.ep_linear, lib.ep_linear_act_grad,
+    lib.ep_linear_grad_input, lib.ep_linear_grad_weight)),
+    _BF16, _F32, _I32, torch.int64, _cur_device, _raw_stream or _current_stream)
 
 
 def _stream(stream) -> Optional[int]:
@@ -520,120 +537,92 @@ def _rows(t: torch.Tensor, what: str) -> Tuple[int, int]:
     return t.shape
 
 
-# A call's own expression says whether its arguments are as they have to be; only
-# where they are not are they looked at one by one, for what to say of them.
-# (The host's part of a small call is longer than the device's.)
-_KINDS = {_BF16: 0, _F32: 1}  # ep_type_t
+# The extension looks a call's arguments over and makes it. Where they are not
+# what the call takes (-1), they are looked at here one by one, for what to say of
+# them.
+def _made(code: int, name: str, look) -> None:
+    if code == EP_OK:
+        return
+    if code < 0:
+        look()
+        raise ValueError(f"{name}: arguments that it does not take")
+    raise EPError(code, name)
 
 
-def _status_ptr(status: Optional[torch.Tensor]) -> Optional[int]:
-    return None if status is None else _ptr(status, _I32, "status")
+def _handle(stream) -> Optional[int]:
+    return None if stream is None else _stream(stream) or 0
 
 
 def ep_route(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
              bias: Optional[torch.Tensor] = None, score: str = "softmax", groups: int = 1,
              topk_groups: int = 1, group_score: str = "max", renormalize: bool = True,
              scale: float = 1.0, stream=None) -> None:
-    shape, pairs = logits.shape, topk_idx.shape
-    kind, how, worth = _KINDS.get(logits.dtype), SCORES.get(score), GROUP_SCORES.get(group_score)
-    if not (len(shape) == 2 and len(pairs) == 2 and kind is not None and how is not None
-            and worth is not None and pairs[0] == shape[0] and topk_w.shape == pairs
-            and topk_idx.dtype is torch.int64 and topk_w.dtype is _F32 and logits.is_contiguous()
-            and topk_idx.is_contiguous() and topk_w.is_contiguous() and logits.is_cuda
-            and logits.get_device() == topk_idx.get_device() == topk_w.get_device() == _cur_device()
-            and (bias is None or bias.dtype is _F32 and bias.dim() == 1 and bias.shape[0] == shape[1]
-                 and bias.is_contiguous() and bias.get_device() == logits.get_device())):
-        (T, E), (_, K) = _rows(logits, "logits"), _rows(topk_idx, "topk_idx")
-        _type(logits, "logits")
-        _arg(logits, logits.dtype, (T, E), "logits")
-        _arg(topk_idx, torch.int64, (T, K), "topk_idx")
-        _arg(topk_w, _F32, (T, K), "topk_w")
-        if bias is not None:
-            _arg(bias, _F32, (E,), "bias")
-        _choice(SCORES, score, "score")
-        _choice(GROUP_SCORES, group_score, "group_score")
-        _on_gpu("ep_route", logits, topk_idx, topk_w, bias)
-    code = lib.ep_route(logits.data_ptr(), kind, shape[0], shape[1], pairs[1],
-                        None if bias is None else bias.data_ptr(), how, groups, topk_groups, worth,
-                        1 if renormalize else 0, scale, topk_idx.data_ptr(), topk_w.data_ptr(),
-                        _stream(stream))
-    if code != EP_OK:
-        raise EPError(code, "ep_route")
+    code = _calls.route(logits, topk_idx, topk_w, bias, SCORES.get(score, -1), groups, topk_groups,
+                        GROUP_SCORES.get(group_score, -1), renormalize, scale,
+                        _handle(stream))
+    if code:
+        def look():
+            (T, E), (_, K) = _rows(logits, "logits"), _rows(topk_idx, "topk_idx")
+            _type(logits, "logits")
+            _arg(logits, logits.dtype, (T, E), "logits")
+            _arg(topk_idx, torch.int64, (T, K), "topk_idx")
+            _arg(topk_w, _F32, (T, K), "topk_w")
+            if bias is not None:
+                _arg(bias, _F32, (E,), "bias")
+            _choice(SCORES, score, "score")
+            _choice(GROUP_SCORES, group_score, "group_score")
+            _on_gpu("ep_route", logits, topk_idx, topk_w, bias)
+        _made(code, "ep_route", look)
 
 
 def ep_route_grad(d_topk_w: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
                   d_logits: torch.Tensor, score: str = "softmax", renormalize: bool = True,
                   scale: float = 1.0, status: Optional[torch.Tensor] = None, stream=None) -> None:
-    shape, pairs, dtype = logits.shape, topk_idx.shape, logits.dtype
-    kind, how = _KINDS.get(dtype), SCORES.get(score)
-    if not (len(shape) == 2 and len(pairs) == 2 and kind is not None and how is not None
-            and pairs[0] == shape[0] and d_topk_w.shape == pairs and d_logits.shape == shape
-            and topk_idx.dtype is torch.int64 and d_topk_w.dtype is _F32 and d_logits.dtype is dtype
-            and logits.is_contiguous() and topk_idx.is_contiguous() and d_topk_w.is_contiguous()
-            and d_logits.is_contiguous() and logits.is_cuda
-            and logits.get_device() == topk_idx.get_device() == d_topk_w.get_device()
-            == d_logits.get_device() == _cur_device()):
-        (T, E), (_, K) = _rows(logits, "logits"), _rows(topk_idx, "topk_idx")
-        _type(logits, "logits")
-        _arg(logits, dtype, (T, E), "logits")
-        _arg(d_topk_w, _F32, (T, K), "d_topk_w")
-        _arg(topk_idx, torch.int64, (T, K), "topk_idx")
-        _arg(d_logits, dtype, (T, E), "d_logits")
-        _choice(SCORES, score, "score")
-        _on_gpu("ep_route_grad", d_topk_w, logits, topk_idx, d_logits)
-    if status is not None:
-        _on_gpu("ep_route_grad", status)
-    code = lib.ep_route_grad(d_topk_w.data_ptr(), logits.data_ptr(), kind, topk_idx.data_ptr(),
-                             shape[0], shape[1], pairs[1], how, 1 if renormalize else 0, scale,
-                             d_logits.data_ptr(), _status_ptr(status), _stream(stream))
-    if code != EP_OK:
-        raise EPError(code, "ep_route_grad")
+    code = _calls.route_grad(d_topk_w, logits, topk_idx, d_logits, SCORES.get(score, -1),
+                             renormalize, scale, status,
+                             _handle(stream))
+    if code:
+        def look():
+            (T, E), (_, K) = _rows(logits, "logits"), _rows(topk_idx, "topk_idx")
+            _type(logits, "logits")
+            _arg(logits, logits.dtype, (T, E), "logits")
+            _arg(d_topk_w, _F32, (T, K), "d_topk_w")
+            _arg(topk_idx, torch.int64, (T, K), "topk_idx")
+            _arg(d_logits, logits.dtype, (T, E), "d_logits")
+            _choice(SCORES, score, "score")
+            _ptr(status, _I32, "status")
+            _on_gpu("ep_route_grad", d_topk_w, logits, topk_idx, d_logits, status)
+        _made(code, "ep_route_grad", look)
 
 
 def ep_linear(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor,
               bias: Optional[torch.Tensor] = None, activation: str = "none",
               residual: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
               status: Optional[torch.Tensor] = None, stream=None) -> None:
-    xs, ws, ys = x.shape, w.shape, y.shape
-    act, kind = ACTIVATIONS.get(activation), _KINDS.get(y.dtype)
-    if not (len(xs) == 2 and len(ws) == 2 and len(ys) == 2 and act is not None and kind is not None
-            and xs[1] == ws[1] and ys[0] == xs[0] and ws[0] == (2 * ys[1] if act == 4 else ys[1])
-            and x.dtype is _BF16 and w.dtype is _BF16 and x.is_contiguous() and w.is_contiguous()
-            and y.is_contiguous() and x.is_cuda
-            and x.get_device() == w.get_device() == y.get_device() == _cur_device()
-            and (bias is None or bias.dtype is _F32 and bias.dim() == 1 and bias.shape[0] == ws[0]
-                 and bias.is_contiguous() and bias.get_device() == x.get_device())
-            and (residual is None or residual.dtype is y.dtype and residual.shape == ys
-                 and residual.is_contiguous() and residual.get_device() == x.get_device())
-            and (z is None or z.dtype is _BF16 and z.dim() == 2 and z.shape[0] == xs[0]
-                 and z.shape[1] == ws[0] and z.is_contiguous()
-                 and z.get_device() == x.get_device())):
-        (M, K), (wide, _) = _rows(x, "x"), _rows(w, "w")
-        _choice(ACTIVATIONS, activation, "activation")
-        N = wide
-        if activation == "swiglu":
-            if wide % 2:
-                raise ValueError(f"w: expected a gate half and an up half, got {wide} rows")
-            N = wide // 2
-        _type(y, "y")
-        _arg(x, _BF16, (M, K), "x")
-        _arg(w, _BF16, (wide, K), "w")
-        _arg(y, y.dtype, (M, N), "y")
-        if bias is not None:
-            _arg(bias, _F32, (wide,), "bias")
-        if residual is not None:
-            _arg(residual, y.dtype, (M, N), "residual")
-        if z is not None:
-            _arg(z, _BF16, (M, wide), "z")
-        _on_gpu("ep_linear", x, w, y, bias, residual, z)
-    if status is not None:
-        _on_gpu("ep_linear", status)
-    code = lib.ep_linear(x.data_ptr(), xs[0], xs[1], w.data_ptr(), ys[1],
-                         None if bias is None else bias.data_ptr(), act,
-                         None if residual is None else residual.data_ptr(), kind, y.data_ptr(),
-                         None if z is None else z.data_ptr(), _status_ptr(status), _stream(stream))
-    if code != EP_OK:
-        raise EPError(code, "ep_linear")
+    code = _calls.linear(x, w, y, bias, ACTIVATIONS.get(activation, -1), residual, z, status,
+                         _handle(stream))
+    if code:
+        def look():
+            (M, K), (wide, _) = _rows(x, "x"), _rows(w, "w")
+            _choice(ACTIVATIONS, activation, "activation")
+            N = wide
+            if activation == "swiglu":
+                if wide % 2:
+                    raise ValueError(f"w: expected a gate half and an up half, got {wide} rows")
+                N = wide // 2
+            _type(y, "y")
+            _arg(x, _BF16, (M, K), "x")
+            _arg(w, _BF16, (wide, K), "w")
+            _arg(y, y.dtype, (M, N), "y")
+            if bias is not None:
+                _arg(bias, _F32, (wide,), "bias")
+            if residual is not None:
+                _arg(residual, y.dtype, (M, N), "residual")
+            if z is not None:
+                _arg(z, _BF16, (M, wide), "z")
+            _ptr(status, _I32, "status")
+            _on_gpu("ep_linear", x, w, y, bias, residual, z, status)
+        _made(code, "ep_linear", look)
 
 
 def linear_pitch(n: int) -> int:
@@ -645,66 +634,56 @@ def ep_linear_act_grad(dy: torch.Tensor, z: Optional[torch.Tensor], dz: Optional
                        d_bias: Optional[torch.Tensor] = None, activation: str = "none",
                        stream=None) -> None:
     """z may be None without an activation; dz is [M, linear_pitch(rows of w)]."""
-    M, N = _rows(dy, "dy")
-    act = _choice(ACTIVATIONS, activation, "activation")
-    wide, kind = 2 * N if act == 4 else N, _type(dy, "dy")
-    pitch = linear_pitch(wide)
-    if z is None and act != 0:
-        raise ValueError("z: expected a tensor")
-    pd = _arg(dy, dy.dtype, (M, N), "dy")
-    pz = None if z is None else _arg(z, _BF16, (M, wide), "z")
-    po = None if dz is None else _arg(dz, _BF16, (M, pitch), "dz")
-    pb = None if d_bias is None else _arg(d_bias, _F32, (wide,), "d_bias")
-    _on_gpu("ep_linear_act_grad", dy, z, dz, d_bias)
-    code = lib.ep_linear_act_grad(pd, kind, pz, M, N, act, po, pitch, pb, _stream(stream))
-    if code != EP_OK:
-        raise EPError(code, "ep_linear_act_grad")
+    code = _calls.act_grad(dy, z, dz, d_bias, ACTIVATIONS.get(activation, -1),
+                           _handle(stream))
+    if code:
+        def look():
+            M, N = _rows(dy, "dy")
+            wide = 2 * N if activation == "swiglu" else N
+            _choice(ACTIVATIONS, activation, "activation")
+            _type(dy, "dy")
+            if z is None and activation != "none":
+                raise ValueError("z: expected a tensor")
+            _arg(dy, dy.dtype, (M, N), "dy")
+            if z is not None:
+                _arg(z, _BF16, (M, wide), "z")
+            if dz is not None:
+                _arg(dz, _BF16, (M, linear_pitch(wide)), "dz")
+            if d_bias is not None:
+                _arg(d_bias, _F32, (wide,), "d_bias")
+            _on_gpu("ep_linear_act_grad", dy, z, dz, d_bias)
+        _made(code, "ep_linear_act_grad", look)
 
 
 def ep_linear_grad_input(dz: torch.Tensor, w: torch.Tensor, dx: torch.Tensor,
                          status: Optional[torch.Tensor] = None, stream=None) -> None:
-    ds, ws, xs = dz.shape, w.shape, dx.shape
-    if not (len(ds) == 2 and len(ws) == 2 and len(xs) == 2 and ds[1] == -(-ws[0] // 8) * 8
-            and xs[0] == ds[0] and xs[1] == ws[1] and dz.dtype is _BF16 and w.dtype is _BF16
-            and dx.dtype is _BF16 and dz.is_contiguous() and w.is_contiguous()
-            and dx.is_contiguous() and dz.is_cuda
-            and dz.get_device() == w.get_device() == dx.get_device() == _cur_device()):
-        (M, _), (N, K) = _rows(dz, "dz"), _rows(w, "w")
-        _arg(dz, _BF16, (M, linear_pitch(N)), "dz")
-        _arg(w, _BF16, (N, K), "w")
-        _arg(dx, _BF16, (M, K), "dx")
-        _on_gpu("ep_linear_grad_input", dz, w, dx)
-    if status is not None:
-        _on_gpu("ep_linear_grad_input", status)
-    code = lib.ep_linear_grad_input(dz.data_ptr(), ds[1], ds[0], ws[0], w.data_ptr(), ws[1],
-                                    dx.data_ptr(), _status_ptr(status), _stream(stream))
-    if code != EP_OK:
-        raise EPError(code, "ep_linear_grad_input")
+    code = _calls.grad_input(dz, w, dx, status, _handle(stream))
+    if code:
+        def look():
+            (M, _), (N, K) = _rows(dz, "dz"), _rows(w, "w")
+            _arg(dz, _BF16, (M, linear_pitch(N)), "dz")
+            _arg(w, _BF16, (N, K), "w")
+            _arg(dx, _BF16, (M, K), "dx")
+            _ptr(status, _I32, "status")
+            _on_gpu("ep_linear_grad_input", dz, w, dx, status)
+        _made(code, "ep_linear_grad_input", look)
 
 
 def ep_linear_grad_weight(dz: torch.Tensor, x: torch.Tensor, d_w: torch.Tensor,
                           accumulate: bool = False, status: Optional[torch.Tensor] = None,
                           stream=None) -> None:
-    ds, xs, ws = dz.shape, x.shape, d_w.shape
-    kind = _KINDS.get(d_w.dtype)
-    if not (len(ds) == 2 and len(xs) == 2 and len(ws) == 2 and ds[1] == -(-ws[0] // 8) * 8
-            and xs[0] == ds[0] and xs[1] == ws[1] and dz.dtype is _BF16 and x.dtype is _BF16
-            and kind is not None and dz.is_contiguous() and x.is_contiguous()
-            and d_w.is_contiguous() and dz.is_cuda
-            and dz.get_device() == x.get_device() == d_w.get_device() == _cur_device()):
-        (M, _), (N, K) = _rows(dz, "dz"), _rows(d_w, "d_w")
-        _type(d_w, "d_w")
-        _arg(dz, _BF16, (M, linear_pitch(N)), "dz")
-        _arg(x, _BF16, (M, K), "x")
-        _arg(d_w, d_w.dtype, (N, K), "d_w")
-        _on_gpu("ep_linear_grad_weight", dz, x, d_w)
-    if status is not None:
-        _on_gpu("ep_linear_grad_weight", status)
-    code = lib.ep_linear_grad_weight(dz.data_ptr(), ds[1], ds[0], ws[0], x.data_ptr(), ws[1], kind,
-                                     d_w.data_ptr(), 1 if accumulate else 0, _status_ptr(status),
-                                     _stream(stream))
-    if code != EP_OK:
-        raise EPError(code, "ep_linear_grad_weight")
+    code = _calls.grad_weight(dz, x, d_w, accumulate, status,
+                              _handle(stream))
+    if code:
+        def look():
+            (M, _), (N, K) = _rows(dz, "dz"), _rows(d_w, "d_w")
+            _type(d_w, "d_w")
+            _arg(dz, _BF16, (M, linear_pitch(N)), "dz")
+            _arg(x, _BF16, (M, K), "x")
+            _arg(d_w, d_w.dtype, (N, K), "d_w")
+            _ptr(status, _I32, "status")
+            _on_gpu("ep_linear_grad_weight", dz, x, d_w, status)
+        _made(code, "ep_linear_grad_weight", look)
 
 
 def ep_sm_partition(num_sms: int) -> Tuple[int, Optional[int], int, int]:

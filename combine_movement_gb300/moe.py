@@ -16,8 +16,8 @@ linear(x, gate_up, activation="swiglu"), linear(h, down, residual=y) adds it to
 combine's y. Both are differentiable.
 
 ``python -m combine_movement_gb300.moe`` builds a layer with random weights,
-runs a batch through it, compares some tokens with the layer in fp32 and
-prints the time of each call as one JSON line.
+runs a batch through it and through a router and a shared expert, compares some
+tokens with the layer in fp32 and prints the time of each call as one JSON line.
 """
 from __future__ import annotations
 
@@ -266,12 +266,14 @@ class _Linear(torch.autograd.Function):
         dy, wide, act = dy.contiguous(), ctx.wide, ctx.activation
         M = dy.shape[0]
         dx = d_w = d_bias = None
-        dz = dy
+        dz = dy  # where it is what the products take
         if act != "none" or dy.dtype is not torch.bfloat16 or wide % 8:
-            dz = dy.new_empty((M, ep.linear_pitch(wide)), dtype=torch.bfloat16)
+            dz = None
+            if need_x or need_w:
+                dz = dy.new_empty((M, ep.linear_pitch(wide)), dtype=torch.bfloat16)
         if need_bias:
             d_bias = dy.new_empty(wide, dtype=torch.float32)
-        if (need_x or need_w) and dz is not dy or need_bias:
+        if need_bias or dz is not dy and dz is not None:
             ep.ep_linear_act_grad(dy, z, None if dz is dy else dz, d_bias, act)
         if need_x:
             dx = dz.new_empty((M, w.shape[1]))
@@ -348,6 +350,30 @@ def _main() -> None:
         "combine": lambda: ep.ep_combine(out, slot, w, y),
         "layer": lambda: forward_fp8(x, idx, w, *gate_up, *down),
     }
+
+    # the router of this layer, and a shared expert of the same width
+    def dense(n, k):
+        return torch.randn((n, k), generator=g, device=dev, dtype=torch.bfloat16) * k ** -0.5
+
+    gate, s13, s2 = dense(wl.E, wl.H), dense(2 * args.width, wl.H), dense(wl.H, args.width)
+    logits = ep.linear(x, gate, out_dtype=torch.float32, status=status)
+    own_idx, own_w = ep.route(logits, wl.K, score="sigmoid")
+    hidden = ep.linear(x, s13, activation="swiglu", status=status)
+    y_all = ep.linear(hidden, s2, residual=y, status=status)
+    assert ep.ep_get_status(status) == ep.EP_OK
+    assert torch.equal(own_idx, logits.sort(dim=1, descending=True, stable=True).indices[:, :wl.K])
+    worst_shared = 0.0
+    for t in tokens:
+        gu = s13.float() @ x[t].float()
+        want = s2.float() @ (torch.nn.functional.silu(gu[:args.width]) * gu[args.width:])
+        worst_shared = max(worst_shared, float((y_all[t].float() - y[t].float() - want).norm()
+                                               / want.norm()))
+    calls.update({
+        "router_logits": lambda: ep.ep_linear(x, gate, logits),
+        "route": lambda: ep.ep_route(logits, own_idx, own_w, score="sigmoid"),
+        "shared_gate_up": lambda: ep.ep_linear(x, s13, hidden, activation="swiglu"),
+        "shared_down": lambda: ep.ep_linear(hidden, s2, y_all, residual=y),
+    })
     us = {}
     for name, call in calls.items():
         for _ in range(3):
@@ -361,7 +387,8 @@ def _main() -> None:
         us[name] = round(begin.elapsed_time(end) / args.steps * 1e3, 2)
     print(json.dumps({"workload": wl.name, "T": T, "H": wl.H, "E": wl.E, "K": K,
                       "width": args.width, "us": us,
-                      "relative_error_against_fp32": round(worst, 4)}))
+                      "relative_error_against_fp32": round(worst, 4),
+                      "shared_relative_error_against_fp32": round(worst_shared, 4)}))
 
 
 if __name__ == "__main__":
