@@ -339,8 +339,8 @@ struct LinearArgs {
 // `partition`: num_sms are those of an SM partition, not the device's.
 cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_t stream);
 
-// The same for at most kFewRows rows, both operands along k (linear_few.cu).
-constexpr int kFewRows = 4;
+// The same for a token or a few, where that is faster (linear_few.cu).
+bool linear_few_takes(const LinearArgs& a);
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t stream);
 
 // dz = dy act'(z) and its column sums (linear_grad.cu).

@@ -28,9 +28,10 @@ namespace ep {
 namespace {
 
 // Who works on a tile: a CTA alone or the CTAs of a cluster that share its blocks
-// along k, on 128 x 64 (gated: 32 columns of each half; kSharedWide 128 x 256), or a
-// pair of CTAs on 256 x 256 (gated: 128 of each half), 128 rows and half of b each.
-enum Mode { kAlone, kShared, kSharedWide, kPair };
+// along k, on 128 x 64 (gated: 32 columns of each half; kSharedMid 128 x 128, kSharedWide
+// 128 x 256), or a pair of CTAs on 256 x 256 (gated: 128 of each half), 128 rows and
+// half of b each.
+enum Mode { kAlone, kShared, kSharedMid, kSharedWide, kPair };
 
 constexpr int kRows = 128;                   // of the output, in one CTA
 constexpr int kTileK = 64;                   // values of one stage along k
@@ -51,8 +52,9 @@ constexpr int kExactBlocks = 16;
 
 template <Mode kMode>
 struct Shape {
-    static constexpr bool kParts = kMode == kShared || kMode == kSharedWide;
-    static constexpr int kCols = kMode == kPair || kMode == kSharedWide ? 256 : 64;  // of the tile
+    static constexpr bool kParts = kMode == kShared || kMode == kSharedMid || kMode == kSharedWide;
+    static constexpr int kCols =                                  // of the tile
+        kMode == kPair || kMode == kSharedWide ? 256 : kMode == kSharedMid ? 128 : 64;
     static constexpr int kTileRows = kMode == kPair ? 2 * kRows : kRows;
     static constexpr int kOwnB = kMode == kPair ? kCols / 2 : kCols;  // rows of b in one CTA
     static constexpr uint32_t kStageBytes = kStageA + kOwnB * kRowBytes;
@@ -698,6 +700,7 @@ cudaError_t launch(const LinearArgs& a, const Maps& maps, int grid, int cluster,
 struct ResidentClusters {
     int pairs;
     int n[kMaxSplit + 1];
+    int mid[kMaxSplit + 1];
     int wide[kMaxSplit + 1];
 };
 
@@ -728,6 +731,8 @@ cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
         for (int split = 2; err == cudaSuccess && split <= kMaxSplit; split *= 2)
             err = count_clusters<kShared>(split, &found->n[split]);
         for (int split = 2; err == cudaSuccess && split <= 8; split *= 2)
+            err = count_clusters<kSharedMid>(split, &found->mid[split]);
+        for (int split = 2; err == cudaSuccess && split <= 8; split *= 2)
             err = count_clusters<kSharedWide>(split, &found->wide[split]);
         return err;
     });
@@ -736,16 +741,20 @@ cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
 int64_t up(int64_t v, int64_t by) { return (v + by - 1) / by; }
 
 // Who works on a tile, and how many CTAs share one: what takes least by the
-// times measured for a block along k (an SM takes in about 120 GB/s from L2: 24 KB of
-// a narrow tile, 48 KB of a wide one; a pair's products fill its time) and
-// for the joining of shared tiles' parts. A partition's SMs may not hold a cluster.
+// times measured for a block along k (an SM takes in 122 GB/s: 24 KB of a narrow
+// tile 0.2 us, 48 KB of a wide one 0.4; a stage's latency where few rows make for few
+// bytes; a pair's products 0.27) and for what comes after them. A partition's SMs may
+// not hold a cluster.
+constexpr float kInBytes = 122e3f;   // to an SM, a microsecond
+constexpr float kLatency = 1.0f;     // us, from asking for a stage to its product
+constexpr float kPairBlock = 0.27f;  // us
 struct Plan {
     Mode mode;
     int split;
     int clusters;  // pairs at a time
 };
-cudaError_t plan_for(const LinearArgs& a, bool gated, int device, int num_sms, bool partition,
-                     Plan* plan) {
+cudaError_t plan_for(const LinearArgs& a, bool gated, bool plain, int a_rows, int device,
+                     int num_sms, bool partition, Plan* plan) {
     *plan = {kAlone, 1, 0};
     if (partition) return cudaSuccess;
     ResidentClusters clusters{};
@@ -753,18 +762,27 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, int device, int num_sms, b
     if (err != cudaSuccess) return err;
     const int half = gated ? 2 : 1;
     const int64_t pairs = up(a.m, Shape<kPair>::kTileRows) * up(a.n, Shape<kPair>::kCols / half);
-    const int64_t narrow = up(a.m, kRows) * up(a.n, Shape<kAlone>::kCols / half);
-    const int64_t wide = up(a.m, kRows) * up(a.n, Shape<kSharedWide>::kCols / half);
-    constexpr float kNarrow = 0.19f, kWide = 0.38f, kPairs = 0.27f;  // us a block
-    float best = up(narrow, num_sms) * (a.k_blocks * kNarrow + 0.5f);
+    auto tiles = [&](int cols) { return up(a.m, kRows) * up(a.n, cols / half); };
+    const int64_t narrow = tiles(64), mid = tiles(128), wide = tiles(256);
+    const float a_bytes = a.a_by_k ? (a.m > 64 ? 2 : 1) * kGroupBytes : a_rows * kRowBytes;
+    auto block = [&](int cols, int stages) {
+        return fmaxf((a_bytes + cols * kRowBytes) / kInBytes, kLatency / stages);
+    };
+    // a tile takes its products' time, or its results' where those take longer
+    const float alone_tile = fmaxf(a.k_blocks * block(64, Shape<kAlone>::kStages), plain ? 0.6f : 1.2f);
+    const float pair_tile = fmaxf(a.k_blocks * kPairBlock, plain ? 2.2f : 4.0f);
+    float best = up(narrow, num_sms) * (alone_tile + 0.3f) + (plain ? 0.2f : 1.2f);
     auto take = [&](float time, Plan p) {
         if (time < best) best = time, *plan = p;
     };
     if (clusters.pairs > 0)
-        take(up(pairs, clusters.pairs) * a.k_blocks * kPairs + 3.0f, {kPair, 1, clusters.pairs});
+        take(up(pairs, clusters.pairs) * pair_tile + 3.0f, {kPair, 1, clusters.pairs});
     for (int n = 2; n <= kMaxSplit && n <= a.k_blocks; n *= 2) {
-        if (narrow <= clusters.n[n]) take(up(a.k_blocks, n) * kNarrow + 2.5f, {kShared, n, 0});
-        if (n <= 8 && wide <= clusters.wide[n]) take(up(a.k_blocks, n) * kWide + 5.0f, {kSharedWide, n, 0});
+        const int64_t blocks = up(a.k_blocks, n);
+        if (narrow <= clusters.n[n]) take(blocks * block(64, Shape<kShared>::kStages) + 2.5f, {kShared, n, 0});
+        if (n > 8) continue;
+        if (mid <= clusters.mid[n]) take(blocks * block(128, Shape<kSharedMid>::kStages) + 3.3f, {kSharedMid, n, 0});
+        if (wide <= clusters.wide[n]) take(blocks * block(256, Shape<kSharedWide>::kStages) + 5.0f, {kSharedWide, n, 0});
     }
     return cudaSuccess;
 }
@@ -774,29 +792,31 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, int device, int num_sms, b
 cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_t stream) {
     const bool gated = a.act == EP_ACT_SWIGLU;
     const int half = gated ? 2 : 1;
-    if (!a.a_by_k && !a.b_by_k && a.m <= kFewRows) return launch_linear_few(a, stream);
+    if (linear_few_takes(a)) return launch_linear_few(a, stream);
     int device = 0;
     cudaError_t err = cudaGetDevice(&device);
     a.k_blocks = static_cast<int>(up(a.k, kTileK));
+    int a_rows = 16;  // of a's box along k: no more than there are
+    while (a_rows < kRows && a_rows < a.m) a_rows *= 2;
+    const bool plain = a.act == EP_ACT_NONE && a.bias == nullptr && a.z == nullptr &&
+                       a.residual == nullptr && a.n % (a.out_f32 ? 4 : 8) == 0;
     Plan plan{};
-    if (err == cudaSuccess) err = plan_for(a, gated, device, num_sms, partition, &plan);
+    if (err == cudaSuccess) err = plan_for(a, gated, plain, a_rows, device, num_sms, partition, &plan);
     if (err != cudaSuccess) return err;
     const bool pair = plan.mode == kPair;
-    const int cols = pair || plan.mode == kSharedWide ? Shape<kPair>::kCols : Shape<kAlone>::kCols;
+    const int cols = pair || plan.mode == kSharedWide ? 256 : plan.mode == kSharedMid ? 128 : 64;
     a.split = plan.split;
     a.row_tiles = up(a.m, pair ? Shape<kPair>::kTileRows : kRows);
     a.col_tiles = up(a.n, cols / half);
     Maps maps;
-    maps.a_rows = 16;  // no more than there are
-    while (maps.a_rows < kRows && (pair || maps.a_rows < a.m)) maps.a_rows *= 2;
+    maps.a_rows = pair ? kRows : a_rows;
     const int64_t b_rows = half * a.n;
     const bool ok =
         (a.a_by_k ? encode_map(&maps.a, a.a, a.k, a.m, a.a_pitch, kTileK)
                   : encode_map(&maps.a, a.a, a.m, a.k, a.a_pitch, maps.a_rows)) &&
         (a.b_by_k ? encode_map(&maps.b, a.b, a.k, b_rows, a.b_pitch, kTileK)
                   : encode_map(&maps.b, a.b, b_rows, a.k, a.b_pitch, cols / 2));
-    maps.plain = a.act == EP_ACT_NONE && a.bias == nullptr && a.z == nullptr && a.residual == nullptr &&
-                 a.n % (a.out_f32 ? 4 : 8) == 0 && (pair || plan.mode == kAlone);
+    maps.plain = plain && (pair || plan.mode == kAlone);
     if (!ok || (maps.plain && !encode_out(&maps.out, a))) return cudaErrorInvalidValue;
     const int64_t tiles = a.row_tiles * a.col_tiles;
     const bool exact = a.out_f32 && a.k_blocks > kExactBlocks;
@@ -807,6 +827,11 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
                          : launch<kPair, false, true>(a, maps, grid, 2, stream);
         return gated ? launch<kPair, true, false>(a, maps, grid, 2, stream)
                      : launch<kPair, false, false>(a, maps, grid, 2, stream);
+    }
+    if (plan.mode == kSharedMid) {
+        const int grid = static_cast<int>(tiles) * a.split;
+        return gated ? launch<kSharedMid, true, false>(a, maps, grid, a.split, stream)
+                     : launch<kSharedMid, false, false>(a, maps, grid, a.split, stream);
     }
     if (plan.mode == kSharedWide) {
         const int grid = static_cast<int>(tiles) * a.split;
