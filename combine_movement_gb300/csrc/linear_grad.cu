@@ -52,7 +52,7 @@ __device__ __forceinline__ Raw<W> load_row(const void* p, bool f32, int64_t at) 
     }
     const uint16_t* q = static_cast<const uint16_t*>(p) + at;
     if constexpr (W == 1) {
-        r.bits[0] = static_cast<uint32_t>(__ldg(q)) << 16;
+        r.bits[0] = __ldg(q);  // (shifted where it is used: here it would wait for the load)
     } else if constexpr (W == 4) {
         const uint2 f = __ldg(reinterpret_cast<const uint2*>(q));
         r.bits[0] = f.x, r.bits[1] = f.y;
@@ -65,7 +65,8 @@ __device__ __forceinline__ Raw<W> load_row(const void* p, bool f32, int64_t at) 
 // Value i of them.
 template <int W>
 __device__ __forceinline__ float value(const Raw<W>& r, bool f32, int i) {
-    if (W == 1 || f32) return __uint_as_float(r.bits[i]);
+    if (f32) return __uint_as_float(r.bits[i]);
+    if (W == 1) return __uint_as_float(r.bits[0] << 16);
     return __uint_as_float(i % 2 == 0 ? r.bits[i / 2] << 16 : r.bits[i / 2] & 0xFFFF0000u);
 }
 template <int W>
@@ -80,10 +81,11 @@ __device__ __forceinline__ void store_row(uint16_t* q, const float (&v)[W]) {
 }
 
 // W columns to a thread, kLanes threads to a row's part.
-template <int W, int kLanes, bool kGated, bool kF32>
-__global__ void __launch_bounds__(kThreads, 2) act_grad_kernel(const ActGradArgs a) {
+// kSums: d_bias is asked for.
+template <int W, int kLanes, bool kGated, bool kF32, bool kSums>
+__global__ void __launch_bounds__(kThreads, kSums ? 2 : 3) act_grad_kernel(const ActGradArgs a) {
     constexpr int kHalves = kGated ? 2 : 1, kRows = kThreads / kLanes, kCols = W * kLanes;
-    constexpr int kAtOnce = W == 8 ? 2 : 4;  // rows whose loads are in flight
+    constexpr int kAtOnce = W == 8 ? (kGated || kF32 ? 2 : 4) : W == 4 ? 4 : 16;  // rows whose loads are in flight
     __shared__ float part[kThreads / 32][kHalves][kCols];
     __shared__ float total[kHalves][kCols];
     griddep_wait();
@@ -100,67 +102,78 @@ __global__ void __launch_bounds__(kThreads, 2) act_grad_kernel(const ActGradArgs
         Raw<W> dy[kAtOnce], z[kAtOnce], zu[kAtOnce];
 #pragma unroll
         for (int j = 0; j < kAtOnce; ++j) {
-            const int64_t r = r0 + j * step;
-            if (r >= a.m) continue;
+            const int64_t r = min(r0 + j * step, a.m - 1);  // (rows past the last: it again)
             dy[j] = load_row<W>(a.dy, kF32, r * a.n + col);
             if (a.act != EP_ACT_NONE) z[j] = load_row<W>(a.z, false, r * wide + col);
             if (kGated) zu[j] = load_row<W>(a.z, false, r * wide + a.n + col);
         }
+        // (what the activation is, is asked once for all of them)
+        auto each = [&](auto slope) {
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const int64_t r = r0 + j * step;
-            if (r >= a.m) continue;
-            float g[W], u[W];
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int64_t r = r0 + j * step;
+                if (r >= a.m) continue;
+                float g[W], u[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const float d = value<W>(dy[j], kF32, i), v = value<W>(z[j], false, i);
+                    if (kGated) {
+                        u[i] = d * silu(v);
+                        g[i] = d * value<W>(zu[j], false, i) * silu_slope(v);
+                        if (kSums) sum[kHalves - 1][i] += u[i];
+                    } else {
+                        g[i] = slope(d, v);
+                    }
+                    if (kSums) sum[0][i] += g[i];
+                }
+                if (a.dz != nullptr) {
+                    store_row<W>(a.dz + r * a.pitch + col, g);
+                    if (kGated) store_row<W>(a.dz + r * a.pitch + a.n + col, u);
+                }
+            }
+        };
+        if (kGated || a.act == EP_ACT_NONE)
+            each([](float d, float) { return d; });
+        else if (a.act == EP_ACT_RELU)
+            each([](float d, float v) { return d * activate_slope(v, EP_ACT_RELU); });
+        else if (a.act == EP_ACT_GELU)
+            each([](float d, float v) { return d * activate_slope(v, EP_ACT_GELU); });
+        else
+            each([](float d, float v) { return d * activate_slope(v, EP_ACT_SILU); });
+    }
+    if constexpr (kSums) {
+        // over the warp's rows, then the CTA's warps, then the cluster's CTAs
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                const float d = value<W>(dy[j], kF32, i), v = value<W>(z[j], false, i);
-                if (kGated) {
-                    u[i] = d * silu(v);
-                    g[i] = d * value<W>(zu[j], false, i) * silu_slope(v);
-                    sum[kHalves - 1][i] += u[i];
-                } else {
-                    g[i] = a.act == EP_ACT_NONE ? d : d * activate_slope(v, a.act);
-                }
-                sum[0][i] += g[i];
+#pragma unroll
+                for (int d = kLanes; d < 32; d <<= 1)
+                    sum[h][i] += __shfl_xor_sync(kFullMask, sum[h][i], d);
+                if (lane < kLanes) part[warp][h][cl * W + i] = sum[h][i];
             }
-            if (a.dz != nullptr) {
-                store_row<W>(a.dz + r * a.pitch + col, g);
-                if (kGated) store_row<W>(a.dz + r * a.pitch + a.n + col, u);
-            }
-        }
-    }
-    if (a.d_bias == nullptr) return;
-    // over the warp's rows, then the CTA's warps, then the cluster's CTAs
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-#pragma unroll
-            for (int d = kLanes; d < 32; d <<= 1)
-                sum[h][i] += __shfl_xor_sync(kFullMask, sum[h][i], d);
-            if (lane < kLanes) part[warp][h][cl * W + i] = sum[h][i];
-        }
-    __syncthreads();
-    for (int i = threadIdx.x; i < kHalves * kCols; i += kThreads) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) s += part[w][i / kCols][i % kCols];
-        total[i / kCols][i % kCols] = s;
-    }
-    cluster_arrive();
-    cluster_wait();
-    if (cluster_rank() == 0) {
+        __syncthreads();
         for (int i = threadIdx.x; i < kHalves * kCols; i += kThreads) {
-            const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + i % kCols;
-            if (c >= a.n) continue;
             float s = 0.0f;
-            for (uint32_t p = 0; p < gridDim.x; ++p)
-                s += load_cluster_f32(cluster_map(smem_u32(&total[i / kCols][i % kCols]), p));
-            a.d_bias[i / kCols * a.n + c] = s;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) s += part[w][i / kCols][i % kCols];
+            total[i / kCols][i % kCols] = s;
         }
+        cluster_arrive();
+        cluster_wait();
+        if (cluster_rank() == 0) {
+            for (int i = threadIdx.x; i < kHalves * kCols; i += kThreads) {
+                const int64_t c = static_cast<int64_t>(blockIdx.y) * kCols + i % kCols;
+                if (c >= a.n) continue;
+                float s = 0.0f;
+                for (uint32_t p = 0; p < gridDim.x; ++p)
+                    s += load_cluster_f32(cluster_map(smem_u32(&total[i / kCols][i % kCols]), p));
+                a.d_bias[i / kCols * a.n + c] = s;
+            }
+        }
+        cluster_arrive();
+        cluster_wait();  // no CTA reads this one's sums any more
     }
-    cluster_arrive();
-    cluster_wait();  // no CTA reads this one's sums any more
 }
 
 template <int W, int kLanes, bool kGated, bool kF32>
@@ -191,7 +204,9 @@ cudaError_t launch(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, act_grad_kernel<W, kLanes, kGated, kF32>, a);
+    if (a.d_bias == nullptr)
+        return cudaLaunchKernelEx(&cfg, act_grad_kernel<W, kLanes, kGated, kF32, false>, a);
+    return cudaLaunchKernelEx(&cfg, act_grad_kernel<W, kLanes, kGated, kF32, true>, a);
 }
 
 // Strips of a quarter of the columns where the clusters of whole ones leave SMs

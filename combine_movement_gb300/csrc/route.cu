@@ -109,16 +109,18 @@ __device__ __forceinline__ void load_part(const void* p, bool bf16, int64_t at, 
             }
         }
     } else {
+        // all loads, then what is made of them: a branch or a shift between them would
+        // wait for each (the last expert again in the place of those past it)
+        uint32_t w[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            v[j] = past;
-            if (e0 + j >= E) continue;
-            if (bf16)
-                v[j] = __uint_as_float(
-                    static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + at + e0 + j)) << 16);
-            else
-                v[j] = __ldg(static_cast<const float*>(p) + at + e0 + j);
+            const int64_t e = at + min(e0 + j, E - 1);
+            w[j] = bf16 ? __ldg(static_cast<const uint16_t*>(p) + e)
+                        : __ldg(static_cast<const uint32_t*>(p) + e);
         }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            v[j] = e0 + j >= E ? past : __uint_as_float(bf16 ? w[j] << 16 : w[j]);
     }
 }
 

@@ -120,6 +120,18 @@ def test_many_tiles(ep):
     case(ep, 9000, 1000, 1048, residual=True, out=torch.float32)
 
 
+# Shapes that tiles of each kind are made for, by which CTAs and with which sums (a CTA
+# alone, 2 to 16 that share one, pairs; long k in fp32).
+@pytest.mark.parametrize("M,N,K", [(1000, 1000, 1000), (600, 1030, 1096), (16, 256, 7168), (130, 260, 4104),
+                                   (512, 250, 2056), (2000, 256, 1544), (3001, 2100, 1100 + 4),
+                                   (5000, 1000, 72), (9000, 260, 2056)])
+@pytest.mark.parametrize("act,out", [("none", bf), ("none", torch.float32), ("swiglu", torch.float32),
+                                     ("gelu", bf)])
+def test_tiles_of_every_kind(ep, M, N, K, act, out):
+    case(ep, M, N, K, act, out=out, seed=K)
+    case(ep, M, N, K, act, True, True, out, True, seed=K + 1)
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_infinities_and_nan_pass_through(ep, act):
     x, w = rand(40, 64), rand(96, 64, seed=1)
@@ -220,7 +232,8 @@ def test_act_grad(ep, act, dtype, M, N):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 8, 8), (5, 60, 64), (130, 57, 136), (300, 256, 1000),
-                                   (64, 2050, 72), (1000, 33, 520), (2049, 300, 2056)])
+                                   (64, 2050, 72), (1000, 33, 520), (2049, 300, 2056),
+                                   (1500, 2050, 2056), (4100, 60, 2048)])
 def test_grad_products(ep, M, N, K):
     dz = torch.full((M, ep.linear_pitch(N)), float("nan"), dtype=bf, device="cuda")
     dz[:, :N] = rand(M, N)
@@ -268,6 +281,19 @@ def test_calls_on_a_stream_and_in_a_graph(ep):
     ep.ep_linear_grad_weight(want, x, d_w)
     for y, d in outs:
         assert torch.equal(y, want) and torch.equal(d, d_w)
+
+
+def test_two_streams_at_once(ep):
+    """Calls that run beside each other, on tiles of different kinds."""
+    shapes = [(128, 256, 7168), (700, 512, 2048), (1, 2048, 7168), (3000, 1024, 512)]
+    args = [(rand(M, K, seed=i), rand(N, K, seed=i + 9)) for i, (M, N, K) in enumerate(shapes)]
+    want = [ep.linear(x, w, out_dtype=torch.float32) for x, w in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [ep.linear(x, w, out_dtype=torch.float32, stream=s) for (x, w), s in zip(args, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_in_a_partition(ep):

@@ -81,7 +81,7 @@ def test_layer_and_gradients(mods):
     q = {k: v.detach().to(f64).requires_grad_(True) for k, v in p.items()}
     want = layer64(q, idx)
     want.backward(dy.to(f64))
-    assert float((y.detach().to(f64) - want).norm() / want.norm()) < 16 * 2.0 ** -8
+    assert float((y.detach().to(f64) - want.detach()).norm() / want.detach().norm()) < 16 * 2.0 ** -8
     for name, v in p.items():
         got, ref = v.grad.to(f64), q[name].grad
         assert v.grad.dtype is v.dtype
@@ -136,3 +136,31 @@ def test_second_derivatives_are_refused(mods):
     g, = torch.autograd.grad(moe.route(l, 2)[1].pow(2).sum(), l, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+def test_a_captured_step(mods):
+    """Forward and backward in a graph, replayed on other inputs."""
+    _, moe = mods
+    x, w = rand(40, 64, seed=1).requires_grad_(True), rand(32, 64, seed=2, scale=0.1).requires_grad_(True)
+    bias = rand(32, seed=3, dtype=torch.float32).requires_grad_(True)
+
+    def step():
+        y = moe.linear(x, w, bias, "silu", out_dtype=torch.float32)
+        idx, weights = moe.route(y, 3, None, "sigmoid")
+        return idx, torch.autograd.grad(weights.pow(2).sum(), (x, w, bias))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        idx, grads = step()
+    with torch.no_grad():
+        x.copy_(rand(40, 64, seed=7))
+    graph.replay()
+    torch.cuda.synchronize()
+    want_idx, want = step()
+    assert torch.equal(idx, want_idx)
+    assert all(torch.equal(a, b) for a, b in zip(grads, want))

@@ -174,6 +174,17 @@ def test_nothing_left(ep, score):
     assert idx.shape == (0, 3) and w.shape == (0, 3)
 
 
+def test_many_tokens(ep):
+    """More tokens than warps at a time; the choice as torch sorts logits, the weights
+    as torch's softmax over them."""
+    l = logits_of(70001, 128, torch.float32, 12)
+    idx, w = ep.route(l, 6)
+    top, want = l.sort(dim=1, descending=True, stable=True)
+    assert torch.equal(idx, want[:, :6])
+    ref = torch.softmax(top[:, :6].to(f64), dim=1)
+    assert bool(((w.to(f64) - ref).abs() <= 16 * 2.0 ** -23 * ref).all())
+
+
 @pytest.mark.parametrize("groups", [1, 4])
 def test_nan_is_chosen_and_shows(ep, groups):
     l = logits_of(6, 32, torch.float32, 9)
