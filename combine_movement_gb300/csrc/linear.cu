@@ -112,97 +112,190 @@ struct Part {
     int rows;
 };
 
-// How a warp goes through the 32 rows of a chunk's columns of out, four of them to a
+// How a warp goes through the 32 rows of a chunk's columns of out, N of them to a
 // lane: kRounds times kAtOnce rows.
-template <bool kGated>
+template <int N, bool kGated>
 struct Walk {
     static constexpr int kCols = kGated ? kChunk / 2 : kChunk;
-    static constexpr int kPieces = kCols / 4, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
+    static constexpr int kPieces = kCols / N, kAtOnce = 32 / kPieces, kRounds = 32 / kAtOnce;
 };
 
+// N neighbouring sums of a row from shared memory.
+template <int N>
+__device__ __forceinline__ Values<N> load_sums(uint32_t at) {
+    if constexpr (N == 4) {
+        const float4 f = load_shared_v4(at);
+        return {{f.x, f.y, f.z, f.w}};
+    } else if constexpr (N == 2) {
+        const float2 f = load_shared_f32x2(at);
+        return {{f.x, f.y}};
+    } else {
+        return {{load_shared_f32(at)}};
+    }
+}
+// Those of row r from value c of a chunk on, in its turning place.
+template <int N>
+__device__ __forceinline__ Values<N> turned(uint32_t turn, int r, int c) {
+    return load_sums<N>(turn_at(turn, r, c / 4) + c % 4 * 4);
+}
+
 // What a lane adds to its values of a chunk, read ahead of them.
-template <bool kGated>
 struct Ahead {
-    Residual r[Walk<kGated>::kRounds];
+    uint32_t bits[32];
 };
-template <bool kGated>
-__device__ __forceinline__ void read_ahead(const LinearArgs& a, const Part& part, int64_t col, bool vec,
-                                           Ahead<kGated>& ahead) {
-    using W = Walk<kGated>;
-    if (a.residual == nullptr) return;
+template <int N, bool kGated>
+__device__ __forceinline__ void read_ahead(const LinearArgs& a, const Part& part, int64_t col,
+                                           Ahead& ahead) {
+    using W = Walk<N, kGated>;
     const int lane = threadIdx.x & 31, r0 = lane / W::kPieces;
-    const int64_t c = col + lane % W::kPieces * 4;
+    const int64_t c = col + lane % W::kPieces * N;
     if (c >= a.n) return;
     int64_t at = (part.row0 + r0) * a.n + c;
 #pragma unroll
-    for (int i = 0; i < W::kRounds; ++i, at += W::kAtOnce * a.n)
-        if (r0 + i * W::kAtOnce < part.rows) ahead.r[i] = load_residual(a, at, a.n - c, vec);
+    for (int i = 0; i < W::kRounds; ++i, at += W::kAtOnce * a.n) {
+        if (r0 + i * W::kAtOnce >= part.rows) continue;
+        const Residual<N> v = load_residual<N>(a, at);
+#pragma unroll
+        for (int j = 0; j < N; ++j) ahead.bits[N * i + j] = v.bits[j];
+    }
+}
+template <bool kGated>
+__device__ __forceinline__ void read_ahead(const LinearArgs& a, const Part& part, int64_t col,
+                                           Ahead& ahead) {
+    if (a.residual != nullptr)
+        by_width(a.n, [&](auto n) { read_ahead<decltype(n)::value, kGated>(a, part, col, ahead); });
 }
 
 // A chunk from its turning place to out, with all that may be asked for: `col` the
-// column of its first sums (gated: of 16 of each half). Two rounds at a time, not
-// unrolled further: a small call goes through these instructions once, and its time
-// is that of bringing them in. (Unrolled, 333 x 1075 with all of it took 4.7 us in
-// here, so 3.) The next rounds' residual is read ahead.
-template <bool kGated>
-__device__ __forceinline__ void finish_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
-                                             int64_t col, bool vec) {
-    using W = Walk<kGated>;
-    const int lane = threadIdx.x & 31, p = lane % W::kPieces, r0 = lane / W::kPieces;
-    const int64_t c = col + p * 4, left = a.n - c;
-    if (left <= 0) return;
-    const Four b0 = load_bias(a.bias, c, left), b1 = load_bias(a.bias, kGated ? a.n + c : c, left);
+// column of its first sums (gated: of 16 of each half). kWhole: all of a lane's values
+// at once, for CTAs that write many chunks: the instructions overlap (a tile of 256 x
+// 256 with silu takes 2.5 us, in eights 9). Else eight values at a time: a small call
+// goes through these instructions once, and its time is that of bringing them in (333 x
+// 1075 with all of it 3 us, whole 4.7); the next ones' residual is on the way.
+template <int N, bool kGated, bool kWhole>
+__device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
+                                            int64_t col, const Ahead& ahead) {
+    using W = Walk<N, kGated>;
+    constexpr int kStep = kWhole ? W::kRounds : 8 / N;  // rounds at a time
+    const int lane = threadIdx.x & 31, p = lane % W::kPieces * N, r0 = lane / W::kPieces;
+    const int64_t c = col + p;
+    if (c >= a.n) return;
+    const Values<N> b0 = load_bias<N>(a.bias, c), b1 = load_bias<N>(a.bias, kGated ? a.n + c : c);
     auto residual = [&](int i) {
         const int r = r0 + i * W::kAtOnce;
-        if (a.residual == nullptr || r >= part.rows) return Residual{};
-        return load_residual(a, (part.row0 + r) * a.n + c, left, vec);
+        if (a.residual == nullptr || r >= part.rows) return Residual<N>{};
+        return load_residual<N>(a, (part.row0 + r) * a.n + c);
     };
-    Residual next[2] = {residual(0), residual(1)};
+    Residual<N> now[kStep], next[kStep];
+#pragma unroll
+    for (int j = 0; j < kStep; ++j) {
+        if constexpr (kWhole) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) now[j].bits[i] = ahead.bits[N * j + i];
+        } else {
+            next[j] = residual(j);
+        }
+    }
 #pragma unroll 1
-    for (int i = 0; i < W::kRounds; i += 2) {
-        const Residual now[2] = {next[0], next[1]};
-        next[0] = residual(i + 2);
-        next[1] = residual(i + 3);
-        Four v[2], up[2];
+    for (int i = 0; i < W::kRounds; i += kStep) {
+        if constexpr (!kWhole) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = r0 + (i + j) * W::kAtOnce;
-            v[j] = four(load_shared_v4(turn_at(turn, r, p))) + b0;
-            up[j] = v[j];
-            if (kGated) up[j] = four(load_shared_v4(turn_at(turn, r, p + W::kPieces))) + b1;
-            if (r < part.rows) keep_z<kGated>(a, part.row0 + r, c, v[j], up[j], left, vec);
+            for (int j = 0; j < kStep; ++j) {
+                now[j] = next[j];
+                next[j] = residual(i + kStep + j);
+            }
         }
-        activate<kGated>(a, v, up);
+        const int r = r0 + i * W::kAtOnce;
+        Values<N> v[kStep], up[kStep];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = r0 + (i + j) * W::kAtOnce;
-            if (r >= part.rows) continue;
-            if (a.residual != nullptr) v[j] = v[j] + residual_values(a, now[j], vec);
-            store_out(a, (part.row0 + r) * a.n + c, v[j], left, vec);
+        for (int j = 0; j < kStep; ++j) {
+            v[j] = turned<N>(turn, r + j * W::kAtOnce, p) + b0;
+            up[j] = kGated ? turned<N>(turn, r + j * W::kAtOnce, p + W::kCols) + b1 : v[j];
         }
+        const int rows = (part.rows - r + W::kAtOnce - 1) / W::kAtOnce;
+        finish<N, kGated>(a, part.row0 + r, c, W::kAtOnce, rows, v, up, now);
     }
 }
 
-// A chunk whose sums have at most a residual to be added, all of it read ahead.
-template <bool kGated>
-__device__ __forceinline__ void write_chunk(const LinearArgs& a, uint32_t turn, const Part& part,
-                                            int64_t col, bool vec, const Ahead<kGated>& ahead) {
-    using W = Walk<kGated>;
-    const int lane = threadIdx.x & 31, p = lane % W::kPieces, r0 = lane / W::kPieces;
-    const int64_t c = col + p * 4, left = a.n - c;
-    if (left <= 0) return;
-    Four v[W::kRounds];
+// The sums of a tile that the cluster's CTAs took parts of k of: each has laid
+// its own out in shared memory; CTA `rank` adds, in the parts' order, and writes
+// those of the rows r = rank mod kParts. A thread takes N neighbouring columns
+// of a few rows at a time, so that its loads overlap.
+template <int N>
+__device__ __forceinline__ Values<N> load_cluster(uint32_t at) {
+    if constexpr (N == 4) {
+        const float4 f = load_cluster_v4(at);
+        return {{f.x, f.y, f.z, f.w}};
+    } else {
+        Values<N> r;
 #pragma unroll
-    for (int i = 0; i < W::kRounds; ++i)
-        v[i] = four(load_shared_v4(turn_at(turn, r0 + i * W::kAtOnce, p)));
-    if (a.residual != nullptr) {
-#pragma unroll
-        for (int i = 0; i < W::kRounds; ++i) v[i] = v[i] + residual_values(a, ahead.r[i], vec);
+        for (int i = 0; i < N; ++i) r.v[i] = load_cluster_f32(at + 4 * i);
+        return r;
     }
-    int64_t at = (part.row0 + r0) * a.n + c;
+}
+template <Mode kMode, int N, bool kGated, int kParts>
+__device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
+                                                  int rank) {
+    using S = Shape<kMode>;
+    constexpr int kCols = kGated ? S::kCols / 2 : S::kCols, kPieces = kCols / N;
+    constexpr int kStep = kOutWarps * 32 / kPieces;  // of this CTA's rows, by all threads
+    constexpr int kMost = kRows / kParts / kStep;    // of them to a thread
+    constexpr int kWant = kParts >= 8 ? 4 / N : 32 / kParts / N;  // loads in flight
+    constexpr int kAtOnce = kMost < 1 || kWant < 1 ? 1 : kMost < kWant ? kMost : kWant;
+    const int64_t rows_left = a.m - tile.row0;
+    const int rows = static_cast<int>(rows_left < kRows ? rows_left : kRows);
+    const int own = (rows + kParts - 1 - rank) / kParts;
+    const int c = threadIdx.x % kPieces * N;
+    const int64_t col = tile.col_tile * kCols + c;
+    if (col >= a.n) return;
+    const Values<N> b0 = load_bias<N>(a.bias, col), b1 = load_bias<N>(a.bias, kGated ? a.n + col : col);
+#pragma unroll 1
+    for (int i0 = threadIdx.x / kPieces; i0 < own; i0 += kAtOnce * kStep) {
+        Values<N> v[kAtOnce][kParts], up[kAtOnce][kParts], vs[kAtOnce], us[kAtOnce];
+        Residual<N> res[kAtOnce] = {};
+        const int64_t row = tile.row0 + i0 * kParts + rank;
 #pragma unroll
-    for (int i = 0; i < W::kRounds; ++i, at += W::kAtOnce * a.n)
-        if (r0 + i * W::kAtOnce < part.rows) store_out(a, at, v[i], left, vec);
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int i = min(i0 + j * kStep, own - 1);  // (rows past the last: it again)
+            if (a.residual != nullptr)
+                res[j] = load_residual<N>(a, (tile.row0 + i * kParts + rank) * a.n + col);
+            const uint32_t at = sums + (i * kParts + rank) * S::kPitch + c * 4;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                const uint32_t from = cluster_map(at, p);
+                v[j][p] = load_cluster<N>(from);
+                if (kGated) up[j][p] = load_cluster<N>(from + kCols * 4);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            vs[j] = v[j][0];
+            us[j] = kGated ? up[j][0] : v[j][0];
+#pragma unroll
+            for (int p = 1; p < kParts; ++p) {
+                vs[j] = vs[j] + v[j][p];
+                if (kGated) us[j] = us[j] + up[j][p];
+            }
+            vs[j] = vs[j] + b0;
+            if (kGated) us[j] = us[j] + b1;
+        }
+        finish<N, kGated>(a, row, col, kStep * kParts, (own - i0 + kStep - 1) / kStep, vs, us, res);
+    }
+}
+template <Mode kMode, bool kGated>
+__device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
+                                                  int rank) {
+    by_width(a.n, [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        if (a.split == 2)
+            write_shared_tile<kMode, N, kGated, 2>(a, sums, tile, rank);
+        else if (a.split == 4)
+            write_shared_tile<kMode, N, kGated, 4>(a, sums, tile, rank);
+        else if (a.split == 8)
+            write_shared_tile<kMode, N, kGated, 8>(a, sums, tile, rank);
+        else if (kMode == kShared && a.split == 16)
+            write_shared_tile<kMode, N, kGated, 16>(a, sums, tile, rank);
+    });
 }
 
 // 32 x 32 sums of a warp into its turning place.
@@ -251,70 +344,6 @@ __device__ __forceinline__ void send_chunk(const LinearArgs& a, const Maps& maps
         bulk_commit();
     }
     __syncwarp();
-}
-
-// The sums of a tile that the cluster's CTAs took parts of k of: each has laid
-// its own out in shared memory; CTA `rank` adds, in the parts' order, and writes
-// those of the rows r = rank mod kParts. A thread takes four neighbouring columns
-// of a few rows at a time, so that its loads overlap.
-template <Mode kMode, bool kGated, int kParts>
-__device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
-                                                  int rank) {
-    using S = Shape<kMode>;
-    constexpr int kCols = kGated ? S::kCols / 2 : S::kCols, kPieces = kCols / 4;
-    constexpr int kStep = kOutWarps * 32 / kPieces;  // of this CTA's rows, by all threads
-    constexpr int kMost = kRows / kParts / kStep;    // of them to a thread
-    constexpr int kAtOnce = kMost < 1 || kParts >= 8 ? 1 : kMost < 8 / kParts ? kMost : 8 / kParts;
-    const int64_t rows_left = a.m - tile.row0;
-    const int rows = static_cast<int>(rows_left < kRows ? rows_left : kRows);
-    const int own = (rows + kParts - 1 - rank) / kParts;
-    const int c = threadIdx.x % kPieces * 4;
-    const int64_t col = tile.col_tile * kCols + c, left = a.n - col;
-    const bool vec = a.n % 4 == 0;
-    if (left <= 0) return;
-#pragma unroll 1
-    for (int i0 = threadIdx.x / kPieces; i0 < own; i0 += kAtOnce * kStep) {
-        Four v[kAtOnce][kParts], up[kAtOnce][kParts];
-        Residual res[kAtOnce] = {};
-        const int64_t row = tile.row0 + i0 * kParts + rank;
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            const int i = i0 + j * kStep;
-            if (i >= own) continue;
-            if (a.residual != nullptr)
-                res[j] = load_residual(a, (row + j * kStep * kParts) * a.n + col, left, vec);
-            const uint32_t at = sums + (i * kParts + rank) * S::kPitch + c * 4;
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) {
-                const uint32_t from = cluster_map(at, p);
-                v[j][p] = four(load_cluster_v4(from));
-                if (kGated) up[j][p] = four(load_cluster_v4(from + kCols * 4));
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-            if (i0 + j * kStep >= own) continue;
-#pragma unroll
-            for (int p = 1; p < kParts; ++p) {
-                v[j][0] = v[j][0] + v[j][p];
-                if (kGated) up[j][0] = up[j][0] + up[j][p];
-            }
-            finish<kGated>(a, row + j * kStep * kParts, col, v[j][0], kGated ? up[j][0] : v[j][0], res[j],
-                           left, vec);
-        }
-    }
-}
-template <Mode kMode, bool kGated>
-__device__ __forceinline__ void write_shared_tile(const LinearArgs& a, uint32_t sums, const Tile& tile,
-                                                  int rank) {
-    if (a.split == 2)
-        write_shared_tile<kMode, kGated, 2>(a, sums, tile, rank);
-    else if (a.split == 4)
-        write_shared_tile<kMode, kGated, 4>(a, sums, tile, rank);
-    else if (a.split == 8)
-        write_shared_tile<kMode, kGated, 8>(a, sums, tile, rank);
-    else if (kMode == kShared && a.split == 16)
-        write_shared_tile<kMode, kGated, 16>(a, sums, tile, rank);
 }
 
 // kExact: sums leave tensor memory every kExactBlocks blocks along k and are added
@@ -495,9 +524,8 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
         constexpr int kCols = kGated ? kChunk / 2 : kChunk, kMine = kGated ? S::kMine / 2 : S::kMine;
         // the second half of a chunk's sums: gated, the up half's
         constexpr int kSecond = kGated ? S::kCols / 2 : 16;
-        const bool vec = a.n % 4 == 0;
         const bool plain = !kGated && maps.plain;
-        const bool as_is = !kGated && a.act == EP_ACT_NONE && a.bias == nullptr && a.z == nullptr;
+        constexpr bool kWhole = kMode == kPair;
         auto release = [&](int i) {
             __syncwarp();
             tcgen05_fence_before();
@@ -515,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
             part.row0 = tile.row0 + (kMode == kPair ? rank * kRows : 0) + quarter * 32;
             part.rows = static_cast<int>(min(static_cast<int64_t>(32), a.m - part.row0));
             const int64_t col0 = tile.col_tile * (2 * kMine) + half * kMine;
-            Ahead<kGated> ahead = {};
-            if (!kExact && !S::kParts && as_is) read_ahead<kGated>(a, part, col0, vec, ahead);
+            Ahead ahead = {};
+            if (kWhole && !kExact) read_ahead<kGated>(a, part, col0, ahead);
             if constexpr (kExact) {
                 // all but the last of the tile's sums into registers, which the last ones
                 // are then added to, in their place
@@ -547,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
                 }
                 if (!ok) break;
                 tmem_store_wait();
-                if (as_is) read_ahead<kGated>(a, part, col0, vec, ahead);
+                if (kWhole) read_ahead<kGated>(a, part, col0, ahead);
             } else {
                 ok = warp_wait<kMode == kPair>(sums + 8 * slot.i, slot.round, abort, a.status);
                 if (!ok) break;
@@ -585,13 +613,11 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
                         }
                         turn_chunk(turn, reinterpret_cast<const float*>(v[0]),
                                    reinterpret_cast<const float*>(v[1]));
-                        if (!as_is) {
-                            finish_chunk<kGated>(a, turn, part, col0 + c, vec);
-                            continue;
-                        }
-                        const Ahead<kGated> now = ahead;
-                        if (c + kCols < kMine) read_ahead<kGated>(a, part, col0 + c + kCols, vec, ahead);
-                        write_chunk<kGated>(a, turn, part, col0 + c, vec, now);
+                        const Ahead now = ahead;
+                        if (kWhole && c + kCols < kMine) read_ahead<kGated>(a, part, col0 + c + kCols, ahead);
+                        by_width(a.n, [&](auto n) {
+                            write_chunk<decltype(n)::value, kGated, kWhole>(a, turn, part, col0 + c, now);
+                        });
                     }
                 }
                 release(slot.i);
@@ -746,6 +772,7 @@ int64_t up(int64_t v, int64_t by) { return (v + by - 1) / by; }
 // bytes; a pair's products 0.27) and for what comes after them. A partition's SMs may
 // not hold a cluster.
 constexpr float kInBytes = 122e3f;   // to an SM, a microsecond
+constexpr float kWideInBytes = 140e3f;
 constexpr float kLatency = 1.0f;     // us, from asking for a stage to its product
 constexpr float kPairBlock = 0.27f;  // us
 struct Plan {
@@ -766,12 +793,12 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, bool plain, int a_rows, in
     const int64_t narrow = tiles(64), mid = tiles(128), wide = tiles(256);
     const float a_bytes = a.a_by_k ? (a.m > 64 ? 2 : 1) * kGroupBytes : a_rows * kRowBytes;
     auto block = [&](int cols, int stages) {
-        return fmaxf((a_bytes + cols * kRowBytes) / kInBytes, kLatency / stages);
+        return fmaxf((a_bytes + cols * kRowBytes) / (cols > 64 ? kWideInBytes : kInBytes), kLatency / stages);
     };
     // a tile takes its products' time, or its results' where those take longer
-    const float alone_tile = fmaxf(a.k_blocks * block(64, Shape<kAlone>::kStages), plain ? 0.6f : 1.2f);
-    const float pair_tile = fmaxf(a.k_blocks * kPairBlock, plain ? 2.2f : 4.0f);
-    float best = up(narrow, num_sms) * (alone_tile + 0.3f) + (plain ? 0.2f : 1.2f);
+    const float alone_tile = fmaxf(a.k_blocks * block(64, Shape<kAlone>::kStages), plain ? 0.6f : 2.0f);
+    const float pair_tile = fmaxf(a.k_blocks * kPairBlock, plain ? 2.2f : 2.8f);
+    float best = up(narrow, num_sms) * (alone_tile + 0.3f) + 0.2f;
     auto take = [&](float time, Plan p) {
         if (time < best) best = time, *plan = p;
     };
@@ -779,7 +806,7 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, bool plain, int a_rows, in
         take(up(pairs, clusters.pairs) * pair_tile + 3.0f, {kPair, 1, clusters.pairs});
     for (int n = 2; n <= kMaxSplit && n <= a.k_blocks; n *= 2) {
         const int64_t blocks = up(a.k_blocks, n);
-        if (narrow <= clusters.n[n]) take(blocks * block(64, Shape<kShared>::kStages) + 2.5f, {kShared, n, 0});
+        if (narrow <= clusters.n[n]) take(blocks * block(64, Shape<kShared>::kStages) + 1.6f, {kShared, n, 0});
         if (n > 8) continue;
         if (mid <= clusters.mid[n]) take(blocks * block(128, Shape<kSharedMid>::kStages) + 3.3f, {kSharedMid, n, 0});
         if (wide <= clusters.wide[n]) take(blocks * block(256, Shape<kSharedWide>::kStages) + 5.0f, {kSharedWide, n, 0});

@@ -101,20 +101,22 @@ __global__ void __launch_bounds__(kThreads, kRows == 1 ? 4 : kRows == 2 ? 3 : 2)
     const int c = i % kCols, r = i / kCols;
     const int64_t col = col0 + c;
     if (r >= a.m || col >= a.n) return;
-    Four v = {}, up = {};
-    Residual res = {};
-    if (a.residual != nullptr) res = load_residual(a, r * a.n + col, 1, false);
+    Values<1> v[1] = {}, up[1] = {};
+    Residual<1> res[1] = {};
+    if (a.residual != nullptr) res[0] = load_residual<1>(a, r * a.n + col);
     if (kLong) {
 #pragma unroll
         for (int p = 0; p < kWarps; ++p) {
-            v.v[0] += part[p][c * kRows + r];
-            if (kGated) up.v[0] += part[p][(c + kCols) * kRows + r];
+            v[0].v[0] += part[p][c * kRows + r];
+            if (kGated) up[0].v[0] += part[p][(c + kCols) * kRows + r];
         }
     } else {
-        v.v[0] = part[warp][c * kRows + r];
-        if (kGated) up.v[0] = part[warp][(c + kCols) * kRows + r];
+        v[0].v[0] = part[warp][c * kRows + r];
+        if (kGated) up[0].v[0] = part[warp][(c + kCols) * kRows + r];
     }
-    finish<kGated>(a, r, col, v, up, res, 1, false);
+    v[0] = v[0] + load_bias<1>(a.bias, col);
+    if (kGated) up[0] = up[0] + load_bias<1>(a.bias, a.n + col);
+    finish<1, kGated>(a, r, col, 0, 1, v, up, res);
 }
 
 template <int kRows, bool kGated>

@@ -8,7 +8,7 @@
 // follow take bf16 operands, so dz is rounded to it, as z was when it was kept; the
 // sums are not.
 //
-// Mapping: a CTA to a strip of 64 columns (32 where rows do not start on 8 bytes;
+// Mapping: a CTA to a strip of 64 columns (32 where they are odd in number;
 // a quarter of those where few columns are summed) and every c-th group of rows, a thread to a few columns of a row; a strip's
 // rows go to the c CTAs of a cluster. A thread adds its rows, the CTA its threads,
 // the cluster its CTAs, each in a fixed order, so that equal calls give equal
@@ -41,6 +41,9 @@ __device__ __forceinline__ Raw<W> load_row(const void* p, bool f32, int64_t at) 
         const uint32_t* q = static_cast<const uint32_t*>(p) + at;
         if constexpr (W == 1) {
             r.bits[0] = __ldg(q);
+        } else if constexpr (W == 2) {
+            const uint2 f = __ldg(reinterpret_cast<const uint2*>(q));
+            r.bits[0] = f.x, r.bits[1] = f.y;
         } else {
 #pragma unroll
             for (int i = 0; i < W; i += 4) {
@@ -53,6 +56,8 @@ __device__ __forceinline__ Raw<W> load_row(const void* p, bool f32, int64_t at) 
     const uint16_t* q = static_cast<const uint16_t*>(p) + at;
     if constexpr (W == 1) {
         r.bits[0] = __ldg(q);  // (shifted where it is used: here it would wait for the load)
+    } else if constexpr (W == 2) {
+        r.bits[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
     } else if constexpr (W == 4) {
         const uint2 f = __ldg(reinterpret_cast<const uint2*>(q));
         r.bits[0] = f.x, r.bits[1] = f.y;
@@ -73,6 +78,8 @@ template <int W>
 __device__ __forceinline__ void store_row(uint16_t* q, const float (&v)[W]) {
     if constexpr (W == 1) {
         *q = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+    } else if constexpr (W == 2) {
+        *reinterpret_cast<uint32_t*>(q) = pack_bf16x2(v[0], v[1]);
     } else if constexpr (W == 4) {
         *reinterpret_cast<uint2*>(q) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     } else {
@@ -85,7 +92,7 @@ __device__ __forceinline__ void store_row(uint16_t* q, const float (&v)[W]) {
 template <int W, int kLanes, bool kGated, bool kF32, bool kSums>
 __global__ void __launch_bounds__(kThreads, kSums ? 2 : 3) act_grad_kernel(const ActGradArgs a) {
     constexpr int kHalves = kGated ? 2 : 1, kRows = kThreads / kLanes, kCols = W * kLanes;
-    constexpr int kAtOnce = W == 8 ? (kGated || kF32 ? 2 : 4) : W == 4 ? 4 : 16;  // rows whose loads are in flight
+    constexpr int kAtOnce = W == 8 ? (kGated || kF32 ? 2 : 4) : W == 4 ? 4 : W == 2 ? 8 : 16;  // rows whose loads are in flight
     __shared__ float part[kThreads / 32][kHalves][kCols];
     __shared__ float total[kHalves][kCols];
     griddep_wait();
@@ -222,6 +229,7 @@ template <bool kGated, bool kF32>
 cudaError_t launch_width(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
     if (a.n % 8 == 0) return launch_lanes<8, 8, kGated, kF32>(a, num_sms, stream);
     if (a.n % 4 == 0) return launch_lanes<4, 16, kGated, kF32>(a, num_sms, stream);
+    if (a.n % 2 == 0) return launch_lanes<2, 32, kGated, kF32>(a, num_sms, stream);
     return launch_lanes<1, 32, kGated, kF32>(a, num_sms, stream);
 }
 
