@@ -7,14 +7,36 @@
 // residual), v kept in bf16 where asked for. Each operand has its rows along k
 // or (its gradients' products) runs along m or n, k by k.
 //
-// Mapping: a persistent grid, one CTA per SM, tiles of 128 x 256 of the output
-// (gated: 128 columns of each half). Four stages of shared memory take 64
-// values along k of both operands (tensor copies, 128-byte swizzle; an operand
-// that runs along m or n in groups of 64 by 64); one thread issues four
-// tcgen05.mma of 128 x 256 x 16 for each. A tile's sums stay in tensor memory,
-// in one of two places, so that eight warps write a tile while the next one's
-// products run. They read 32 columns of 32 rows at a time and turn them around in
-// shared memory, so that eight lanes write 128 bytes of a row.
+// Mapping. A stage of shared memory takes 64 values along k of a tile's rows of both
+// operands (tensor copies, 128-byte swizzle; an operand that runs along m or n in
+// groups of 64 by 64, which the product reads as it lies); one thread issues four
+// tcgen05.mma, 16 values along k each, and a tile's sums stay in tensor memory, in one
+// of two places, so that eight warps write a tile while the next one's products run.
+// Three ways to make a tile, by what the sizes leave to do (plan_for):
+//  - pairs of CTAs (cta_group::2) on 256 x 256, persistent: each brings in its 128 rows
+//    of a and half of b, 32 KB for 512 cycles of products, which is what an SM
+//    takes in (64 bytes a cycle; one CTA on 128 x 256 needs 96, and took 20 % longer);
+//  - one CTA on 128 x 64, persistent: more tiles of small outputs;
+//  - clusters of 2 to 16 CTAs on 128 x 64, 128 or 256 that share a tile's blocks along k
+//    and add their sums through shared memory: few tiles, long k.
+// A tensor core's fp32 sum loses more at each of its steps than rounding to nearest does,
+// and to one side: 7168 products in a row are off by 8e-6 of their norm, 9e-7 in parts of
+// 1024 that are added in fp32 registers, as those of fp32 results are (bf16 results
+// lose 2e-3 at their end).
+//
+// Results. Sums that are the result but for rounding leave by the copy engine, 32 x 32
+// at a time. The others are turned around in shared memory, from a row to a lane to
+// rows across lanes, for bias, activation and residual and for stores along rows.
+//
+// What bounds it. Large products: the tensor cores at 0.87 of their cycles (4096 x 4096 x
+// 7168: 119-130 us cool, 1.9-2.0 PFLOP/s; for seconds the board's power limit, 145 us,
+// where the library's product takes 139). 16384 x 2048 x 7168 with a residual 262 us
+// cool, 317 for seconds (the library's 345). Few columns: 16384 x 7168 x 256 48 us, 0.8
+// of the copy rate: 64 pairs leave 24 SMs idle, and each reads all of b. Small ones:
+// 128 x 7168 x 256 7.1 us: 0.2 us from launch to the first copy, 1.1 until it lands, 0.2 a
+// block along k (24 KB at an SM's 120 GB/s), 2 to join 16 parts, 0.7 to end together.
+// Measured and not kept: k begun at another block in each tile (nothing), rows brought
+// into L2 ahead (2-30 % slower).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -49,6 +71,7 @@ constexpr int kMaxSplit = 16;
 constexpr int kRowGroup = 8;                 // row tiles that share a column tile's turn
 // Blocks along k after which fp32 results take a tile's sums out of tensor memory.
 constexpr int kExactBlocks = 16;
+constexpr int kLongBlocks = 1 << 17;
 
 template <Mode kMode>
 struct Shape {
@@ -846,7 +869,8 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
     maps.plain = plain && (pair || plan.mode == kAlone);
     if (!ok || (maps.plain && !encode_out(&maps.out, a))) return cudaErrorInvalidValue;
     const int64_t tiles = a.row_tiles * a.col_tiles;
-    const bool exact = a.out_f32 && a.k_blocks > kExactBlocks;
+    // (of a very long k, too, so that no warp waits for its sums for a second)
+    const bool exact = a.k_blocks > kExactBlocks && (a.out_f32 || a.k_blocks > kLongBlocks);
     if (pair) {
         const int grid = 2 * static_cast<int>(tiles < plan.clusters ? tiles : plan.clusters);
         if (exact)
