@@ -613,29 +613,46 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
         uint32_t next_head = __shfl_down_sync(kFullMask, mine_head, 1);
         if (lane == 31) next_head = last_head;  // (K = 32)
         bool doubt = lane < min(n - 1, a.K) && !clear(mine_head, next_head);
-        if (__any_sync(kFullMask, doubt)) {
-            // the lost bits back, and equal ones
+        const uint32_t first_doubts = __ballot_sync(kFullMask, doubt);
+        if (first_doubts != 0) {
+            // with the lost bits back, and equal ones by their index
+            auto settled = [&](int e1, float l1, int e2, float l2) {
+                if (by_logit) {
+                    const uint32_t k1 = key_of(l1), k2 = key_of(l2);
+                    return k1 > k2 || (k1 == k2 && e1 < e2);
+                }
+                const float b1 = __ldg(a.bias + e1), b2 = __ldg(a.bias + e2);
+                const float c1 = score.of(l1) + b1, c2 = score.of(l2) + b2;
+                const float off = 2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * 0x1p-22f;
+                return (l1 == l2 && b1 == b2 && e1 < e2) || c1 - c2 > off ||
+                       (c1 != c1 && (c2 == c2 || e1 < e2));
+            };
             int next = __shfl_down_sync(kFullMask, mine, 1);
             if (lane == 31) next = index(last_owner, last_head);
-            if (doubt) {
-                const float l1 = load_logit(a, row + mine), l2 = load_logit(a, row + next);
-                if (!by_logit) {
-                    const float b1 = __ldg(a.bias + mine), b2 = __ldg(a.bias + next);
-                    const float c1 = score.of(l1) + b1, c2 = score.of(l2) + b2;
-                    const float off = 2.0f * score.bound + (fabsf(c1) + fabsf(c2)) * 0x1p-22f;
-                    doubt = !(l1 == l2 && b1 == b2 && mine < next) && !(c1 - c2 > off) &&
-                        !(c1 != c1 && (c2 == c2 || mine < next));
-                } else {
-                    const uint32_t k1 = key_of(l1), k2 = key_of(l2);
-                    doubt = k1 < k2 || (k1 == k2 && mine > next);
+            if (doubt)
+                doubt = !settled(mine, load_logit(a, row + mine), next, load_logit(a, row + next));
+            // Is the last of the K also larger than what was not taken, of which the lost
+            // bits may hide a larger one?
+            bool beaten = false;
+            if ((first_doubts >> (a.K - 1)) & 1) {
+                const int in = __shfl_sync(kFullMask, mine, a.K - 1);
+                const uint32_t in_head = __shfl_sync(kFullMask, mine_head, a.K - 1);
+                const float in_l = load_logit(a, row + in);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    // (of sorted ones none follows one that is out)
+                    if (((kSort ? key[0] : key[j]) & ~kLast) <= kOutKey) continue;
+                    if ((key[j] & ~kLast) <= kOutKey || clear(in_head, key[j])) continue;
+                    const int e = index(lane, key[j]);
+                    beaten |= !settled(in, in_l, e, load_logit(a, row + e));
                 }
             }
-            const uint32_t doubts = __ballot_sync(kFullMask, doubt);
-            if (doubts != 0) {
-                // the candidates for the K places, down to a clear step
+            if (__any_sync(kFullMask, doubt || beaten)) {
+                // the candidates for the K places, down to a clear step (with an order in
+                // doubt the last of the K need not be the least of them)
                 int count = a.K;
                 bool found = true;
-                if ((doubts >> (a.K - 1)) & 1) {
+                if ((first_doubts >> (a.K - 1)) & 1) {
                     found = false;
                     for (count = n; !found && count < 32;) {
                         const uint32_t before = last_head;

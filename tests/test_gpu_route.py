@@ -151,6 +151,23 @@ def test_orders_that_32_bits_cannot_settle(ep, score, groups, worth):
               max(1, groups // 2), worth)
 
 
+@pytest.mark.parametrize("E,K", [(256, 8), (64, 4), (60, 7), (500, 3), (32, 32), (1000, 32)])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("groups,worth", [(1, "max"), (4, "max"), (4, "top2")])
+def test_values_a_few_units_apart(ep, E, K, biased, groups, worth):
+    """Logits (with a bias, their scores' neighbours too) one to forty units of 2^-23 apart,
+    so that integers without their last bits put them in a wrong order, at the border
+    of what is chosen too."""
+    g = torch.Generator().manual_seed(E)
+    l = 1.0 + torch.randint(0, 40, (48, E), generator=g).float() * 2.0 ** -23
+    l[::3] = 1.0 + torch.randint(0, 3, (16, E), generator=g).float() * 2.0 ** -23
+    l[1::6, ::2] += 0.5
+    b = torch.randint(0, 3, (E,), generator=g).float() * 2.0 ** -24 if biased else None
+    kept = groups if E // groups * (groups // 2) < K else max(1, groups // 2)
+    check(ep, l.cuda(), K, None if b is None else b.cuda(), "sigmoid", groups, kept, worth)
+    check(ep, l.cuda(), K, None if b is None else b.cuda(), "softmax", groups, kept, worth)
+
+
 def test_scores_beyond_32_bits(ep):
     """Logits whose scores underflow keep their order and their ratios."""
     l = torch.tensor([[-200.0, -201.0, -199.5, -300.0], [-120.0, -90.0, -104.0, -119.0],
