@@ -21,7 +21,7 @@
 //    and add their sums through shared memory: few tiles, long k.
 // A tensor core's fp32 sum loses more at each of its steps than rounding to nearest does,
 // and to one side: 7168 products in a row are off by 8e-6 of their norm, 9e-7 in parts of
-// 1024 that are added in fp32 registers, as those of fp32 results are (bf16 results
+// 1024 that are added in fp32 registers, as all of fp32 results are (bf16 results
 // lose 2e-3 at their end).
 //
 // Results. Sums that are the result but for rounding leave by the copy engine, 32 x 32
@@ -370,7 +370,7 @@ __device__ __forceinline__ void send_chunk(const LinearArgs& a, const Maps& maps
 }
 
 // kExact: sums leave tensor memory every kExactBlocks blocks along k and are added
-// in registers (not of shared tiles, whose parts are added as they are joined).
+// in registers.
 template <Mode kMode, bool kGated, bool kExact>
 __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
     linear_kernel(const LinearArgs a, const __grid_constant__ Maps maps) {
@@ -579,9 +579,12 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
                     const bool last = kb + per_sum >= kb_end;
 #pragma unroll
                     for (int c = 0; c < S::kMine / 16; ++c) {
-                        // gated, 64 of each half: the columns that it writes
-                        const uint32_t at = from + slot.i * S::kCols + half * kMine + 16 * c +
-                                            (16 * c >= kMine ? S::kCols / 2 - kMine : 0);
+                        // gated, half of each half: the columns that it writes (of a shared
+                        // tile it lays out neighbouring ones)
+                        const uint32_t at =
+                            from + slot.i * S::kCols + 16 * c +
+                            (S::kParts ? half * S::kMine
+                                       : half * kMine + (16 * c >= kMine ? S::kCols / 2 - kMine : 0));
                         uint32_t v[16];
                         tmem_load16(at, v);
                         tmem_load_wait16(v);
@@ -744,6 +747,17 @@ cudaError_t launch(const LinearArgs& a, const Maps& maps, int grid, int cluster,
     return launch_dependent_clusters(kern, grid, cluster, kThreads, kSmem, stream, a, maps);
 }
 
+template <Mode kMode>
+cudaError_t launch_shared(const LinearArgs& a, const Maps& maps, bool gated, bool exact, int64_t tiles,
+                          cudaStream_t stream) {
+    const int grid = static_cast<int>(tiles) * a.split;
+    if (exact)
+        return gated ? launch<kMode, true, true>(a, maps, grid, a.split, stream)
+                     : launch<kMode, false, true>(a, maps, grid, a.split, stream);
+    return gated ? launch<kMode, true, false>(a, maps, grid, a.split, stream)
+                 : launch<kMode, false, false>(a, maps, grid, a.split, stream);
+}
+
 // Pairs, and clusters of 2, 4, 8, 16 CTAs that share a tile (wide ones at most 8), that a device holds at a
 // time: fewer than SMs / size, because a cluster's lie in one part (GPC) of it.
 struct ResidentClusters {
@@ -870,7 +884,8 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
     if (!ok || (maps.plain && !encode_out(&maps.out, a))) return cudaErrorInvalidValue;
     const int64_t tiles = a.row_tiles * a.col_tiles;
     // (of a very long k, too, so that no warp waits for its sums for a second)
-    const bool exact = a.k_blocks > kExactBlocks && (a.out_f32 || a.k_blocks > kLongBlocks);
+    const int64_t sum_blocks = up(a.k_blocks, a.split);
+    const bool exact = sum_blocks > kExactBlocks && (a.out_f32 || sum_blocks > kLongBlocks);
     if (pair) {
         const int grid = 2 * static_cast<int>(tiles < plan.clusters ? tiles : plan.clusters);
         if (exact)
@@ -879,21 +894,9 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
         return gated ? launch<kPair, true, false>(a, maps, grid, 2, stream)
                      : launch<kPair, false, false>(a, maps, grid, 2, stream);
     }
-    if (plan.mode == kSharedMid) {
-        const int grid = static_cast<int>(tiles) * a.split;
-        return gated ? launch<kSharedMid, true, false>(a, maps, grid, a.split, stream)
-                     : launch<kSharedMid, false, false>(a, maps, grid, a.split, stream);
-    }
-    if (plan.mode == kSharedWide) {
-        const int grid = static_cast<int>(tiles) * a.split;
-        return gated ? launch<kSharedWide, true, false>(a, maps, grid, a.split, stream)
-                     : launch<kSharedWide, false, false>(a, maps, grid, a.split, stream);
-    }
-    if (plan.mode == kShared) {
-        const int grid = static_cast<int>(tiles) * a.split;
-        return gated ? launch<kShared, true, false>(a, maps, grid, a.split, stream)
-                     : launch<kShared, false, false>(a, maps, grid, a.split, stream);
-    }
+    if (plan.mode == kSharedMid) return launch_shared<kSharedMid>(a, maps, gated, exact, tiles, stream);
+    if (plan.mode == kSharedWide) return launch_shared<kSharedWide>(a, maps, gated, exact, tiles, stream);
+    if (plan.mode == kShared) return launch_shared<kShared>(a, maps, gated, exact, tiles, stream);
     const int grid = static_cast<int>(tiles < num_sms ? tiles : num_sms);
     if (exact)
         return gated ? launch<kAlone, true, true>(a, maps, grid, 1, stream)

@@ -132,6 +132,39 @@ def test_tiles_of_every_kind(ep, M, N, K, act, out):
     case(ep, M, N, K, act, True, True, out, True, seed=K + 1)
 
 
+# Sums of positive numbers: what the tensor cores' steps lose adds up. A step takes at
+# least 8 products and loses at most a unit of the sum so far, which grows evenly: of
+# 1024 products at most 64.5 units of 2^-23 of their sum. Adding P parts loses at most
+# half a unit of the sum so far each time, (P + 1) / 4 in all. (The numbers lie in 1 to 2,
+# so that no sum of 8 is further than a quarter from the others: 1.25 times that.) In one
+# sum of K products it would be up to K / 16 units.
+@pytest.mark.parametrize("M,N,K", [(128, 256, 32768), (2000, 256, 7168), (1000, 1000, 7168), (512, 512, 16384),
+                                   (300, 2048, 16384), (4096, 4096, 8192), (5000, 64, 8192)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_fp32_results_are_of_short_sums(ep, M, N, K, act):
+    x, w = rand(M, K).uniform_(1, 2), rand(N, K, seed=1).uniform_(1, 2)
+    units = 1.25 * (64.5 + (K / 1024 + 1) / 4)
+    if act == "swiglu":  # gates of 1, by the first product; silu and products: 10 + 4
+        N, units = N // 2, units + 14
+        w[:N], w[:N, 0], x[:, 0] = 0, 1, 1
+    y = torch.empty(M, N, device="cuda")
+    ep.ep_linear(x, w, y, activation=act)
+    want = x.to(f64) @ w[-N:].to(f64).T
+    if act == "swiglu":
+        want = want * torch.sigmoid(torch.ones((), dtype=f64, device="cuda"))
+    assert float(((y.to(f64) - want).abs() / want).max()) < units * U
+
+
+@pytest.mark.parametrize("M,N,K", [(8192, 256, 2048), (16384, 256, 1024), (16384, 64, 512), (9000, 1000, 520)])
+def test_fp32_weight_gradients_are_of_short_sums(ep, M, N, K):
+    dz, x = rand(M, ep.linear_pitch(N)).uniform_(1, 2), rand(M, K, seed=1).uniform_(1, 2)
+    d_w = torch.empty(N, K, device="cuda")
+    ep.ep_linear_grad_weight(dz, x, d_w)
+    want = dz[:, :N].to(f64).T @ x.to(f64)
+    units = 1.25 * (64.5 + (M / 1024 + 1) / 4)
+    assert float(((d_w.to(f64) - want).abs() / want).max()) < units * U
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_infinities_and_nan_pass_through(ep, act):
     x, w = rand(40, 64), rand(96, 64, seed=1)
