@@ -872,7 +872,9 @@ ep_status_t ep_linear_act_grad(const void* dy, int dy_type, const uint16_t* z, i
     a.dz = dz;
     a.pitch = pitch;
     a.d_bias = d_bias;
-    return from_cuda(ep::launch_act_grad(a, sm_count, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int part = ep::partition_sms(s);
+    return from_cuda(ep::launch_act_grad(a, part > 0 ? part : sm_count, part > 0, s));
 }
 
 ep_status_t ep_linear_grad_input(const uint16_t* dz, int64_t pitch, int64_t M, int64_t N,

@@ -355,7 +355,7 @@ struct ActGradArgs {
     float* d_bias;             // [n] (gated: [2n]), nullable
 };
 
-cudaError_t launch_act_grad(const ActGradArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_act_grad(const ActGradArgs& a, int num_sms, bool partition, cudaStream_t stream);
 
 // Launch a kernel of the hot path. With programmatic dependent launch the
 // launch may start while the previous kernel on the stream finishes: its CTAs

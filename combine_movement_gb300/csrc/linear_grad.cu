@@ -189,15 +189,15 @@ __global__ void __launch_bounds__(kThreads, kSums ? 2 : 3) act_grad_kernel(const
 }
 
 template <int W, int kLanes, bool kGated, bool kF32>
-cudaError_t launch(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const ActGradArgs& a, int num_sms, bool partition, cudaStream_t stream) {
     constexpr int kRows = kThreads / kLanes, kCols = W * kLanes;
     const int64_t strips = (a.n + kCols - 1) / kCols;
     const int64_t groups = a.m > 0 ? (a.m + kRows - 1) / kRows : 1;
-    // with sums the grid's rows of CTAs are a cluster; else as many as there is
-    // work for
+    // with sums the grid's rows of CTAs are a cluster, of one where a partition's SMs
+    // may not hold more; else as many as there is work for
     int64_t parts = 8 * num_sms / strips + 1;
     if (a.d_bias != nullptr) {
-        int64_t c = kMaxCluster;
+        int64_t c = partition ? 1 : kMaxCluster;
         while (c > 1 && c > groups) c /= 2;
         parts = c;
     } else if (parts > groups) {
@@ -224,28 +224,29 @@ cudaError_t launch(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
 // Strips of a quarter of the columns where the clusters of whole ones leave SMs
 // idle.
 template <int W, int kLanes, bool kGated, bool kF32>
-cudaError_t launch_lanes(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.d_bias != nullptr && (a.n + W * kLanes - 1) / (W * kLanes) * kMaxCluster < num_sms)
-        return launch<W, kLanes / 4, kGated, kF32>(a, num_sms, stream);
-    return launch<W, kLanes, kGated, kF32>(a, num_sms, stream);
+cudaError_t launch_lanes(const ActGradArgs& a, int num_sms, bool partition, cudaStream_t stream) {
+    const int64_t strips = (a.n + W * kLanes - 1) / (W * kLanes);
+    if (a.d_bias != nullptr && strips * (partition ? 1 : kMaxCluster) < num_sms)
+        return launch<W, kLanes / 4, kGated, kF32>(a, num_sms, partition, stream);
+    return launch<W, kLanes, kGated, kF32>(a, num_sms, partition, stream);
 }
 
 template <bool kGated, bool kF32>
-cudaError_t launch_width(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.n % 8 == 0) return launch_lanes<8, 8, kGated, kF32>(a, num_sms, stream);
-    if (a.n % 4 == 0) return launch_lanes<4, 16, kGated, kF32>(a, num_sms, stream);
-    if (a.n % 2 == 0) return launch_lanes<2, 32, kGated, kF32>(a, num_sms, stream);
-    return launch_lanes<1, 32, kGated, kF32>(a, num_sms, stream);
+cudaError_t launch_width(const ActGradArgs& a, int num_sms, bool partition, cudaStream_t stream) {
+    if (a.n % 8 == 0) return launch_lanes<8, 8, kGated, kF32>(a, num_sms, partition, stream);
+    if (a.n % 4 == 0) return launch_lanes<4, 16, kGated, kF32>(a, num_sms, partition, stream);
+    if (a.n % 2 == 0) return launch_lanes<2, 32, kGated, kF32>(a, num_sms, partition, stream);
+    return launch_lanes<1, 32, kGated, kF32>(a, num_sms, partition, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_act_grad(const ActGradArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_act_grad(const ActGradArgs& a, int num_sms, bool partition, cudaStream_t stream) {
     if (a.act == EP_ACT_SWIGLU)
-        return a.dy_f32 ? launch_width<true, true>(a, num_sms, stream)
-                        : launch_width<true, false>(a, num_sms, stream);
-    return a.dy_f32 ? launch_width<false, true>(a, num_sms, stream)
-                    : launch_width<false, false>(a, num_sms, stream);
+        return a.dy_f32 ? launch_width<true, true>(a, num_sms, partition, stream)
+                        : launch_width<true, false>(a, num_sms, partition, stream);
+    return a.dy_f32 ? launch_width<false, true>(a, num_sms, partition, stream)
+                    : launch_width<false, false>(a, num_sms, partition, stream);
 }
 
 }  // namespace ep

@@ -344,3 +344,27 @@ def test_in_a_partition(ep):
     close(y, want, err)
     assert torch.allclose(d_b.to(f64), y.to(f64).sum(dim=0), rtol=0,
                           atol=float(80 * U * y.abs().sum(dim=0).max()))
+
+
+@pytest.mark.parametrize("M,N", [(5000, 512), (3000, 57), (700, 6000)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_act_grad_in_a_partition(ep, M, N, act):
+    """Sums over many rows where a partition's SMs may hold no cluster (bounds: those of
+    test_act_grad)."""
+    raw, _, sms, _ = ep.ep_sm_partition(8)
+    s = torch.cuda.ExternalStream(raw)
+    wide = 2 * N if act == "swiglu" else N
+    dy, z = rand(M, N), rand(M, wide, seed=1)
+    dz = torch.empty(M, ep.linear_pitch(wide), dtype=bf, device="cuda")
+    d_b = torch.full((wide,), float("nan"), device="cuda")
+    torch.cuda.synchronize()
+    ep.ep_linear_act_grad(dy, z if act != "none" else None, dz, d_b, act, stream=s)
+    s.synchronize()
+    want = slopes64(z, dy, act)
+    err = 0 * want
+    if act == "swiglu":
+        g, u, d = z[:, :N].to(f64).abs(), z[:, N:].to(f64).abs(), dy.to(f64).abs()
+        err = (40 + 4 * torch.cat([g, g], 1) ** 2) * U * torch.cat([d * u * (1 + g), d * g], 1) + 2.0 ** -126
+    close(dz[:, :wide], want, err)
+    sums = (d_b.to(f64) - want.sum(dim=0)).abs()
+    assert bool((sums <= err.sum(dim=0) + (M + 16) * U * (want.abs() + err).sum(dim=0)).all())
