@@ -244,6 +244,14 @@ def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
                              group_score=group_score, renormalize=renormalize, scale=scale))
 
 
+# Rows as the products read them: a copy where they do not lie one after the other or
+# do not start on 16 bytes (flat parameters, the gradient of one of several results that
+# were joined).
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, residual, activation, out_dtype):
@@ -263,7 +271,7 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, z = ctx.saved_tensors
         need_x, need_w, need_bias, need_residual = ctx.needs_input_grad[:4]
-        dy, wide, act = dy.contiguous(), ctx.wide, ctx.activation
+        dy, wide, act = _dense(dy), ctx.wide, ctx.activation
         M = dy.shape[0]
         dx = d_w = d_bias = None
         dz = dy  # where it is what the products take
@@ -294,8 +302,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     gradient wants it, and rounds what comes back through the activation to bf16
     before the gradients' products."""
     _check_shape(x, (x.shape[0], w.shape[-1]), "x")
-    return _Linear.apply(x.contiguous(), w.contiguous(), bias,
-                         None if residual is None else residual.contiguous(), activation, out_dtype)
+    return _Linear.apply(_dense(x), _dense(w), bias, None if residual is None else _dense(residual),
+                         activation, out_dtype)
 
 
 def _main() -> None:

@@ -125,6 +125,27 @@ def test_strided_arguments(mods):
     assert torch.allclose(x2.grad.float(), w.float().sum(dim=0).expand(50, 64), rtol=2e-2, atol=2e-2)
 
 
+@pytest.mark.parametrize("out", [bf, torch.float32])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_arguments_off_16_bytes(mods, out, act):
+    """Flat parameters and activations hand out matrices that start anywhere, and so
+    does the gradient of a result that was one of several joined ones."""
+    _, moe = mods
+    x, w, r = rand(5, 64, seed=1), rand(24, 64, seed=2), rand(5, 24, seed=3, dtype=out)
+    ones = [t.clone().requires_grad_() for t in (x, w, r)]
+    y = moe.linear(ones[0], ones[1], None, act, ones[2], out)
+    g = rand(3 + y.numel(), seed=4, dtype=out)
+    y.backward(g[3:].view_as(y).clone())
+    parts = [torch.cat([t.new_zeros(3), t.flatten()]).requires_grad_() for t in (x, w, r)]
+    args = [f[3:].view_as(t) for f, t in zip(parts, (x, w, r))]
+    assert all(a.data_ptr() % 16 for a in args)
+    got = moe.linear(args[0], args[1], None, act, args[2], out)
+    assert torch.equal(got, y)
+    torch.cat([got.new_zeros(3), got.flatten()]).backward(g)
+    for f, t in zip(parts, ones):
+        assert torch.equal(f.grad[3:].view_as(t), t.grad)
+
+
 def test_second_derivatives_are_refused(mods):
     _, moe = mods
     x = rand(8, 64, seed=1).requires_grad_(True)
