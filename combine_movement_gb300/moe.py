@@ -302,8 +302,11 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     gradient wants it, and rounds what comes back through the activation to bf16
     before the gradients' products."""
     _check_shape(x, (x.shape[0], w.shape[-1]), "x")
-    return _Linear.apply(_dense(x), _dense(w), bias, None if residual is None else _dense(residual),
-                         activation, out_dtype)
+    x, w, residual = _dense(x), _dense(w), None if residual is None else _dense(residual)
+    # (a function's forward is not told that no gradient is recorded, and would keep z)
+    if not torch.is_grad_enabled():
+        return ep.linear(x, w, bias, activation, residual, out_dtype)
+    return _Linear.apply(x, w, bias, residual, activation, out_dtype)
 
 
 def _main() -> None:

@@ -146,6 +146,20 @@ def test_arguments_off_16_bytes(mods, out, act):
         assert torch.equal(f.grad[3:].view_as(t), t.grad)
 
 
+def test_without_a_gradient_nothing_is_kept(mods):
+    """Parameters ask for a gradient, but not where none is recorded."""
+    _, moe = mods
+    x, w = rand(512, 256, seed=1), rand(4096, 256, seed=2).requires_grad_()
+    with torch.no_grad():
+        moe.linear(x, w, activation="silu")  # (the libraries' own first allocations)
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        y = moe.linear(x, w, activation="silu")
+    assert torch.cuda.max_memory_allocated() - before == y.numel() * 2
+    assert torch.equal(y, moe.linear(x, w, activation="silu").detach())
+
+
 def test_second_derivatives_are_refused(mods):
     _, moe = mods
     x = rand(8, 64, seed=1).requires_grad_(True)
