@@ -55,6 +55,7 @@ namespace {
 // half of b each.
 enum Mode { kAlone, kShared, kSharedMid, kSharedWide, kPair };
 
+constexpr unsigned kFullMask = 0xFFFFFFFFu;
 constexpr int kRows = 128;                   // of the output, in one CTA
 constexpr int kTileK = 64;                   // values of one stage along k
 constexpr uint32_t kRowBytes = kTileK * 2;
@@ -380,11 +381,12 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ Control ctl;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // the swizzle's period
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (from one lane: what the warps' loops go by is then known to be the same in all)
+    const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t full = smem_u32(ctl.full), done = smem_u32(ctl.done);
     const uint32_t sums = smem_u32(ctl.sums), sums_read = smem_u32(ctl.sums_read);
     const uint32_t abort = smem_u32(&ctl.abort);
-    const int rank = kClusters ? static_cast<int>(cluster_rank()) : 0;
+    const int rank = kClusters ? __shfl_sync(kFullMask, static_cast<int>(cluster_rank()), 0) : 0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
     tcgen05_fence_after();
     griddep_wait();
     griddep_launch_dependents();
-    const uint32_t tmem = ctl.tmem;
+    const uint32_t tmem = __shfl_sync(kFullMask, ctl.tmem, 0);
     const int64_t tiles = a.row_tiles * a.col_tiles;
     const int size = kMode == kPair ? 2 : S::kParts ? a.split : 1;
     const int64_t t0 = blockIdx.x / size;
@@ -475,11 +477,10 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
 #pragma unroll
                         for (int g = 0; g < S::kOwnB / 64; ++g)
                             load(dst_b + g * kGroupBytes, &maps.b, c + 64 * g, k, bar);
-                    } else if (kMode == kPair) {
-                        load(dst_b, &maps.b, k, rank == 1 ? col1 : col0, bar);
                     } else {
-                        load(dst_b, &maps.b, k, col0, bar);
-                        load(dst_b + S::kCols / 2 * kRowBytes, &maps.b, k, col1, bar);
+                        load(dst_b, &maps.b, k, kMode == kPair && rank == 1 ? col1 : col0, bar);
+                        if (kGated && kMode != kPair)
+                            load(dst_b + S::kCols / 2 * kRowBytes, &maps.b, k, col1, bar);
                     }
                 }
                 __syncwarp();
@@ -879,7 +880,7 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
         (a.a_by_k ? encode_map(&maps.a, a.a, a.k, a.m, a.a_pitch, kTileK)
                   : encode_map(&maps.a, a.a, a.m, a.k, a.a_pitch, maps.a_rows)) &&
         (a.b_by_k ? encode_map(&maps.b, a.b, a.k, b_rows, a.b_pitch, kTileK)
-                  : encode_map(&maps.b, a.b, b_rows, a.k, a.b_pitch, cols / 2));
+                  : encode_map(&maps.b, a.b, b_rows, a.k, a.b_pitch, gated || pair ? cols / 2 : cols));
     maps.plain = plain && (pair || plan.mode == kAlone);
     if (!ok || (maps.plain && !encode_out(&maps.out, a))) return cudaErrorInvalidValue;
     const int64_t tiles = a.row_tiles * a.col_tiles;
