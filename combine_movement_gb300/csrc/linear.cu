@@ -804,15 +804,26 @@ cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
 
 int64_t up(int64_t v, int64_t by) { return (v + by - 1) / by; }
 
-// Who works on a tile, and how many CTAs share one: what takes least by the
-// times measured for a block along k (an SM takes in 122 GB/s: 24 KB of a narrow
-// tile 0.2 us, 48 KB of a wide one 0.4; a stage's latency where few rows make for few
-// bytes; a pair's products 0.27) and for what comes after them. A partition's SMs may
-// not hold a cluster.
-constexpr float kInBytes = 122e3f;   // to an SM, a microsecond
-constexpr float kWideInBytes = 140e3f;
-constexpr float kLatency = 1.0f;     // us, from asking for a stage to its product
-constexpr float kPairBlock = 0.27f;  // us
+// Who works on a tile, and how many CTAs share one: what takes least by a model of the
+// times (us; fitted to 1226 shapes of 2 to 8000 rows, 32 to 16384 columns and k, each in
+// all ways: what it takes is on average 1 % slower than the best of them, at worst 50 %). A
+// block along k takes its issue or a stage's latency by the stages that are on their way, all
+// of them what L2 and memory give; then come the results, by what a tile's CTAs have to join
+// and by how many values of a row are stored at once. A partition's SMs may not hold a cluster.
+struct Times {
+    float block;      // along k
+    float end, rows;  // what follows, in any tile and in one of 128 rows besides
+};
+constexpr Times kSharedTimes{0.17f, 0.7f, 1.5f}, kMidTimes{0.17f, 1.5f, 2.1f}, kWideTimes{0.29f, 2.0f, 3.7f};
+constexpr float kAloneBlock = 0.19f, kPairBlock = 0.31f, kPairEnd = 2.1f;
+constexpr float kAloneTurn = 0.25f, kPairTurn = 0.5f;  // from a tile to the next
+constexpr float kWideGated = 1.0f;                     // after a gated wide tile
+constexpr float kLatency = 0.89f;                      // from asking for a stage to its product
+constexpr float kMemory = 8.2e6f, kL2 = 20e6f;         // bytes
+struct Results {
+    float narrow, pair;  // of a tile of 128 x 64 by one CTA, of a pair's
+};
+constexpr Results kPlainResults{0.6f, 2.3f}, kFours{1.1f, 2.6f}, kTwos{1.3f, 3.6f}, kOnes{2.5f, 5.2f};
 struct Plan {
     Mode mode;
     int split;
@@ -826,28 +837,45 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, bool plain, int a_rows, in
     const cudaError_t err = resident_clusters(device, &clusters);
     if (err != cudaSuccess) return err;
     const int half = gated ? 2 : 1;
-    const int64_t pairs = up(a.m, Shape<kPair>::kTileRows) * up(a.n, Shape<kPair>::kCols / half);
-    auto tiles = [&](int cols) { return up(a.m, kRows) * up(a.n, cols / half); };
-    const int64_t narrow = tiles(64), mid = tiles(128), wide = tiles(256);
     const float a_bytes = a.a_by_k ? (a.m > 64 ? 2 : 1) * kGroupBytes : a_rows * kRowBytes;
-    auto block = [&](int cols, int stages) {
-        return fmaxf((a_bytes + cols * kRowBytes) / (cols > 64 ? kWideInBytes : kInBytes), kLatency / stages);
-    };
-    // a tile takes its products' time, or its results' where those take longer
-    const float alone_tile = fmaxf(a.k_blocks * block(64, Shape<kAlone>::kStages), plain ? 0.6f : 2.0f);
-    const float pair_tile = fmaxf(a.k_blocks * kPairBlock, plain ? 2.2f : 2.8f);
-    float best = up(narrow, num_sms) * (alone_tile + 0.3f) + 0.2f;
+    auto part = [&](int rows) { return a.m < rows ? static_cast<float>(a.m) / rows : 1.0f; };
+    const Results results = plain ? kPlainResults : a.n % 4 == 0 ? kFours : a.n % 2 == 0 ? kTwos : kOnes;
+    const float memory = 2.0f * a.k * (a.m + static_cast<float>(half) * a.n) / kMemory;
+    auto tiles = [&](int cols) { return up(a.m, kRows) * up(a.n, cols / half); };
+    auto from_l2 = [&](int64_t blocks, int cols) { return blocks * (a_bytes + cols * kRowBytes) / kL2; };
+    float best;
     auto take = [&](float time, Plan p) {
         if (time < best) best = time, *plan = p;
     };
-    if (clusters.pairs > 0)
-        take(up(pairs, clusters.pairs) * pair_tile + 3.0f, {kPair, 1, clusters.pairs});
+    // CTAs that take several tiles: a tile takes its products' time, or its results' where
+    // those take longer
+    auto persistent = [&](int64_t turns, float block, float result, float turn) {
+        return turns * fmaxf(a.k_blocks * block, turns > 1 ? result : 0.0f) + (turns - 1) * turn;
+    };
+    const int64_t narrow = tiles(64);
+    best = fmaxf(fmaxf(persistent(up(narrow, num_sms), kAloneBlock, results.narrow, kAloneTurn), memory),
+                 from_l2(narrow * a.k_blocks, 64)) +
+           results.narrow * part(kRows);
+    if (clusters.pairs > 0) {
+        constexpr int kRowsEach = Shape<kPair>::kTileRows;
+        const int64_t n = up(a.m, kRowsEach) * up(a.n, Shape<kPair>::kCols / half);
+        take(fmaxf(persistent(up(n, clusters.pairs), kPairBlock, results.pair, kPairTurn), memory) + kPairEnd +
+                 results.pair * part(kRowsEach),
+             {kPair, 1, clusters.pairs});
+    }
+    auto shared = [&](Mode mode, int split, int cols, int stages, int resident, const Times& t) {
+        const int64_t n = tiles(cols), blocks = up(a.k_blocks, split);
+        if (n > resident) return;
+        const float in = fmaxf(blocks * fmaxf(t.block, kLatency / stages), memory);
+        const float out = t.end + part(kRows) * (t.rows + results.narrow * cols / (128 * split)) +
+                          (mode == kSharedWide && gated ? kWideGated : 0.0f);
+        take(fmaxf(in, from_l2(n * split * blocks, cols)) + out, {mode, split, 0});
+    };
     for (int n = 2; n <= kMaxSplit && n <= a.k_blocks; n *= 2) {
-        const int64_t blocks = up(a.k_blocks, n);
-        if (narrow <= clusters.n[n]) take(blocks * block(64, Shape<kShared>::kStages) + 1.6f, {kShared, n, 0});
+        shared(kShared, n, 64, Shape<kShared>::kStages, clusters.n[n], kSharedTimes);
         if (n > 8) continue;
-        if (mid <= clusters.mid[n]) take(blocks * block(128, Shape<kSharedMid>::kStages) + 3.3f, {kSharedMid, n, 0});
-        if (wide <= clusters.wide[n]) take(blocks * block(256, Shape<kSharedWide>::kStages) + 5.0f, {kSharedWide, n, 0});
+        shared(kSharedMid, n, 128, Shape<kSharedMid>::kStages, clusters.mid[n], kMidTimes);
+        shared(kSharedWide, n, 256, Shape<kSharedWide>::kStages, clusters.wide[n], kWideTimes);
     }
     return cudaSuccess;
 }
