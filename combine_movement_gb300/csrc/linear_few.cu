@@ -143,14 +143,15 @@ cudaError_t launch_rows(const LinearArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// One row always; up to four where the weights are at most 32 MB: the more rows the
-// fewer loads its registers leave in flight (2 x 7168 x 2048: 7.6 us here, 9.4 in tiles; 4
-// rows 9.8 and 9.5; of 58.7 MB, gated, 1 row 10.5 and 13.5, 2 rows 15.4 and 13.7, 4 rows
-// 15.8 and 13.7; 4 x 1000 x 1000 4.4 and 4.7).
+// One row always; two where the weights are at most 32 MB, up to four where they are at most
+// 16: the more rows the fewer loads its registers leave in flight (7168 x 2048: 2 rows 7.6 us
+// here, 8.8 in tiles, 4 rows 9.7 and 8.9; gated 2 x 2048 x 2048: 2 rows 5.8 and 7.0, 4 rows 6.7
+// and 7.0; of 58.7 MB, gated, 1 row 10.5 and 13.3, 2 rows 15.4 and 13.3; 4 x 1000 x 1000
+// 4.3 and 4.4).
 bool linear_few_takes(const LinearArgs& a) {
     if (a.a_by_k || a.b_by_k || a.m > 4) return false;
     const int64_t rows = a.act == EP_ACT_SWIGLU ? 2 * a.n : a.n;
-    return a.m == 1 || rows * a.k <= (int64_t{16} << 20);
+    return a.m == 1 || rows * a.k <= (int64_t{a.m == 2 ? 16 : 8} << 20);
 }
 
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t stream) {
