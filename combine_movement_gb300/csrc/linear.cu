@@ -33,10 +33,16 @@
 // where the library's product takes 139). 16384 x 2048 x 7168 with a residual 262 us
 // cool, 317 for seconds (the library's 345). Few columns: 16384 x 7168 x 256 48 us, 0.8
 // of the copy rate: 64 pairs leave 24 SMs idle, and each reads all of b. Small ones:
-// 128 x 7168 x 256 7.1 us: 0.2 us from launch to the first copy, 1.1 until it lands, 0.2 a
-// block along k (24 KB at an SM's 120 GB/s), 2 to join 16 parts, 0.7 to end together.
+// 128 x 7168 x 256 7.0 us: 0.2 us from launch to the first copy, 1.1 until it lands, 0.17 a
+// block along k (what the copying and the product's warp take to wait for it and issue it, the
+// same without the copies or without the products), 2 to join 16 parts, 0.7 to end
+// together. A few rows: 8 x 7168 x 2048 8.7 us, of which 2.7 are a kernel with one block;
+// 8 x 7168 x 4096 14 (4.3 TB/s).
 // Measured and not kept: k begun at another block in each tile (nothing), rows brought
-// into L2 ahead (2-30 % slower).
+// into L2 ahead (2-30 % slower), more stages where few rows of a leave room (0.4 us slower on
+// small calls, their number not being a constant), 128 values to a stage (0-10 % slower), a look
+// at the next barrier before a block's issue (0.1-0.3 us slower on small calls), a warp's loop
+// gone through by one lane alone (0.33 us a block).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -13,7 +13,9 @@ no entry maps to are zero in both directions (``ep_clear_unused_rows``).
 ``linear`` is a product in bf16 with bias, activation and residual, for those
 logits and for an expert that every token goes through: with h =
 linear(x, gate_up, activation="swiglu"), linear(h, down, residual=y) adds it to
-combine's y. Both are differentiable.
+combine's y. Both are differentiable. (Like any backward pass, theirs is captured into a
+CUDA graph only while no graph of autograd from outside the capture holds the same leaves:
+torch would join the two's streams.)
 
 ``python -m combine_movement_gb300.moe`` builds a layer with random weights,
 runs a batch through it and through a router and a shared expert, compares some
