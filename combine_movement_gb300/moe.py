@@ -26,6 +26,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import ep
 
@@ -55,6 +56,13 @@ def quantize_weights(w: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
 def _check_shape(t: torch.Tensor, shape: Tuple[int, ...], what: str) -> None:
     if t.shape != shape:
         raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+# Whether one of them carries a forward-mode tangent. No call here has a forward-mode
+# derivative: a function of autograd that gets such a tensor says so, the library's
+# calls would drop the tangent without a word. (no_grad does not switch it off.)
+def _has_tangent(*tensors: Optional[torch.Tensor]) -> bool:
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def forward_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
@@ -306,7 +314,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     _check_shape(x, (x.shape[0], w.shape[-1]), "x")
     x, w, residual = _dense(x), _dense(w), None if residual is None else _dense(residual)
     # (a function's forward is not told that no gradient is recorded, and would keep z)
-    if not torch.is_grad_enabled():
+    if not torch.is_grad_enabled() and not _has_tangent(x, w, bias, residual):
         return ep.linear(x, w, bias, activation, residual, out_dtype)
     return _Linear.apply(x, w, bias, residual, activation, out_dtype)
 
