@@ -75,9 +75,11 @@ def forward_fp8(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
     w_gate_up e4m3 [E, 2I, H] and w_down e4m3 [E, H, I] with their scales, as
     ``quantize_weights`` makes them. Everything is enqueued on the current
     stream; nothing waits for the device. There is no gradient: where an input
-    asks for one, a backward pass through the result raises."""
+    asks for one, a backward pass through the result raises, and a tangent of
+    forward mode is refused."""
     args = (x, topk_idx, topk_w, w_gate_up, s_gate_up, w_down, s_down, status)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args):
+    recorded = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args)
+    if recorded or _has_tangent(*args):
         return _ForwardFp8.apply(*args)
     return _forward_fp8(*args)
 

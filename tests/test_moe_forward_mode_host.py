@@ -39,3 +39,21 @@ def test_linear_without_a_tangent(mods, recorded):
         assert mods[1].linear(**linear_arguments()).shape == (4, 8)
     with torch.inference_mode():
         assert mods[1].linear(**linear_arguments()).shape == (4, 8)
+
+
+# -- the 8-bit layer ------------------------------------------------------------
+
+FORWARD_FP8 = ["x", "topk_w", "w_gate_up", "s_gate_up", "w_down", "s_down"]
+
+
+@pytest.mark.parametrize("recorded", [True, False])
+@pytest.mark.parametrize("name", ["x", "topk_w", "s_gate_up", "s_down"])
+def test_forward_fp8_refuses_a_tangent(mods, monkeypatch, recorded, name):
+    monkeypatch.setattr(mods[1], "_forward_fp8", lambda x, *rest: torch.zeros_like(x))
+    args = {n: torch.ones(4, 4) for n in FORWARD_FP8}
+    args["topk_idx"] = torch.zeros(4, 4, dtype=torch.int64)
+    with torch.set_grad_enabled(recorded), forward_ad.dual_level():
+        assert mods[1].forward_fp8(**args).shape == (4, 4)
+        args[name] = forward_ad.make_dual(args[name], torch.ones(4, 4))
+        with pytest.raises(NotImplementedError):
+            mods[1].forward_fp8(**args)
