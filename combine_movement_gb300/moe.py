@@ -133,7 +133,11 @@ def _combine_grad(dy, expert_out, slot, topk_w, num_recv, need_w):
 # The movement's differentiable functions. Each one's backward is made of the
 # others (dispatch is linear, combine bilinear), so that every derivative has
 # a graph of its own where one is asked for (create_graph, which leaves the
-# gradient mode on in a backward).
+# gradient mode on in a backward), and refuses a forward-mode tangent.
+
+
+def _as_function(*grads: Optional[torch.Tensor]) -> bool:
+    return torch.is_grad_enabled() or _has_tangent(*grads)
 
 
 class _Dispatch(torch.autograd.Function):
@@ -145,7 +149,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     def backward(ctx, d_recv):
         (slot,) = ctx.saved_tensors
-        grad = _DispatchGrad.apply if torch.is_grad_enabled() else ep.dispatch_grad
+        grad = _DispatchGrad.apply if _as_function(d_recv) else ep.dispatch_grad
         return grad(d_recv.contiguous(), slot), None, None
 
 
@@ -176,7 +180,7 @@ class _Combine(torch.autograd.Function):
     def backward(ctx, dy):
         expert_out, slot, topk_w = ctx.saved_tensors
         need_rows, _, need_w = ctx.needs_input_grad
-        grad = _CombineGrad.apply if torch.is_grad_enabled() else _combine_grad
+        grad = _CombineGrad.apply if _as_function(dy) else _combine_grad
         d_rows, d_w = grad(dy.contiguous(), expert_out, slot, topk_w,
                            ctx.num_recv if need_rows else None, need_w)
         return d_rows, None, d_w
@@ -228,6 +232,11 @@ def combine(expert_out: torch.Tensor, slot: torch.Tensor, topk_w: torch.Tensor) 
     return _Combine.apply(expert_out.contiguous(), slot, topk_w)
 
 
+def _refuse_tangent(name: str, t: torch.Tensor) -> None:
+    if _has_tangent(t):
+        raise NotImplementedError(f"{name}: no forward-mode derivative of its backward pass")
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, bias, kind):
@@ -240,6 +249,7 @@ class _Route(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, _, d_w):
+        _refuse_tangent("route", d_w)
         logits, idx = ctx.saved_tensors
         return ep.route_grad(d_w.contiguous(), logits, idx, **ctx.kind), None, None, None
 
@@ -283,6 +293,8 @@ class _Linear(torch.autograd.Function):
     def backward(ctx, dy):
         x, w, z = ctx.saved_tensors
         need_x, need_w, need_bias, need_residual = ctx.needs_input_grad[:4]
+        if need_x or need_w or need_bias:
+            _refuse_tangent("linear", dy)
         dy, wide, act = _dense(dy), ctx.wide, ctx.activation
         M = dy.shape[0]
         dx = d_w = d_bias = None
