@@ -20,9 +20,12 @@
 //  - clusters of 2 to 16 CTAs on 128 x 64, 128 or 256 that share a tile's blocks along k
 //    and add their sums through shared memory: few tiles, long k.
 // A tensor core's fp32 sum loses more at each of its steps than rounding to nearest does,
-// and to one side: 7168 products in a row are off by 8e-6 of their norm, 9e-7 in parts of
-// 1024 that are added in fp32 registers, as all of fp32 results are (bf16 results
-// lose 2e-3 at their end).
+// and to one side: 7168 products in a row are off by 8e-6 of their norm where their signs
+// are mixed and by 4e-5 where they are alike, 131072 by 7e-4, a million by 6.5e-3. In parts of
+// 1024 that are added in fp32 registers 7168 are off by 9e-7. So are all fp32
+// results made, and bf16 results of more than 8192 products in a row (a step loses at
+// most a unit of 2^-23 of the sum so far and takes at least 8 products: of 8192 at most 2^-14,
+// a 64th of what a bf16 result loses at its end). Parts take 1-3 % longer.
 //
 // Results. Sums that are the result but for rounding leave by the copy engine, 32 x 32
 // at a time. The others are turned around in shared memory, from a row to a lane to
@@ -76,9 +79,10 @@ constexpr uint32_t kTurnBytes = 32 * kChunk * 4;
 constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 16;
 constexpr int kRowGroup = 8;                 // row tiles that share a column tile's turn
-// Blocks along k after which fp32 results take a tile's sums out of tensor memory.
+// Blocks along k after which a tile's sums leave tensor memory, for fp32 results; and
+// how many bf16 results may be of before they do the same.
 constexpr int kExactBlocks = 16;
-constexpr int kLongBlocks = 1 << 17;
+constexpr int kLongBlocks = 128;
 
 template <Mode kMode>
 struct Shape {
@@ -918,7 +922,6 @@ cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_
     maps.plain = plain && (pair || plan.mode == kAlone);
     if (!ok || (maps.plain && !encode_out(&maps.out, a))) return cudaErrorInvalidValue;
     const int64_t tiles = a.row_tiles * a.col_tiles;
-    // (of a very long k, too, so that no warp waits for its sums for a second)
     const int64_t sum_blocks = up(a.k_blocks, a.split);
     const bool exact = sum_blocks > kExactBlocks && (a.out_f32 || sum_blocks > kLongBlocks);
     if (pair) {

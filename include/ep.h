@@ -486,7 +486,9 @@ typedef enum {
  * silu's error is that of ep_expert_gate_up_fp8; gelu is off by (16 + z^2) 2^-23
  * of its value, where P(z) is below 2^-125 by all of it. fp32 results are added
  * up from sums of at most 1024 products of the tensor cores (fewer rows: of the
- * fp32 units). y and z may not overlap x, w or each other. */
+ * fp32 units), bf16 results from one sum of at most 8192 or from such parts: before
+ * their rounding they are off by at most 2^-14 of their products' magnitudes and
+ * the parts' additions. y and z may not overlap x, w or each other. */
 EP_API ep_status_t ep_linear(const uint16_t* x, int64_t M, int64_t K, const uint16_t* w, int64_t N,
                              const float* bias, int activation, const void* residual, int y_type,
                              void* y, uint16_t* z, int32_t* status, void* stream);
