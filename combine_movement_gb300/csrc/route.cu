@@ -195,6 +195,13 @@ __device__ __forceinline__ float approx_exp(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.44269504088896341f));
     return r;
 }
+// e^(l - m), l <= m. The difference's rounding, half a unit of 2^-24 of up to 128, would be
+// up to 32 units of 2^-23 of the result: what l and m have lost in it is put back.
+__device__ __forceinline__ float exp_difference(float l, float m) {
+    const float d = l - m, l_in = d + m, m_in = l_in - d;
+    const float e = expf(d), lost = (l - l_in) - (m - m_in);
+    return e > 0.0f ? fmaf(e, lost, e) : e;  // (of infinities nothing is put back)
+}
 __device__ __forceinline__ float sigmoid(float l) { return approx_reciprocal(1.0f + expf(-l)); }
 
 // The groups to keep, as a bit mask, from each lane's group (`key` of its worth,
@@ -677,15 +684,16 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 7 : 2) route_kernel(cons
         if (!a.softmax && __any_sync(kFullMask, lk >= 0.0f)) {
             w = mine >= 0 ? sigmoid(lk) : 0.0f;
         } else if (const float high = warp_max(lk); a.softmax) {
-            w = mine >= 0 ? expf(lk - high) : 0.0f;
+            w = mine >= 0 ? exp_difference(lk, high) : 0.0f;
         } else {
             // by e^high, so that scores below fp32's range keep their ratios
-            w = mine >= 0 ? __fdiv_rn(expf(lk - high) * (1.0f + expf(high)), 1.0f + expf(lk)) : 0.0f;
+            w = mine >= 0 ? __fdiv_rn(exp_difference(lk, high) * (1.0f + expf(high)), 1.0f + expf(lk))
+                          : 0.0f;
         }
         const float sum = warp_sum(w);
         w = mine >= 0 ? w * approx_reciprocal(sum) : 0.0f;
     } else if (mine >= 0) {
-        w = a.softmax ? expf(lk - m) * score.r : sigmoid(lk);
+        w = a.softmax ? exp_difference(lk, m) * score.r : sigmoid(lk);
     }
     if (lane < a.K) {
         a.topk_idx[t * a.K + lane] = mine;
@@ -758,11 +766,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
         float p = 0.0f;
         if (live) {
             if (a.softmax)
-                p = expf(lk - high);
+                p = exp_difference(lk, high);
             else if (high >= 0.0f)
                 p = sigmoid(lk);
             else
-                p = __fdiv_rn(expf(lk - high) * (1.0f + expf(high)), 1.0f + expf(lk));
+                p = __fdiv_rn(exp_difference(lk, high) * (1.0f + expf(high)), 1.0f + expf(lk));
         }
         const float sum = warp_sum(p);
         p = live ? __fdiv_rn(p, sum) : 0.0f;
@@ -770,7 +778,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
         d = live ? p * (g - dot) : 0.0f;
         if (live && !a.softmax) d *= sigmoid(-lk);
     } else if (a.softmax) {
-        dot = warp_sum(live ? g * __fdiv_rn(expf(lk - m), z) : 0.0f);
+        dot = warp_sum(live ? g * __fdiv_rn(exp_difference(lk, m), z) : 0.0f);
         d = live ? g : 0.0f;
     } else if (live) {
         d = g * sigmoid(lk) * sigmoid(-lk);

@@ -431,7 +431,7 @@ typedef enum { EP_GROUP_MAX = 0, EP_GROUP_TOP2 = 1 } ep_group_score_t;
  * the movement skips. NaN counts as larger than every number, so that it is
  * chosen and shows in the weights. Weights are off by at most 16 units of 2^-23
  * of their value, softmax weights that are not renormalised by E / 32 more;
- * those below 2^-125 may be 0.
+ * those that are below 2^-125 before scale may be 0.
  * 1 <= K <= min(32, E), groups divides E, groups <= EP_MAX_GROUPS, and the
  * groups that stay hold at least K experts. (groups 1: no groups.) The
  * SM budget does not apply, as for the layout. T == 0 is valid. */
