@@ -239,10 +239,10 @@ def _refuse_tangent(name: str, t: torch.Tensor) -> None:
 
 class _Route(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, k, bias, kind):
+    def forward(ctx, logits, k, bias, kind, status):
         idx, w = ep.route(logits, k, bias, **kind)
         ctx.save_for_backward(logits, idx)
-        ctx.kind = {n: kind[n] for n in ("score", "renormalize", "scale")}
+        ctx.kind = dict({n: kind[n] for n in ("score", "renormalize", "scale")}, status=status)
         ctx.mark_non_differentiable(idx)
         return idx, w
 
@@ -251,19 +251,21 @@ class _Route(torch.autograd.Function):
     def backward(ctx, _, d_w):
         _refuse_tangent("route", d_w)
         logits, idx = ctx.saved_tensors
-        return ep.route_grad(d_w.contiguous(), logits, idx, **ctx.kind), None, None, None
+        return ep.route_grad(d_w.contiguous(), logits, idx, **ctx.kind), None, None, None, None
 
 
 def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
           score: str = "softmax", groups: int = 1, topk_groups: int = 1, group_score: str = "max",
-          renormalize: bool = True, scale: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
+          renormalize: bool = True, scale: float = 1.0, status: Optional[torch.Tensor] = None
+          ) -> Tuple[torch.Tensor, torch.Tensor]:
     """``ep.route`` -- (topk_idx int64 [T, k], topk_w fp32 [T, k]), what layout and
     combine take -- with a gradient of topk_w for the logits, once (a second
-    derivative raises). The bias, for the choice alone, has none."""
+    derivative raises). The bias, for the choice alone, has none. ``status`` is the
+    backward pass's."""
     _check_shape(logits, (logits.shape[0], logits.shape[-1]), "logits")
     return _Route.apply(logits.contiguous(), k, None if bias is None else bias.detach(),
                         dict(score=score, groups=groups, topk_groups=topk_groups,
-                             group_score=group_score, renormalize=renormalize, scale=scale))
+                             group_score=group_score, renormalize=renormalize, scale=scale), status)
 
 
 # Rows as the products read them: a copy where they do not lie one after the other or
@@ -276,16 +278,16 @@ def _dense(t: torch.Tensor) -> torch.Tensor:
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, bias, residual, activation, out_dtype):
+    def forward(ctx, x, w, bias, residual, activation, out_dtype, status):
         M, wide = x.shape[0], w.shape[0]
         y = x.new_empty((M, wide // 2 if activation == "swiglu" else wide), dtype=out_dtype)
         need = any(ctx.needs_input_grad[:3])
         z = x.new_empty((M, wide)) if need and activation != "none" else None
-        ep.ep_linear(x, w, y, bias, activation, residual, z)
+        ep.ep_linear(x, w, y, bias, activation, residual, z, status)
         # the rows are for the weight's gradient alone, the weight for the rows'
         ctx.save_for_backward(x if ctx.needs_input_grad[1] else None,
                               w if ctx.needs_input_grad[0] else None, z)
-        ctx.activation, ctx.wide = activation, wide
+        ctx.activation, ctx.wide, ctx.status = activation, wide, status
         return y
 
     @staticmethod
@@ -309,28 +311,30 @@ class _Linear(torch.autograd.Function):
             ep.ep_linear_act_grad(dy, z, None if dz is dy else dz, d_bias, act)
         if need_x:
             dx = dz.new_empty((M, w.shape[1]))
-            ep.ep_linear_grad_input(dz, w, dx)
+            ep.ep_linear_grad_input(dz, w, dx, ctx.status)
         if need_w:
             d_w = dz.new_empty((wide, x.shape[1]))
-            ep.ep_linear_grad_weight(dz, x, d_w)
-        return dx, d_w, d_bias, dy if need_residual else None, None, None
+            ep.ep_linear_grad_weight(dz, x, d_w, status=ctx.status)
+        return dx, d_w, d_bias, dy if need_residual else None, None, None, None
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
            activation: str = "none", residual: Optional[torch.Tensor] = None,
-           out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+           out_dtype: torch.dtype = torch.bfloat16, status: Optional[torch.Tensor] = None
+           ) -> torch.Tensor:
     """act(x w^T + bias) + residual with gradients for all four, once (a second
     derivative raises): x bf16 [M, K], w bf16 [N, K] (swiglu: [2N, K], the gate
     half first), bias fp32, residual [M, N] of out_dtype, which is bf16 or, for a
     router's logits, fp32. Keeps x w^T + bias in bf16 where an activation's
     gradient wants it, and rounds what comes back through the activation to bf16
-    before the gradients' products."""
+    before the gradients' products. ``status`` (int32 [1]) takes what a product reports,
+    here and in the backward pass: after a wait that gave up results are not whole."""
     _check_shape(x, (x.shape[0], w.shape[-1]), "x")
     x, w, residual = _dense(x), _dense(w), None if residual is None else _dense(residual)
     # (a function's forward is not told that no gradient is recorded, and would keep z)
     if not torch.is_grad_enabled() and not _has_tangent(x, w, bias, residual):
-        return ep.linear(x, w, bias, activation, residual, out_dtype)
-    return _Linear.apply(x, w, bias, residual, activation, out_dtype)
+        return ep.linear(x, w, bias, activation, residual, out_dtype, status)
+    return _Linear.apply(x, w, bias, residual, activation, out_dtype, status)
 
 
 def _main() -> None:
