@@ -1,5 +1,5 @@
 """Build libep_gb300.so in-tree for sm_103a (nvcc, one -gencode, TUs compiled
-in parallel, no cmake), and the binding's extension _calls.so (the C compiler).
+in parallel, no cmake), and the binding's extension _calls (the C compiler).
 ``python -m combine_movement_gb300.build`` or ``build()``; skipped when they are
 newer than every source."""
 from __future__ import annotations
@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_objs")
 LIB_PATH = os.path.join(PKG, "libep_gb300.so")
-CALLS_PATH = os.path.join(PKG, "_calls.so")
+# (with the interpreter's tag: another interpreter neither finds it fresh nor loads it)
+CALLS_PATH = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 CALLS_SOURCE = os.path.join(CSRC, "calls.c")
 
 GENCODE = "arch=compute_103a,code=sm_103a"
@@ -53,6 +54,9 @@ def is_stale() -> bool:
 
 def build_calls(force: bool = False) -> str:
     """Build the binding's extension; returns its path."""
+    untagged = os.path.join(os.path.dirname(CALLS_PATH), "_calls.so")
+    if untagged != CALLS_PATH and os.path.exists(untagged):  # any interpreter would load it
+        os.remove(untagged)
     inputs = [CALLS_SOURCE, os.path.join(INCLUDE, "ep.h")]
     if not force and os.path.exists(CALLS_PATH) and all(
             os.path.getmtime(p) <= os.path.getmtime(CALLS_PATH) for p in inputs):

@@ -5,8 +5,8 @@
  * through here, of which the kernel's launch is 1.9.
  *
  * Each function returns the library's status, or -1 where an argument is not what
- * the call takes; ep.py then looks at them one by one and says which. Plain C and
- * the limited set of calls that every CPython 3 has; no header of torch or CUDA.
+ * the call takes; ep.py then looks at them one by one and says which. Plain C, for the
+ * interpreter (3.9 or later) whose headers it was built with; no header of torch or CUDA.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

@@ -159,7 +159,7 @@ lib = _load()
 try:
     from . import _calls
 except ImportError as e:
-    raise ImportError(f"the binding's extension _calls.so is not built ({e}); run "
+    raise ImportError(f"the binding's extension _calls is not built ({e}); run "
                       "`python -m combine_movement_gb300.build`") from e
 
 
