@@ -5,6 +5,8 @@ newer than every source."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import fcntl
 import glob
 import os
 import shutil
@@ -52,15 +54,41 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _inputs())
 
 
+@contextlib.contextmanager
+def _alone(folder: str):
+    """One build at a time in `folder` (ranks and test workers each ask for one); the
+    ones that waited find it done."""
+    os.makedirs(folder, exist_ok=True)
+    with open(os.path.join(folder, ".lock"), "w") as f:
+        fcntl.flock(f, fcntl.LOCK_EX)
+        yield
+
+
+def _untagged() -> str:
+    """The extension without a tag, which any interpreter would load."""
+    return os.path.join(os.path.dirname(CALLS_PATH), "_calls.so")
+
+
+def calls_stale() -> bool:
+    if os.path.exists(_untagged()) or not os.path.exists(CALLS_PATH):
+        return True
+    t = os.path.getmtime(CALLS_PATH)
+    return any(os.path.getmtime(p) > t for p in (CALLS_SOURCE, os.path.join(INCLUDE, "ep.h")))
+
+
 def build_calls(force: bool = False) -> str:
     """Build the binding's extension; returns its path."""
-    untagged = os.path.join(os.path.dirname(CALLS_PATH), "_calls.so")
-    if untagged != CALLS_PATH and os.path.exists(untagged):  # any interpreter would load it
-        os.remove(untagged)
-    inputs = [CALLS_SOURCE, os.path.join(INCLUDE, "ep.h")]
-    if not force and os.path.exists(CALLS_PATH) and all(
-            os.path.getmtime(p) <= os.path.getmtime(CALLS_PATH) for p in inputs):
-        return CALLS_PATH
+    if force or calls_stale():
+        with _alone(OBJ_DIR):
+            _build_calls(force)
+    return CALLS_PATH
+
+
+def _build_calls(force: bool) -> None:
+    if not force and not calls_stale():
+        return
+    if os.path.exists(_untagged()):
+        os.remove(_untagged())
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
         raise RuntimeError("no C compiler found for the binding's extension")
@@ -71,7 +99,6 @@ def build_calls(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"{cc} failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS_PATH)
-    return CALLS_PATH
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
@@ -82,12 +109,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     default library)."""
     lib_path = os.path.join(out_dir, "libep_gb300.so") if out_dir else LIB_PATH
     obj_dir = os.path.join(out_dir, "_objs") if out_dir else OBJ_DIR
-    if out_dir is None:
-        build_calls(force)
-    if out_dir is None and not force and not is_stale():
-        return LIB_PATH
+    if out_dir is None and not force and not calls_stale() and not is_stale():
+        return LIB_PATH  # (nothing is written where nothing is to be built)
+    with _alone(obj_dir):
+        if out_dir is None:
+            _build_calls(force)
+            if not force and not is_stale():
+                return LIB_PATH
+        return _build_library(lib_path, obj_dir, verbose, extra_flags)
+
+
+def _build_library(lib_path: str, obj_dir: str, verbose: bool, extra_flags: list[str] | None) -> str:
     nvcc = _nvcc()
-    os.makedirs(obj_dir, exist_ok=True)
     flags = NVCC_FLAGS + list(extra_flags or [])
 
     def compile_one(src: str) -> str:

@@ -1,7 +1,11 @@
 """The build of the binding's extension."""
+import concurrent.futures
 import os
 import sys
 import sysconfig
+import threading
+import time
+import types
 
 import pytest
 
@@ -31,3 +35,55 @@ def test_another_interpreters_is_not_taken_for_it(build, tmp_path):
     assert (tmp_path / "_calls.cpython-30-any.so").exists()
     before = os.path.getmtime(path)
     assert build.build_calls() == path and os.path.getmtime(path) == before
+
+
+@pytest.fixture
+def slow_compilers(build, monkeypatch, tmp_path):
+    """Compilers that write their output in two parts; gives the outputs that two of
+    them wrote at once."""
+    busy, lock, clashes = set(), threading.Lock(), []
+
+    def run(cmd, **kind):
+        out = cmd[cmd.index("-o") + 1]
+        with lock:
+            if out in busy:
+                clashes.append(out)
+            busy.add(out)
+        with open(out, "wb") as f:
+            f.write(b"one ")
+            f.flush()
+            time.sleep(0.05)
+            f.write(b"two")
+        with lock:
+            busy.discard(out)
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(build, "OBJ_DIR", str(tmp_path / "_objs"))
+    monkeypatch.setattr(build, "LIB_PATH", str(tmp_path / "libep_gb300.so"))
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return clashes
+
+
+@pytest.mark.parametrize("call", ["build_calls", "build"])
+def test_two_builds_at_once(build, slow_compilers, call):
+    with concurrent.futures.ThreadPoolExecutor(3) as ex:
+        paths = list(ex.map(lambda _: getattr(build, call)(), range(3)))
+    assert not slow_compilers
+    for path in paths:
+        with open(path, "rb") as f:
+            assert f.read() == b"one two"
+
+
+def test_of_those_that_waited_only_one_compiles(build, slow_compilers, monkeypatch):
+    runs, inner = [], build.subprocess.run
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kind: (runs.append(cmd), inner(cmd, **kind))[1])
+    with concurrent.futures.ThreadPoolExecutor(4) as ex:
+        list(ex.map(lambda _: build.build(), range(4)))
+    assert len(runs) == len(build.sources()) + 2  # each source, the library, the extension
+
+
+def test_nothing_is_written_where_nothing_is_to_be_built(build, slow_compilers, monkeypatch):
+    build.build()
+    monkeypatch.setattr(build, "OBJ_DIR", os.path.join(build.OBJ_DIR, "not", "there"))
+    monkeypatch.setattr(build.os, "makedirs", lambda *a, **k: pytest.fail("a folder was made"))
+    assert build.build() == build.LIB_PATH and build.build_calls() == build.CALLS_PATH
