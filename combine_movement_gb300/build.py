@@ -1,7 +1,7 @@
 """Build libep_gb300.so in-tree for sm_103a (nvcc, one -gencode, TUs compiled
 in parallel, no cmake), and the binding's extension _calls (the C compiler).
 ``python -m combine_movement_gb300.build`` or ``build()``; skipped when they are
-newer than every source."""
+newer than every source. Without Python.h the library is built alone."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -13,6 +13,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -77,7 +78,7 @@ def calls_stale() -> bool:
 
 
 def build_calls(force: bool = False) -> str:
-    """Build the binding's extension; returns its path."""
+    """Build the binding's extension, where Python.h is there; returns its path."""
     if force or calls_stale():
         with _alone(OBJ_DIR):
             _build_calls(force)
@@ -90,11 +91,15 @@ def _build_calls(force: bool) -> None:
     if os.path.exists(_untagged()):
         os.remove(_untagged())
     cc = shutil.which("gcc") or shutil.which("cc")
-    if cc is None:
-        raise RuntimeError("no C compiler found for the binding's extension")
+    headers = sysconfig.get_paths()["include"]
+    missing = "a C compiler" if cc is None else "Python.h"
+    if cc is None or not os.path.exists(os.path.join(headers, "Python.h")):
+        warnings.warn(f"the binding's extension is not built: {missing} was not found (the router's "
+                      "and the dense products' calls need it, the others do not)")
+        return
     tmp = CALLS_PATH + ".tmp"
     cmd = [cc, "-O2", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall", "-I", INCLUDE,
-           "-I", sysconfig.get_paths()["include"], CALLS_SOURCE, "-o", tmp]
+           "-I", headers, CALLS_SOURCE, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cc} failed on {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
@@ -112,14 +117,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if out_dir is None and not force and not calls_stale() and not is_stale():
         return LIB_PATH  # (nothing is written where nothing is to be built)
     with _alone(obj_dir):
+        if out_dir is not None or force or is_stale():
+            _build_library(lib_path, obj_dir, verbose, extra_flags)
         if out_dir is None:
             _build_calls(force)
-            if not force and not is_stale():
-                return LIB_PATH
-        return _build_library(lib_path, obj_dir, verbose, extra_flags)
+    return lib_path
 
 
-def _build_library(lib_path: str, obj_dir: str, verbose: bool, extra_flags: list[str] | None) -> str:
+def _build_library(lib_path: str, obj_dir: str, verbose: bool,
+                   extra_flags: list[str] | None) -> None:
     nvcc = _nvcc()
     flags = NVCC_FLAGS + list(extra_flags or [])
 
@@ -142,7 +148,6 @@ def _build_library(lib_path: str, obj_dir: str, verbose: bool, extra_flags: list
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path)
-    return lib_path
 
 
 if __name__ == "__main__":

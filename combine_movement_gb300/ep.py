@@ -156,11 +156,26 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+
+class _NoCalls:
+    """In the extension's place where it is not built: its calls say so, the others need
+    it not."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name: str):
+        if name.startswith("__"):
+            raise AttributeError(name)
+        raise ImportError("the router's and the dense products' calls need the binding's extension "
+                          f"_calls, which is not built ({self._why}); run "
+                          "`python -m combine_movement_gb300.build`")
+
+
 try:
     from . import _calls
 except ImportError as e:
-    raise ImportError(f"the binding's extension _calls is not built ({e}); run "
-                      "`python -m combine_movement_gb300.build`") from e
+    _calls = _NoCalls(e)
 
 
 # --------------------------------------------------------------------------
@@ -190,10 +205,11 @@ def _current_stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-_calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-    lib.ep_route, lib.ep_route_grad, lib.ep_linear, lib.ep_linear_act_grad,
-    lib.ep_linear_grad_input, lib.ep_linear_grad_weight)),
-    _BF16, _F32, _I32, torch.int64, _cur_device, _raw_stream or _current_stream)
+if not isinstance(_calls, _NoCalls):
+    _calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.ep_route, lib.ep_route_grad, lib.ep_linear, lib.ep_linear_act_grad,
+        lib.ep_linear_grad_input, lib.ep_linear_grad_weight)),
+        _BF16, _F32, _I32, torch.int64, _cur_device, _raw_stream or _current_stream)
 
 
 def _stream(stream) -> Optional[int]:

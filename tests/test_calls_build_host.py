@@ -1,6 +1,7 @@
 """The build of the binding's extension."""
 import concurrent.futures
 import os
+import subprocess
 import sys
 import sysconfig
 import threading
@@ -87,3 +88,45 @@ def test_nothing_is_written_where_nothing_is_to_be_built(build, slow_compilers, 
     monkeypatch.setattr(build, "OBJ_DIR", os.path.join(build.OBJ_DIR, "not", "there"))
     monkeypatch.setattr(build.os, "makedirs", lambda *a, **k: pytest.fail("a folder was made"))
     assert build.build() == build.LIB_PATH and build.build_calls() == build.CALLS_PATH
+
+
+def test_without_the_headers_the_library_is_built(build, slow_compilers, monkeypatch, tmp_path):
+    monkeypatch.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path / "none")})
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert build.build() == build.LIB_PATH
+    assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.CALLS_PATH)
+
+
+def test_a_broken_extension_does_not_keep_the_library_back(build, slow_compilers, monkeypatch):
+    inner = build.subprocess.run
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kind: inner(cmd, **kind) if "nvcc" in cmd[0]
+                        else types.SimpleNamespace(returncode=1, stdout="", stderr="broken"))
+    with pytest.raises(RuntimeError, match="broken"):
+        build.build()
+    assert os.path.exists(build.LIB_PATH)
+
+
+WITHOUT = """
+import sys
+sys.modules["combine_movement_gb300._calls"] = None  # an import of it fails
+import torch
+from combine_movement_gb300 import ep, moe
+z = torch.zeros
+try:
+    ep.ep_dispatch(z(4, 8, dtype=torch.bfloat16), z(4, 2, dtype=torch.int32), z(8, 8, dtype=torch.bfloat16))
+except ValueError as e:  # what it says of tensors that are not on a GPU
+    print("movement:", e)
+for call in (lambda: ep.ep_linear(z(4, 8), z(8, 8), z(4, 8)), lambda: moe.route(z(4, 8), 2)):
+    try:
+        call()
+    except ImportError as e:
+        print("needs it:", e)
+"""
+
+
+def test_without_the_extension_the_movement_is_there(build):
+    r = subprocess.run([sys.executable, "-c", WITHOUT], capture_output=True, text=True, cwd=build.ROOT)
+    lines = r.stdout.splitlines()
+    assert r.returncode == 0, r.stderr
+    assert lines[0].startswith("movement:") and "CUDA" in lines[0]
+    assert [l.startswith("needs it:") and "not built" in l for l in lines[1:]] == [True, True]
