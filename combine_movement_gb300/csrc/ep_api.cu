@@ -936,6 +936,34 @@ ep_status_t ep_linear_grad_weight(const uint16_t* dz, int64_t pitch, int64_t M, 
     return run_linear(a, s);
 }
 
+int ep_linear_tiles(int product, int64_t M, int64_t N, int64_t K, int activation, int out_type,
+                    int epilogue, void* stream, int* shared_by, int* in_parts) {
+    if (product < 0 || product > 2 || activation < EP_ACT_NONE || activation > EP_ACT_SWIGLU ||
+        (product != 0 && activation != EP_ACT_NONE) || (out_type != EP_BF16 && out_type != EP_F32) ||
+        (product == 1 && (out_type != EP_BF16 || epilogue)))
+        return -1;
+    ep::LinearArgs a{};
+    a.a_by_k = product == 2;
+    a.b_by_k = product != 0;
+    a.m = product == 2 ? N : M;
+    a.n = product == 0 ? N : K;
+    a.k = product == 0 ? K : product == 1 ? N : M;
+    a.act = activation;
+    a.out_f32 = out_type == EP_F32;
+    if (M < 1 || check_linear(M, N, K, activation == EP_ACT_SWIGLU, nullptr) != EP_OK ||
+        !linear_fits(a.m, a.n))
+        return -1;
+    int sm_count = 0, smem_optin = 0;
+    if (!device_limits(&sm_count, &smem_optin)) return -1;
+    const int part = ep::partition_sms(static_cast<cudaStream_t>(stream));
+    ep::LinearTiles tiles{};
+    if (ep::linear_tiles(a, epilogue != 0, part > 0 ? part : sm_count, part > 0, &tiles) != cudaSuccess)
+        return -1;
+    if (shared_by != nullptr) *shared_by = tiles.shared_by;
+    if (in_parts != nullptr) *in_parts = tiles.in_parts ? 1 : 0;
+    return tiles.kind;
+}
+
 ep_status_t ep_get_status(const int32_t* status, void* stream) {
     if (status == nullptr) return EP_ERR_INVALID;
     int32_t v = 0;

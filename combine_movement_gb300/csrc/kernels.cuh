@@ -339,6 +339,15 @@ struct LinearArgs {
 // `partition`: num_sms are those of an SM partition, not the device's.
 cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_t stream);
 
+// How launch_linear makes its tiles (ep_linear_tiles). `epilogue`: with a bias, a residual or
+// z, which `a` need not have here.
+struct LinearTiles {
+    ep_tiles_t kind;
+    int shared_by;
+    bool in_parts;
+};
+cudaError_t linear_tiles(LinearArgs a, bool epilogue, int num_sms, bool partition, LinearTiles* tiles);
+
 // The same for a token or a few, where that is faster (linear_few.cu).
 bool linear_few_takes(const LinearArgs& a);
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t stream);

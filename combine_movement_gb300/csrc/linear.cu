@@ -890,40 +890,75 @@ cudaError_t plan_for(const LinearArgs& a, bool gated, bool plain, int a_rows, in
     return cudaSuccess;
 }
 
+// A call's way: the rule's plan, and what it went by. `epilogue`: more than rounding the sums.
+struct Way {
+    Plan plan;
+    int a_rows;   // of a's box along k: no more than there are
+    bool plain;   // out is the rounded sums, in aligned rows
+    bool exact;   // sums leave tensor memory in parts
+};
+cudaError_t way_of(LinearArgs& a, bool epilogue, int num_sms, bool partition, Way* way) {
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    a.k_blocks = static_cast<int>(up(a.k, kTileK));
+    way->a_rows = 16;
+    while (way->a_rows < kRows && way->a_rows < a.m) way->a_rows *= 2;
+    way->plain = !epilogue && a.act == EP_ACT_NONE && a.n % (a.out_f32 ? 4 : 8) == 0;
+    if (err == cudaSuccess)
+        err = plan_for(a, a.act == EP_ACT_SWIGLU, way->plain, way->a_rows, device, num_sms, partition,
+                       &way->plan);
+    if (err != cudaSuccess) return err;
+    a.split = way->plan.split;
+    const int64_t sum_blocks = up(a.k_blocks, a.split);
+    way->exact = sum_blocks > kExactBlocks && (a.out_f32 || sum_blocks > kLongBlocks);
+    return cudaSuccess;
+}
+
 }  // namespace
+
+cudaError_t linear_tiles(LinearArgs a, bool epilogue, int num_sms, bool partition, LinearTiles* tiles) {
+    *tiles = {EP_TILES_FEW_ROWS, 1, false};
+    if (linear_few_takes(a)) return cudaSuccess;
+    Way way{};
+    const cudaError_t err = way_of(a, epilogue, num_sms, partition, &way);
+    if (err != cudaSuccess) return err;
+    switch (way.plan.mode) {
+        case kAlone: tiles->kind = EP_TILES_ALONE; break;
+        case kShared: tiles->kind = EP_TILES_SHARED_64; break;
+        case kSharedMid: tiles->kind = EP_TILES_SHARED_128; break;
+        case kSharedWide: tiles->kind = EP_TILES_SHARED_256; break;
+        case kPair: tiles->kind = EP_TILES_PAIR; break;
+    }
+    tiles->shared_by = way.plan.mode == kPair ? 2 : way.plan.split;
+    tiles->in_parts = way.exact;
+    return cudaSuccess;
+}
 
 cudaError_t launch_linear(LinearArgs a, int num_sms, bool partition, cudaStream_t stream) {
     const bool gated = a.act == EP_ACT_SWIGLU;
     const int half = gated ? 2 : 1;
     if (linear_few_takes(a)) return launch_linear_few(a, stream);
-    int device = 0;
-    cudaError_t err = cudaGetDevice(&device);
-    a.k_blocks = static_cast<int>(up(a.k, kTileK));
-    int a_rows = 16;  // of a's box along k: no more than there are
-    while (a_rows < kRows && a_rows < a.m) a_rows *= 2;
-    const bool plain = a.act == EP_ACT_NONE && a.bias == nullptr && a.z == nullptr &&
-                       a.residual == nullptr && a.n % (a.out_f32 ? 4 : 8) == 0;
-    Plan plan{};
-    if (err == cudaSuccess) err = plan_for(a, gated, plain, a_rows, device, num_sms, partition, &plan);
+    Way way{};
+    const bool epilogue = a.bias != nullptr || a.z != nullptr || a.residual != nullptr;
+    const cudaError_t err = way_of(a, epilogue, num_sms, partition, &way);
     if (err != cudaSuccess) return err;
+    const Plan& plan = way.plan;
+    const bool exact = way.exact;
     const bool pair = plan.mode == kPair;
     const int cols = pair || plan.mode == kSharedWide ? 256 : plan.mode == kSharedMid ? 128 : 64;
-    a.split = plan.split;
     a.row_tiles = up(a.m, pair ? Shape<kPair>::kTileRows : kRows);
     a.col_tiles = up(a.n, cols / half);
     Maps maps;
-    maps.a_rows = pair ? kRows : a_rows;
+    maps.a_rows = pair ? kRows : way.a_rows;
     const int64_t b_rows = half * a.n;
     const bool ok =
         (a.a_by_k ? encode_map(&maps.a, a.a, a.k, a.m, a.a_pitch, kTileK)
                   : encode_map(&maps.a, a.a, a.m, a.k, a.a_pitch, maps.a_rows)) &&
         (a.b_by_k ? encode_map(&maps.b, a.b, a.k, b_rows, a.b_pitch, kTileK)
                   : encode_map(&maps.b, a.b, b_rows, a.k, a.b_pitch, gated || pair ? cols / 2 : cols));
-    maps.plain = plain && (pair || plan.mode == kAlone);
+    maps.plain = way.plain && (pair || plan.mode == kAlone);
     if (!ok || (maps.plain && !encode_out(&maps.out, a))) return cudaErrorInvalidValue;
     const int64_t tiles = a.row_tiles * a.col_tiles;
-    const int64_t sum_blocks = up(a.k_blocks, a.split);
-    const bool exact = sum_blocks > kExactBlocks && (a.out_f32 || sum_blocks > kLongBlocks);
     if (pair) {
         const int grid = 2 * static_cast<int>(tiles < plan.clusters ? tiles : plan.clusters);
         if (exact)

@@ -37,6 +37,8 @@ EP_MAX_GROUPS = 32
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"max": 0, "top2": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
+PRODUCTS = {"linear": 0, "grad_input": 1, "grad_weight": 2}
+TILES = ("few rows", "alone", "shared 64", "shared 128", "shared 256", "pair")
 
 # Values that share one scale in the 8-bit operands.
 FP8_BLOCK = 128
@@ -142,6 +144,9 @@ def _load() -> ctypes.CDLL:
     lib.ep_linear_grad_input.restype = i32
     lib.ep_linear_grad_weight.argtypes = [p, i64, i64, i64, p, i64, i32, p, i32, p, p]
     lib.ep_linear_grad_weight.restype = i32
+    pi32 = ctypes.POINTER(i32)
+    lib.ep_linear_tiles.argtypes = [i32, i64, i64, i64, i32, i32, i32, p, pi32, pi32]
+    lib.ep_linear_tiles.restype = i32
     lib.ep_sm_partition.argtypes = [i32, ctypes.POINTER(p), ctypes.POINTER(p),
                                     ctypes.POINTER(i32), ctypes.POINTER(i32)]
     lib.ep_sm_partition.restype = i32
@@ -532,9 +537,9 @@ def _on_gpu(name: str, *tensors: Optional[torch.Tensor]) -> None:
                              f"got one on {t.device}")
 
 
-def _choice(table: dict, key: str, what: str) -> int:
+def _choice(table: dict, key, what: str) -> int:
     if key not in table:
-        raise ValueError(f"{what}: expected one of {', '.join(table)}, got {key!r}")
+        raise ValueError(f"{what}: expected one of {', '.join(map(str, table))}, got {key!r}")
     return table[key]
 
 
@@ -700,6 +705,20 @@ def ep_linear_grad_weight(dz: torch.Tensor, x: torch.Tensor, d_w: torch.Tensor,
             _ptr(status, _I32, "status")
             _on_gpu("ep_linear_grad_weight", dz, x, d_w, status)
         _made(code, "ep_linear_grad_weight", look)
+
+
+def ep_linear_tiles(product: str, M: int, N: int, K: int, activation: str = "none",
+                    out_dtype: torch.dtype = _BF16, epilogue: bool = False, stream=None
+                    ) -> Optional[Tuple[str, int, bool]]:
+    """(one of TILES, CTAs that share a tile, whether sums are added up from parts), or
+    None for sizes that the call does not take."""
+    shared_by, in_parts = ctypes.c_int(), ctypes.c_int()
+    kind = lib.ep_linear_tiles(_choice(PRODUCTS, product, "product"), M, N, K,
+                               _choice(ACTIVATIONS, activation, "activation"),
+                               _choice({_BF16: 0, _F32: 1}, out_dtype, "out_dtype"), epilogue,
+                               _stream(stream),
+                               ctypes.byref(shared_by), ctypes.byref(in_parts))
+    return None if kind < 0 else (TILES[kind], shared_by.value, bool(in_parts.value))
 
 
 def ep_sm_partition(num_sms: int) -> Tuple[int, Optional[int], int, int]:

@@ -523,6 +523,27 @@ EP_API ep_status_t ep_linear_grad_weight(const uint16_t* dz, int64_t pitch, int6
                                          const uint16_t* x, int64_t K, int d_w_type, void* d_w,
                                          int accumulate, int32_t* status, void* stream);
 
+/* How a dense product's tiles are made, by what its sizes leave to do. */
+typedef enum {
+    EP_TILES_FEW_ROWS = 0,    /* without tiles: the weights are streamed */
+    EP_TILES_ALONE = 1,       /* 128 x 64, a CTA each */
+    EP_TILES_SHARED_64 = 2,   /* 128 x 64, CTAs of a cluster share its sums' length */
+    EP_TILES_SHARED_128 = 3,
+    EP_TILES_SHARED_256 = 4,
+    EP_TILES_PAIR = 5         /* 256 x 256, a pair of CTAs each */
+} ep_tiles_t;
+
+/* What a call of these sizes would do on `stream` of the current device:
+ * ep_tiles_t, or -1 for invalid sizes or when the device cannot be queried.
+ *   product    0 ep_linear, 1 ep_linear_grad_input, 2 ep_linear_grad_weight;
+ *              M, N, K as there, activation EP_ACT_NONE for 1 and 2
+ *   out_type   of y or d_w
+ *   epilogue   1 with a bias, a residual (accumulate) or z
+ *   shared_by  out, nullable: CTAs that share a tile
+ *   in_parts   out, nullable: 1 where sums are added up from parts of 1024 */
+EP_API int ep_linear_tiles(int product, int64_t M, int64_t N, int64_t K, int activation, int out_type,
+                           int epilogue, void* stream, int* shared_by, int* in_parts);
+
 /* Layout without a workspace argument, for callers that cannot allocate
  * device memory. The pages have no counterpart; this is a library addition.
  * Such callers include a serving engine that reserved nearly all of HBM up
