@@ -426,7 +426,8 @@ __device__ __noinline__ uint32_t settle_groups(const RouteArgs& a, int64_t row, 
             __reduce_min_sync(kFullMask, worth != 0 && stays ? key_of(value - error) : 0xFFFFFFFFu);
         const uint32_t high =
             __reduce_max_sync(kFullMask, worth != 0 && !stays ? key_of(value + error) : 0u);
-        if (high < low) return kept;
+        // (a sum past fp32's range, infinite here, has another value in 64 bits)
+        if (high < low && low < key_of(kInf)) return kept;
     }
     Exact x{};
     if (a.softmax && scores) x = exact_softmax(a, row);
