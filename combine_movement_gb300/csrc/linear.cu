@@ -32,10 +32,11 @@
 // rows across lanes, for bias, activation and residual and for stores along rows.
 //
 // What bounds it. Large products: the tensor cores at 0.87 of their cycles (4096 x 4096 x
-// 7168: 119-130 us cool, 1.9-2.0 PFLOP/s; for seconds the board's power limit, 145 us,
-// where the library's product takes 139). 16384 x 2048 x 7168 with a residual 262 us
-// cool, 317 for seconds (the library's 345). Few columns: 16384 x 7168 x 256 48 us, 0.8
-// of the copy rate: 64 pairs leave 24 SMs idle, and each reads all of b. Small ones:
+// 7168: 119-138 us for a few launches after a rest, 1.75-2.0 PFLOP/s by card; for seconds the
+// board's power limit, 146 us, where the library's product takes 139-142). 16384 x 2048 x 7168
+// with a residual 261 us after a rest, 300-317 for seconds (the library's 345). Few columns:
+// 16384 x 7168 x 256 47-51 us, 0.8 of the copy rate: 64 pairs leave 24 SMs idle, and each
+// reads all of b. Small ones:
 // 128 x 7168 x 256 7.0 us: 0.2 us from launch to the first copy, 1.1 until it lands, 0.17 a
 // block along k (what the copying and the product's warp take to wait for it and issue it, the
 // same without the copies or without the products), 2 to join 16 parts, 0.7 to end
@@ -815,8 +816,11 @@ cudaError_t resident_clusters(int device, ResidentClusters* clusters) {
 int64_t up(int64_t v, int64_t by) { return (v + by - 1) / by; }
 
 // Who works on a tile, and how many CTAs share one: what takes least by a model of the
-// times (us; fitted to 1226 shapes of 2 to 8000 rows, 32 to 16384 columns and k, each in
-// all ways: what it takes is on average 1 % slower than the best of them, at worst 50 %). A
+// times (us; fitted to 1231 shapes of 2 to 8000 rows, 32 to 16384 columns and k, each in
+// all ways: what it takes is on average 1 % slower than the best of them, for 36 of them by
+// more than 10 %, for 13 by more than 20 and at worst by 53. Those 13 have sums of 32 to 704
+// products, most of them for more results than a round of CTAs makes: 3007 x 192 x 2112, 293 x
+// 64 x 13120. There CTAs alone and pairs take nearly the same by the model, and not in fact). A
 // block along k takes its issue or a stage's latency by the stages that are on their way, all
 // of them what L2 and memory give; then come the results, by what a tile's CTAs have to join
 // and by how many values of a row are stored at once. A partition's SMs may not hold a cluster.

@@ -27,14 +27,14 @@
 // first ones and one ballot, and ties fall to the lower index by themselves.
 //
 // Bound by instructions, half of them on the integer pipe, which takes two a cycle:
-// 16384 tokens, 256 experts, bias, 8 groups, top-8 take 20-24 us (930 instructions a
+// 16384 tokens, 256 experts, bias, 8 groups, top-8 take 20-27 us (950 instructions a
 // token; without groups 19, without a bias 15; the bytes would be 2.7). One token: 3.2 us,
 // the chain of its rounds. Measured on the way: arguments passed by address to a function
 // that is not inlined make a copy of them in local memory, unless they are constant
 // (__grid_constant__); groups' worths from integers with lost bits alone sent a token of
 // a thousand into 64 bits, 14 us until the last was done; a persistent grid with the next
 // token on its way was 20 % slower (registers); 2, 4 and 8 warps to a CTA are alike. The
-// gradient of 16383 tokens, 128 experts, dense: 7.8-8.8 us (430 instructions a token).
+// gradient of 16383 tokens, 128 experts, dense: 8.0-8.8 us (440 instructions a token).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -326,8 +326,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     derivative raises): x bf16 [M, K], w bf16 [N, K] (swiglu: [2N, K], the gate
     half first), bias fp32, residual [M, N] of out_dtype, which is bf16 or, for a
     router's logits, fp32. Keeps x w^T + bias in bf16 where an activation's
-    gradient wants it, and rounds what comes back through the activation to bf16
-    before the gradients' products. ``status`` (int32 [1]) takes what a product reports,
+    gradient wants it, and rounds what comes back, through the activation or in fp32,
+    to bf16 before the gradients' products. ``status`` (int32 [1]) takes what a product reports,
     here and in the backward pass: after a wait that gave up results are not whole."""
     _check_shape(x, (x.shape[0], w.shape[-1]), "x")
     x, w, residual = _dense(x), _dense(w), None if residual is None else _dense(residual)

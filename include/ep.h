@@ -500,7 +500,8 @@ EP_API ep_status_t ep_linear(const uint16_t* x, int64_t M, int64_t K, const uint
  *   dy      bf16 or fp32 [M][N]
  *   z       bf16 [M][N] ([M][2N]) from ep_linear; not read for EP_ACT_NONE
  *   dz      bf16 [M][pitch], nullable; pitch a multiple of 8 of at least w's
- *           rows (values past those are left as they are)
+ *           rows (values past those are left as they are). Its rounding, also of an
+ *           fp32 dy, is in both products' results as much as their own
  *   d_bias  fp32 [N] ([2N]), nullable; M == 0 is valid and gives zeros
  * N at most 2097120. Without an activation and a d_bias there is nothing to do
  * for a bf16 dy whose rows start on 16 bytes: it is dz. */
