@@ -62,6 +62,8 @@ def _check_shape(t: torch.Tensor, shape: Tuple[int, ...], what: str) -> None:
 # derivative: a function of autograd that gets such a tensor says so, the library's
 # calls would drop the tangent without a word. (no_grad does not switch it off.)
 def _has_tangent(*tensors: Optional[torch.Tensor]) -> bool:
+    if getattr(forward_ad, "_current_level", 0) < 0:  # (to ask a tensor takes 0.5 us)
+        return False
     return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 

@@ -15,6 +15,7 @@ import pytest
 def build(monkeypatch, tmp_path):
     """The build module, its extension in a folder of its own."""
     from combine_movement_gb300 import build
+    build.build()
     monkeypatch.setattr(build, "CALLS_PATH", str(tmp_path / os.path.basename(build.CALLS_PATH)))
     return build
 
