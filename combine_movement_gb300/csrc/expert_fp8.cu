@@ -650,16 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A byte matrix [rows][width], read in boxes of box_rows x 128 bytes laid out
 // with the 128-byte swizzle.
 bool encode_map(CUtensorMap* map, const uint8_t* p, int64_t rows, int64_t width, int box_rows) {
-    const EncodeFn fn = encode_fn();
-    if (fn == nullptr) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width)};
-    const cuuint32_t box[2] = {kTileK, static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t step[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, box, step,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rows, width, width, box_rows, kTileK,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // The warpgroups' registers come out of those of the launch; with fewer the

@@ -713,31 +713,17 @@ __global__ void __launch_bounds__(kThreads, kMode == kShared ? 2 : 1)
 // the 128-byte swizzle.
 bool encode_map(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t width, int64_t pitch,
                 int box_rows) {
-    const EncodeFn fn = encode_fn();
-    if (fn == nullptr) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t step[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p), dims, strides, box,
-              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, rows, width, pitch * 2, box_rows, 64,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // out, written in boxes of 32 x 32.
 bool encode_out(CUtensorMap* map, const LinearArgs& a) {
-    const EncodeFn fn = encode_fn();
-    if (fn == nullptr) return false;
-    const cuuint64_t size = a.out_f32 ? 4 : 2;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.n), static_cast<cuuint64_t>(a.m)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.n) * size};
-    const cuuint32_t box[2] = {kChunk, 32};
-    const cuuint32_t step[2] = {1, 1};
-    return fn(map, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-              a.out, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              a.out_f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_2d(map,
+                     a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     a.out, a.m, a.n, a.n * (a.out_f32 ? 4 : 2), 32, kChunk,
+                     a.out_f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 // What a kernel's launches need beyond the defaults: its shared memory, and for narrow

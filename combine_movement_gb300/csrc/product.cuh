@@ -138,4 +138,27 @@ inline EncodeFn encode_fn() {
     return fn;
 }
 
+// A map of a matrix of rows of `width` values, `stride` bytes from one to the next, in boxes of
+// box_rows x box_width; what lies out of range reads 0 and is not written.
+inline bool encode_2d(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t rows,
+                      int64_t width, int64_t stride, int box_rows, int box_width,
+                      CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_width), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t step[2] = {1, 1};
+    auto encode = [&] {
+        return fn(map, type, 2, const_cast<void*>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (encode()) return true;
+    // The driver wants a current context, and a thread that has made no call of the runtime
+    // yet has none: it gets its device's.
+    int device = 0;
+    return cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess && encode();
+}
+
 }  // namespace ep
